@@ -523,6 +523,7 @@ const char *kvq_strerror(int code) {
     case KVQ_EALIGN: return "device buffer not 16-byte aligned";
     case KVQ_ECUDA: return "CUDA error";
     case KVQ_ETIMEOUT: return "device-side wait timed out";
+    case KVQ_EPAGE: return "token outside the block table or its pages";
   }
   return "unknown error";
 }

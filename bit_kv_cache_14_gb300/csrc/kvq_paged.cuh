@@ -1,0 +1,80 @@
+// Paged cache (include/kvq.h, "Paged cache"): what its translation units share.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+constexpr int kAtom = 16;         // tokens stored together inside a page
+constexpr int kPagedGroup = 32;   // channels that share a scale and a zero point
+constexpr int kMaxSeqs = 4096;
+constexpr float kPagedLimit = 32768.0f;  // stored magnitudes saturate here
+
+// One paged call, resolved on the host and copied by value into every kernel.
+struct Paged {
+  int H, Hq, rg, d, bits, page, bf16;
+  int rb;             // bytes of one row of codes
+  int atom_bytes;
+  int64_t head_bytes;  // one head of one page
+  int64_t page_bytes;
+  int64_t n_pages;
+  uint8_t *pages;
+  int32_t *status;
+  const int32_t *table, *lens, *cu;
+  int64_t width;      // block table entries per sequence
+  int B;
+  int max_tokens;
+  int64_t T;          // rows of the packed arrays
+};
+
+int resolve_paged(const kvq_paged_config *cfg, Paged *p);
+
+// Calls on the packed rows (cudaError_t of the launch).
+cudaError_t launch_paged_write(const Paged &p, const void *k, int64_t ks, const void *v,
+                               int64_t vs, cudaStream_t st);
+cudaError_t launch_paged_read(const Paged &p, void *k, void *v, cudaStream_t st);
+cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, void *out,
+                                   float scale, void *ws, cudaStream_t st, int *launches);
+size_t paged_workspace_bytes();
+
+namespace {
+
+// ---- device helpers ------------------------------------------------------
+// The first error of a call stays in the status word until it is read.
+__device__ __forceinline__ void paged_error(const Paged &p, int code) {
+  atomicCAS(p.status, 0, code);
+}
+
+// Rows [0, min(cu[B], T)) are real.  Sequence of row t, or -1 for padding
+// (also for a cu_tokens array that does not increase around t).
+__device__ __forceinline__ int seq_of_row(const Paged &p, int64_t t) {
+  int lo = 0, hi = p.B;  // the largest b with cu[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return (t >= p.cu[lo] && t < p.cu[lo + 1]) ? lo : -1;
+}
+
+// Position of row t of sequence b (negative: the row precedes its sequence).
+__device__ __forceinline__ int64_t row_position(const Paged &p, int b, int64_t t) {
+  return (int64_t)p.lens[b] - p.cu[b + 1] + t;
+}
+
+// Address of the atom that holds position `pos` (>= 0) of sequence b and head
+// 0, or null with KVQ_EPAGE recorded.
+__device__ __forceinline__ uint8_t *atom_of(const Paged &p, int b, int64_t pos) {
+  const int64_t i = pos / p.page;
+  int64_t id = -1;
+  if (i < p.width) id = p.table[b * p.width + i];
+  if (id < 0 || id >= p.n_pages) {
+    paged_error(p, KVQ_EPAGE);
+    return nullptr;
+  }
+  return p.pages + id * p.page_bytes + (int64_t)((int)(pos % p.page) / kAtom) * p.atom_bytes;
+}
+
+}  // namespace
+}  // namespace kvq

@@ -24,6 +24,7 @@ KVQ_ECAPACITY = -3
 KVQ_EALIGN = -4
 KVQ_ECUDA = -5
 KVQ_ETIMEOUT = -6
+KVQ_EPAGE = -7
 KIVI = 0
 INNERQ = 1
 INNERQ_KNORM = 2  # InnerQ with the one-shot per-channel key normalization
@@ -39,6 +40,8 @@ EXPORTS = (
     "kvq_last_launch_count", "kvq_strerror", "kvq_debug_stall_waits",
     "kvq_decode_attention_noalloc", "kvq_append_decode", "kvq_decode_attention_rope",
     "kvq_decode_kernel_name", "kvq_quantize_prefill_ragged", "kvq_rope_kernel_name",
+    "kvq_paged_cache_bytes", "kvq_paged_workspace_bytes", "kvq_paged_write", "kvq_paged_read",
+    "kvq_paged_attention", "kvq_paged_status",
 )
 
 
@@ -62,6 +65,22 @@ class Cache(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("n_quant", "n_resid", "n_sink", "ring_head")] + [
         ("dev_status", ctypes.c_void_p), ("seq_prompt", ctypes.c_void_p),
         ("n_appended", ctypes.c_int64)]
+
+
+class PagedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_q_heads", "n_kv_heads", "head_dim", "bits", "page_size", "dtype")] + [
+        ("n_pages", ctypes.c_int64)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+class _PagedBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("block_table", "seq_lens", "cu_tokens")] + [
+        (n, ctypes.c_int64) for n in ("table_width", "n_tokens")] + [
+        (n, ctypes.c_int32) for n in ("n_seqs", "max_tokens")]
 
 
 class KVQError(RuntimeError):
@@ -101,6 +120,15 @@ def lib():
             L.kvq_decode_kernel_name.argtypes = [C, I64, ctypes.c_char_p, ctypes.c_size_t]
             L.kvq_rope_kernel_name.argtypes = [C, I64, ctypes.c_char_p, ctypes.c_size_t]
             L.kvq_get_device_status.argtypes = [CA, P]
+            PC, PV, PB = (ctypes.POINTER(t) for t in (PagedConfig, _PagedCache, _PagedBatch))
+            PS = ctypes.POINTER(ctypes.c_size_t)
+            L.kvq_paged_cache_bytes.argtypes = [PC, PS, PS]
+            L.kvq_paged_workspace_bytes.argtypes = [PC, PS]
+            L.kvq_paged_write.argtypes = [PC, PV, PB, P, I64, P, I64, P]
+            L.kvq_paged_read.argtypes = [PC, PV, PB, P, P, P]
+            L.kvq_paged_attention.argtypes = [PC, PV, PB, P, I64, P, ctypes.c_float, P,
+                                              ctypes.c_size_t, P]
+            L.kvq_paged_status.argtypes = [PV, P]
             L.kvq_last_launch_count.argtypes = []
             L.kvq_debug_stall_waits.argtypes = [ctypes.c_int64]
             L.kvq_debug_stall_waits.restype = None
@@ -434,6 +462,174 @@ class QuantizedKVCache:
 
     def last_launch_count(self) -> int:
         return lib().kvq_last_launch_count()
+
+
+# ---- paged cache ------------------------------------------------------------
+F16 = 0
+BF16 = 1
+_PAGED_DTYPES = {torch.float16: F16, torch.bfloat16: BF16}
+
+
+def make_paged_config(n_q_heads, n_kv_heads, head_dim, bits, page_size, n_pages,
+                      dtype=torch.float16) -> PagedConfig:
+    """dtype: torch.float16 or torch.bfloat16, the type of keys, values,
+    queries and outputs."""
+    if dtype not in _PAGED_DTYPES:
+        raise TypeError("expected torch.float16 or torch.bfloat16, got %s" % dtype)
+    return PagedConfig(n_q_heads, n_kv_heads, head_dim, bits, page_size, _PAGED_DTYPES[dtype],
+                       n_pages)
+
+
+def paged_cache_bytes(cfg: PagedConfig):
+    """(bytes of the page pool, bytes of one page)."""
+    pool, page = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().kvq_paged_cache_bytes(ctypes.byref(cfg), ctypes.byref(pool), ctypes.byref(page)),
+           "kvq_paged_cache_bytes")
+    return pool.value, page.value
+
+
+class PagedBatch:
+    """The sequences of one call (kvq_paged_batch): int32 device tensors
+    block_table [n_seqs][width], seq_lens [n_seqs] and cu_tokens [n_seqs + 1].
+    Their contents may change between calls (and between replays of a captured
+    graph); n_tokens (rows of the packed tensors) and max_tokens (an upper
+    bound of the rows of any one sequence; default n_tokens) are fixed here."""
+
+    def __init__(self, block_table, seq_lens, cu_tokens, n_tokens: int,
+                 max_tokens: int | None = None):
+        for t, dims in ((block_table, 2), (seq_lens, 1), (cu_tokens, 1)):
+            if t.dtype != torch.int32:
+                raise TypeError("expected an int32 tensor, got %s" % t.dtype)
+            if t.dim() != dims or not t.is_contiguous():
+                raise ValueError("expected a contiguous %d-d tensor, got shape %s"
+                                 % (dims, tuple(t.shape)))
+        n = seq_lens.shape[0]
+        if block_table.shape[0] != n or cu_tokens.shape[0] != n + 1:
+            raise ValueError("block_table %s, seq_lens %s and cu_tokens %s do not match"
+                             % tuple(tuple(t.shape) for t in (block_table, seq_lens, cu_tokens)))
+        if not block_table.device == seq_lens.device == cu_tokens.device:
+            raise ValueError("block_table, seq_lens and cu_tokens are on different devices")
+        self.block_table, self.seq_lens, self.cu_tokens = block_table, seq_lens, cu_tokens
+        self.n_tokens = int(n_tokens)
+        self.max_tokens = int(n_tokens if max_tokens is None else max_tokens)
+        self.device = block_table.device
+        self.view = _PagedBatch(block_table.data_ptr(), seq_lens.data_ptr(),
+                                cu_tokens.data_ptr(), block_table.shape[1], self.n_tokens, n,
+                                self.max_tokens)
+        self._ref = ctypes.byref(self.view)
+
+
+class PagedKVCache:
+    """A page pool (torch-allocated unless ``pages`` is given) with the status
+    word and the attention scratch, and the paged calls on it.  Calls run on
+    ``stream`` (default: the current stream of the cache's device); calls that
+    can run at the same time need caches (or scratch) of their own."""
+
+    def __init__(self, cfg: PagedConfig, device="cuda", pages: torch.Tensor | None = None):
+        self.cfg = cfg
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.dtype = torch.bfloat16 if cfg.dtype == BF16 else torch.float16
+        pool, self.page_bytes = paged_cache_bytes(cfg)
+        if pages is None:
+            pages = torch.empty(pool, dtype=torch.uint8, device=self.device)
+        if pages.dtype != torch.uint8 or not pages.is_contiguous() or pages.numel() != pool:
+            raise ValueError("pages: a contiguous uint8 tensor of %d bytes is needed" % pool)
+        self._on_device(pages)
+        self.pages = pages
+        self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self.view = _PagedCache(pages.data_ptr(), self.status.data_ptr())
+        n = ctypes.c_size_t()
+        _check(lib().kvq_paged_workspace_bytes(ctypes.byref(cfg), ctypes.byref(n)),
+               "kvq_paged_workspace_bytes")
+        self.ws_bytes = n.value
+        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._refs = ctypes.byref(cfg), ctypes.byref(self.view)
+        self._scale = 1.0 / math.sqrt(cfg.head_dim)
+
+    def _on_device(self, t) -> None:
+        if t.device != self.device:
+            raise ValueError("expected a tensor on %s, got one on %s" % (self.device, t.device))
+
+    def _rows(self, t: torch.Tensor, batch: PagedBatch, heads: int) -> int:
+        """Checks a packed tensor [n_tokens][heads][head_dim] (rows of any
+        stride, each contiguous); returns the stride between rows."""
+        if t.dtype != self.dtype:
+            raise TypeError("expected a %s tensor, got %s" % (self.dtype, t.dtype))
+        if t.shape != (batch.n_tokens, heads, self.cfg.head_dim):
+            raise ValueError("expected shape %s, got %s"
+                             % ((batch.n_tokens, heads, self.cfg.head_dim), tuple(t.shape)))
+        self._on_device(t)
+        s0, s1, s2 = t.stride()
+        if t.shape[0] <= 1:
+            s0 = max(s0, heads * self.cfg.head_dim)
+        if s2 != 1 or (heads > 1 and s1 != self.cfg.head_dim):
+            raise ValueError("each row must be contiguous (got strides %s)" % (t.stride(),))
+        return s0
+
+    def _call(self, fn, batch: PagedBatch, stream, *args) -> None:
+        if batch.device != self.device:
+            raise ValueError("the batch is on %s, the cache on %s" % (batch.device, self.device))
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if torch.cuda.current_device() == self.device.index:
+            code = fn(*self._refs, batch._ref, *args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                code = fn(*self._refs, batch._ref, *args, stream.cuda_stream)
+        if code != KVQ_OK:
+            raise KVQError(code, fn.__name__)
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, batch: PagedBatch, stream=None) -> None:
+        """Quantizes k, v [n_tokens][n_kv_heads][head_dim] (the batch's newest
+        tokens) into their pages."""
+        H = self.cfg.n_kv_heads
+        ks, vs = self._rows(k, batch, H), self._rows(v, batch, H)
+        self._call(lib().kvq_paged_write, batch, stream, k.data_ptr(), ks, v.data_ptr(), vs)
+
+    def read(self, batch: PagedBatch, out=None, stream=None):
+        """Reads the batch's tokens back: (k, v), each contiguous
+        [n_tokens][n_kv_heads][head_dim] (``out``: the two tensors to fill)."""
+        H, d = self.cfg.n_kv_heads, self.cfg.head_dim
+        if out is None:
+            k, v = (torch.empty((batch.n_tokens, H, d), dtype=self.dtype, device=self.device)
+                    for _ in range(2))
+        else:
+            k, v = out
+            for t in out:
+                self._rows(t, batch, H)
+                _ptr(t)
+        self._call(lib().kvq_paged_read, batch, stream, k.data_ptr(), v.data_ptr())
+        return k, v
+
+    def attend(self, q: torch.Tensor, batch: PagedBatch, out: torch.Tensor | None = None,
+               scale: float | None = None, stream=None) -> torch.Tensor:
+        """Causal attention of q [n_tokens][n_q_heads][head_dim], the rows of
+        the batch's newest tokens, over everything their sequences hold (write
+        those tokens first).  Returns [n_tokens][n_q_heads][head_dim]."""
+        qs = self._rows(q, batch, self.cfg.n_q_heads)
+        if out is None:
+            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+        else:
+            self._rows(out, batch, self.cfg.n_q_heads)
+            _ptr(out)
+        self._call(lib().kvq_paged_attention, batch, stream, q.data_ptr(), qs, out.data_ptr(),
+                   self._scale if scale is None else float(scale), self.ws.data_ptr(),
+                   self.ws_bytes)
+        return out
+
+    def device_status(self, stream=None) -> int:
+        """Synchronizes, reads and clears the status word.  After an error the
+        scratch is zero-filled again."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        with torch.cuda.device(self.device):
+            code = lib().kvq_paged_status(ctypes.byref(self.view), stream.cuda_stream)
+            if code != KVQ_OK:
+                self.ws.zero_()
+                torch.cuda.synchronize(self.device)
+        return code
 
 
 def debug_stall_waits(iterations: int) -> None:

@@ -88,6 +88,7 @@ extern "C" {
 #define KVQ_EALIGN (-4)       /* a device buffer is not 16-byte aligned */
 #define KVQ_ECUDA (-5)        /* a CUDA launch or copy failed */
 #define KVQ_ETIMEOUT (-6)     /* a bounded device-side wait gave up (status word) */
+#define KVQ_EPAGE (-7)        /* a token's page is not in the block table (status word) */
 
 #define KVQ_KIVI 0
 #define KVQ_INNERQ 1
@@ -390,6 +391,135 @@ int kvq_decode_kernel_name(const kvq_config *cfg, int64_t n_quant, char *buf, si
  * groups of 32 or more and no cache options; other shapes name
  * "rope_decode_kernel<...>").  Host only, no CUDA call; same returns. */
 int kvq_rope_kernel_name(const kvq_config *cfg, int64_t n_quant, char *buf, size_t len);
+
+/* ---- Paged cache ---------------------------------------------------------
+ *
+ * A cache whose tokens live in fixed-size pages, for serving: sequences grow,
+ * end and share prefixes without moving data.  A sequence is a row of a block
+ * table (its pages in order), so several sequences may name the same page to
+ * read it.  Every token is quantized as it is written, per token and head in
+ * groups of 32 channels, keys and values alike: there is no fp16 residual and
+ * no per-sequence state beyond the lengths, which the caller keeps on the
+ * device.  The calls read lengths and tables on the device only, so a captured
+ * CUDA graph follows them from replay to replay.
+ *
+ * Stored form (b bits, per group of 32 channels of one token and head; x the
+ * 16-bit input, infinities and |x| > 32768 saturated to +-32768, NaN taken as
+ * 0, so the cache holds finite values only):
+ *   scale = fp16((max - min) / (2^b - 1)), zero = fp16(min),
+ *   code  = clamp(rint((x - zero) / scale), 0, 2^b - 1), 0 where scale is 0,
+ *   x_hat = code * scale + zero          (fp32; each rounding to nearest even)
+ *
+ * Layout.  pages u8 [n_pages][n_kv_heads][page_size/16][atom]; an atom holds
+ * 16 consecutive tokens of one head, rb = d*b/8 bytes of codes per row:
+ *   K codes [16][rb], V codes [16][rb],
+ *   K statistics fp16 [16][2][d/32], V statistics fp16 [16][2][d/32]
+ *     (per token the scales of its groups, then their zeros)
+ *   atom = 32 * (rb + 4*d/32) bytes.
+ * Within a row the codes are permuted so that a tensor-core fragment is a
+ * plain load.  Slot s of a row is its bits [s*b, (s+1)*b) (little endian):
+ *   K: channel 32*G + 8*j + 2*k + e (j, k in 0..3, e in 0..1) sits in 32-bit
+ *      word floor(p*b/16) of quarter j of the row, p = 4*G + k, at bit
+ *      (p*b mod 16) + 16*e;
+ *   V: channel 32*(2*h + e) + 4*g + i (g in 0..7, i in 0..3) sits in eighth g
+ *      of the row, p = 4*h + i, in its unit floor(p*b/w) of 2*w bits at bit
+ *      (p*b mod w) + w*e, w = 16 (8 when d = 64, b = 2).
+ */
+#define KVQ_F16 0
+#define KVQ_BF16 1
+
+/*
+ *   n_q_heads, n_kv_heads: n_q_heads = r * n_kv_heads, 1 <= r <= 128; query
+ *     head hq reads KV head hq / r.
+ *   head_dim d: 64 or 128.  bits: 2, 4 or 8.  page_size: tokens per page, 16,
+ *     32, 64, 128 or 256.  dtype: type of keys, values, queries and outputs.
+ *   n_pages: pages in the pool.
+ */
+typedef struct kvq_paged_config {
+  int32_t n_q_heads, n_kv_heads, head_dim, bits, page_size, dtype;
+  int64_t n_pages;
+} kvq_paged_config;
+
+/* Caller's buffers: the pages (kvq_paged_cache_bytes, 16-byte aligned; pages
+ * need no initial value) and one int32 status word, zero-filled once. */
+typedef struct kvq_paged_cache {
+  void *pages;
+  int32_t *dev_status;
+} kvq_paged_cache;
+
+/*
+ * One call's sequences.  Device arrays:
+ *   block_table int32 [n_seqs][table_width]  page of tokens [i*page_size,
+ *     (i+1)*page_size) of sequence b at [b][i]; entries behind a sequence's
+ *     last page are not read
+ *   seq_lens    int32 [n_seqs]   tokens sequence b holds, the call's included
+ *   cu_tokens   int32 [n_seqs+1] the call's rows [cu[b], cu[b+1]) belong to
+ *     sequence b and are its LAST n_b = cu[b+1] - cu[b] tokens: row cu[b] + i
+ *     is position seq_lens[b] - n_b + i.  cu[0] = 0, not decreasing.
+ * Host values: n_seqs (1..4096), table_width, n_tokens = rows of the packed
+ * arrays (rows from cu[n_seqs] on are padding: never read, never written),
+ * max_tokens >= every n_b.
+ * What the device arrays say is checked there: a row at a negative position
+ * is skipped (write), reads as zeros (read), attends to nothing (attention);
+ * a token whose page entry lies outside [0, n_pages) or behind table_width is
+ * skipped, reads as zeros or is not attended to, and KVQ_EPAGE goes to the
+ * status word; a sequence with more than max_tokens rows is not attended for
+ * and gives KVQ_EINVAL there.
+ */
+typedef struct kvq_paged_batch {
+  const int32_t *block_table, *seq_lens, *cu_tokens;
+  int64_t table_width, n_tokens;
+  int32_t n_seqs, max_tokens;
+} kvq_paged_batch;
+
+/* Bytes of the page pool, and of one page (out parameters may be null).
+ * Returns KVQ_OK, KVQ_EINVAL or KVQ_EUNSUPPORTED.  Host only. */
+int kvq_paged_cache_bytes(const kvq_paged_config *cfg, size_t *pool, size_t *page);
+
+/* Bytes of scratch kvq_paged_attention needs (any batch).  Zero-fill it once;
+ * every call leaves what must be zero at zero again.  Calls that can run at
+ * the same time need scratch of their own. */
+int kvq_paged_workspace_bytes(const kvq_paged_config *cfg, size_t *bytes);
+
+/*
+ * Quantize the call's tokens into their pages.  k, v: device, row t of head h
+ * at k + t*k_stride + h*head_dim (dtype elements; strides in elements, at
+ * least n_kv_heads*head_dim, multiples of 8), so a slice of a fused q-k-v
+ * projection can be given as it is.  Each written token must have a slot of
+ * its own: where two rows of a call name one slot (a page shared by two
+ * sequences that both write to it) that slot holds a mixture of the two.
+ * Errors: KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EALIGN, KVQ_ECUDA.
+ */
+int kvq_paged_write(const kvq_paged_config *cfg, kvq_paged_cache *cache,
+                    const kvq_paged_batch *batch, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, void *stream);
+
+/*
+ * Read the call's tokens back: x_hat rounded once to dtype, k_out and v_out
+ * [n_tokens][n_kv_heads][head_dim] contiguous.  cu_tokens = running sums of
+ * seq_lens reads whole sequences.  Errors as kvq_paged_write.
+ */
+int kvq_paged_read(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
+                   const kvq_paged_batch *batch, void *k_out, void *v_out, void *stream);
+
+/*
+ * Causal attention of the call's rows over the pages: row i of sequence b, at
+ * position p = seq_lens[b] - n_b + i, sees the sequence's tokens 0..p (its own
+ * included: write first).  One row per sequence is a decode step; chunks of
+ * any length, and batches that mix both, are one call.
+ *   q: device, row t of query head h at q + t*q_stride + h*head_dim
+ *   out [n_tokens][n_q_heads][head_dim], contiguous, dtype:
+ *     softmax(softmax_scale * q.K^T) V; zeros for a row that sees nothing.
+ *   ws: device scratch, ws_bytes >= kvq_paged_workspace_bytes.
+ * Errors: as kvq_paged_write; KVQ_ECAPACITY (ws too small).
+ */
+int kvq_paged_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
+                        const kvq_paged_batch *batch, const void *q, int64_t q_stride, void *out,
+                        float softmax_scale, void *ws, size_t ws_bytes, void *stream);
+
+/* Synchronizes `stream`, reads and clears the status word; KVQ_OK, or what a
+ * kernel recorded there (KVQ_EPAGE, KVQ_EINVAL, KVQ_ETIMEOUT), or KVQ_ECUDA. */
+int kvq_paged_status(kvq_paged_cache *cache, void *stream);
 
 /* Number of kernel launches the last successful call of this thread enqueued. */
 int kvq_last_launch_count(void);
