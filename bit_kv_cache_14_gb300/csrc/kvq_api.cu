@@ -18,6 +18,8 @@ bool pow2_group(int x) { return x == 16 || x == 32 || x == 64 || x == 128; }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
+}  // namespace
+
 // SM count per device, looked up once; calls from several host threads may
 // race to fill an entry, and all of them store the same value.
 int num_sms_cached() {
@@ -32,7 +34,6 @@ int num_sms_cached() {
   }
   return n;
 }
-}  // namespace
 
 void note_launch(int n) { t_last_launches = n; }
 

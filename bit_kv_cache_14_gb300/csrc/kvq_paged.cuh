@@ -29,6 +29,11 @@ struct Paged {
   int64_t T;          // rows of the packed arrays
 };
 
+// Attention of sequences with at most this many query rows (tokens x query
+// heads) per KV head goes to the split kernel (kvq_paged_rows.cu).
+constexpr int kPagedFewRows = 16;
+constexpr int kPagedRowBlocks = 320;  // its most blocks
+
 int resolve_paged(const kvq_paged_config *cfg, Paged *p);
 
 // Calls on the packed rows (cudaError_t of the launch).
@@ -38,6 +43,10 @@ cudaError_t launch_paged_read(const Paged &p, void *k, void *v, cudaStream_t st)
 cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, void *out,
                                    float scale, void *ws, cudaStream_t st, int *launches);
 size_t paged_workspace_bytes();
+cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
+                              void *ws, int num_sms, cudaStream_t st);
+size_t paged_rows_workspace();
+int num_sms_cached();
 
 namespace {
 

@@ -85,10 +85,14 @@ paged_attention_kernel(Paged p, const uint16_t *q, int64_t qs, uint16_t *out, fl
 
 }  // namespace
 
-size_t paged_workspace_bytes() { return 16; }
+size_t paged_workspace_bytes() { return paged_rows_workspace(); }
 
 cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, void *out,
                                    float scale, void *ws, cudaStream_t st, int *launches) {
+  if ((int64_t)p.max_tokens * p.rg <= kPagedFewRows) {
+    *launches = 1;
+    return launch_paged_rows(p, q, qs, out, scale, ws, num_sms_cached(), st);
+  }
   const unsigned grid = (unsigned)((p.T * p.Hq + kAttnThreads / 32 - 1) / (kAttnThreads / 32));
   auto kern = p.d == 128 ? (p.bits == 2   ? paged_attention_kernel<128, 2>
                             : p.bits == 4 ? paged_attention_kernel<128, 4>

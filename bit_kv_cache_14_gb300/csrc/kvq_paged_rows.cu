@@ -1,0 +1,747 @@
+// Paged cache: attention of sequences with few query rows (decode steps, a few
+// speculated tokens): at most 16 rows per KV head, a row being one query token
+// and head.
+//
+// What bounds it: the cache is read once, 2*(d*b/8 + d/8) bytes per token and
+// head against 4*d operations per row, so HBM, if the instructions per code stay
+// few enough (at 4 bits about 3.4 lane instructions per element keep up).
+//
+//  * Split: the 16-token atoms of all (sequence, head) pairs form one list, cut
+//    into equal contiguous ranges, one per block; inside a block the eight
+//    warps share each pair's atoms evenly.  Pairs that end up in several
+//    blocks leave partials (m, l, o), and the block that finishes a pair last
+//    joins them in block order, so results do not depend on timing.
+//  * A warp streams its atoms through a ring of shared-memory slots, one
+//    cp.async.bulk per atom (contiguous by layout), page numbers read one atom
+//    ahead of their use.
+//  * Keys: S^T[token][row] on mma.sync m16n8k16 with the raw codes as the A
+//    operand: a masked code in the low ten bits of a half is the fp16
+//    subnormal code * 2^(bit position) * 2^-24, exactly; the query operand
+//    divides the position out.  The row permutation of the layout makes a
+//    lane's share of a row one aligned vector.  Each group's sum is multiplied
+//    by the token's scale in fp32; the zero points enter through one
+//    m16n8k8 with the query's group sums in fp16 hi + lo.
+//  * Values: O^T[channel][row] with the codes of two tokens joined by a PRMT as
+//    the A operand and w = p * scale (fp16, one per group) as the B operand;
+//    movmatrix turns the score fragment into it.  Zero points: sum p * zero in
+//    fp32.
+//  * Softmax: a lazy reference per row, moved only when a score passes it by
+//    more than 2 (log2 units), decided by one vote.  The reference also carries
+//    E, the exponent of the largest value scale seen, so that w <= 2^2 and
+//    keeps fp16's full precision whatever the scale of the values.
+#include "kvq_paged.cuh"
+#include "kvq_tc_common.cuh"
+
+namespace kvq {
+
+int debug_stall_limit();
+
+namespace {
+
+constexpr int kRowWarps = 8;
+constexpr int kRowThreads = 32 * kRowWarps;
+constexpr int kRowWaitLimit = 1 << 24;
+constexpr float kNoRef = -1e30f;
+
+struct RowsArgs {
+  Paged p;
+  const uint16_t *q;
+  int64_t qs;
+  uint16_t *out;
+  float scale_log2;
+  float *ws_ml;    // [2 * blocks][rows][2]
+  float *ws_o;     // [2 * blocks][rows][d]
+  int *ws_count;   // [blocks], zero between calls
+  int min_units, snap;
+  int stall_limit;
+};
+
+template <int D, int BITS, int NT>
+struct RowsCfg {
+  static constexpr int RB = D * BITS / 8, SB = 4 * D / kPagedGroup, NG = D / kPagedGroup;
+  static constexpr int AB = 2 * kAtom * (RB + SB);
+  static constexpr int kBlocks = NT == 1 ? 2 : 1;  // per SM
+  // ring slots per warp: about 160 KB in flight per SM
+  static constexpr int S = NT == 1 ? (AB > 4000 ? 2 : AB > 2000 ? 3 : AB > 1400 ? 5 : 8)
+                                   : (AB > 4000 ? 3 : AB > 2000 ? 5 : 8);
+  static constexpr int ROWB = D * 4 + 16;  // padded row of the merge buffer
+  static constexpr int off_merge = kRowWarps * S * AB;
+  static constexpr int off_ml = off_merge + kRowWarps * 8 * NT * ROWB;
+  static constexpr int off_bar = off_ml + kRowWarps * 8 * NT * 8;
+  static constexpr int off_prefix = off_bar + kRowWarps * (S + 1) * 8;
+  static constexpr int smem(int seqs) { return off_prefix + (seqs + 1) * 8; }
+};
+
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+
+// Codes at bit `off` of both halves of w: code * 2^(off % 8) * 2^-24 as fp16.
+template <int BITS>
+__device__ __forceinline__ uint32_t codes_at(uint32_t w, uint32_t w8, int off) {
+  constexpr uint32_t kOne = (1u << BITS) - 1;
+  return (off & 8 ? w8 : w) & ((kOne | kOne << 16) << (off & 7));
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t *src, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(src + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(src);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(src);
+  }
+}
+
+
+// Where a unit index lies: sequence, head, offset inside the pair.
+struct Place {
+  int b, h, off, atoms;
+};
+__device__ __forceinline__ Place locate(const int64_t *prefix, int H, int64_t x, int b) {
+  while (H * prefix[b + 1] <= x) ++b;
+  Place u;
+  u.b = b;
+  u.atoms = (int)(prefix[b + 1] - prefix[b]);
+  const int64_t r = x - H * prefix[b];
+  u.h = (int)(r / u.atoms);
+  u.off = (int)(r - (int64_t)u.h * u.atoms);
+  return u;
+}
+__device__ __forceinline__ int seq_of_unit(const int64_t *prefix, int B, int H, int64_t x) {
+  int lo = 0, hi = B;  // the last b with H * prefix[b] <= x and units of its own
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (H * prefix[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// First unit of block c: c * U, moved to a pair's border when one is near.
+__device__ __forceinline__ int64_t border(const int64_t *prefix, int B, int H, int64_t total,
+                                          int64_t U, int snap, int64_t c) {
+  const int64_t x = c * U;
+  if (x >= total) return total;
+  if (x == 0) return 0;
+  const Place u = locate(prefix, H, x, seq_of_unit(prefix, B, H, x));
+  if (u.off <= snap && u.off <= u.atoms - u.off) return x - u.off;
+  if (u.atoms - u.off <= snap) return x + u.atoms - u.off;
+  return x;
+}
+
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(kRowThreads, RowsCfg<D, BITS, NT>::kBlocks)
+paged_rows_kernel(const __grid_constant__ RowsArgs a) {
+  using C = RowsCfg<D, BITS, NT>;
+  constexpr int RB = C::RB, SB = C::SB, NG = C::NG, S = C::S;
+  constexpr int KW = RB / 16, VW = (RB / 8 + 3) / 4;  // words of a key quarter, a value eighth
+  constexpr int kRows = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int sh_flag;
+  const Paged &p = a.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
+  uint8_t *ring = smem + warp * S * C::AB;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::off_bar) + warp * (S + 1);
+  int64_t *prefix = reinterpret_cast<int64_t *>(smem + C::off_prefix);
+
+  if (lane <= S) bar_init(&bars[lane], 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+
+  // ---- the list of work: prefix[b] = atoms of one head of the sequences
+  // before b that have between 1 and kMaxRows rows
+  {
+    __shared__ int64_t warp_sum[kRowWarps];
+    const int per = (p.B + kRowThreads - 1) / kRowThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int n = p.cu[b + 1] - p.cu[b];
+      int64_t atoms = 0;
+      if (n > p.max_tokens || p.cu[b] < 0 || p.cu[b + 1] > p.T) {
+        if (blockIdx.x == 0) paged_error(p, KVQ_EINVAL);
+      } else if (n > 0 && (int64_t)n * p.rg <= kPagedFewRows) {
+        const int64_t cap = p.width * p.page, len = p.lens[b];
+        if (len > cap && blockIdx.x == 0) paged_error(p, KVQ_EPAGE);
+        atoms = (min(len, cap) + kAtom - 1) / kAtom;
+        if (atoms < 1) atoms = 1;  // rows that see nothing are written too
+      }
+      sum += atoms;
+      prefix[b + 1] = sum;
+    }
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    for (int b = b0; b < b1; ++b) prefix[b + 1] += before;
+    if (tid == 0) prefix[0] = 0;
+    __syncthreads();
+  }
+  const int H = p.H;
+  const int64_t total = H * prefix[p.B];
+  const int64_t U = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)a.min_units);
+  const int64_t x0 = border(prefix, p.B, H, total, U, a.snap, blockIdx.x);
+  const int64_t x1 = border(prefix, p.B, H, total, U, a.snap, blockIdx.x + 1);
+  if (x0 >= x1) return;
+
+  const uint64_t policy = l2_evict_first();
+  bool dead = false;
+  if (a.stall_limit > 0 && !bar_wait(&bars[S], 0, a.stall_limit)) {
+    if (lane == 0) paged_error(p, KVQ_ETIMEOUT);
+    dead = true;
+  }
+  const int first_b = seq_of_unit(prefix, p.B, H, x0);
+
+  // ---- fetch side: this warp's atoms of every segment of [x0, x1) in turn.
+  // (fb, fh): the pair being fetched; f0: next atom; pid: its page, read ahead
+  int64_t fx = x0;
+  int fb = first_b, fh = 0, f0 = 0, f1 = 0;
+  const int apage_log = __ffs(p.page / kAtom) - 1;
+  int pid = -1;
+  auto fetch_next = [&]() {  // moves to the next atom; false at the end
+    while (f0 == f1) {
+      if (fx >= x1) return false;
+      const Place u = locate(prefix, H, fx, fb);
+      const int n = (int)min((int64_t)(u.atoms - u.off), x1 - fx);
+      fb = u.b, fh = u.h;
+      f0 = u.off + (int)((int64_t)n * warp / kRowWarps);
+      f1 = u.off + (int)((int64_t)n * (warp + 1) / kRowWarps);
+      fx += n;
+    }
+    return true;
+  };
+  auto read_pid = [&]() {
+    // (a pair that holds no tokens has one atom without a page: any entry)
+    pid = __ldg(p.table + fb * p.width + (f0 >> apage_log));
+  };
+  int issued = 0, used = 0;
+  uint32_t skip = 0;  // bit per slot: the atom's page does not exist
+  bool more = fetch_next();
+  if (more) read_pid();
+  auto issue = [&]() {
+    const int slot = issued % S;
+    const int at = f0 & ((1 << apage_log) - 1), head = fh;
+    const int64_t id = pid;
+    const bool ok = id >= 0 && id < p.n_pages;
+    // the next atom's page number is on its way while this one's copy starts
+    ++f0;
+    more = fetch_next();
+    if (more) read_pid();
+    if (ok) {
+      skip &= ~(1u << slot);
+      if (lane == 0) {
+        bulk_g2s_pred(true, smem_u32(&bars[slot]), C::AB, smem_u32(ring + slot * C::AB),
+                      p.pages + id * p.page_bytes + head * p.head_bytes + (int64_t)at * C::AB,
+                      C::AB, policy);
+      }
+    } else {
+      skip |= 1u << slot;
+      if (lane == 0) bar_expect_tx(&bars[slot], 0);
+    }
+    ++issued;
+  };
+  if (!dead)
+    for (int i = 0; i < S && more; ++i) issue();
+
+  // ---- consume side, segment by segment
+  int b = first_b;
+  for (int64_t x = x0; x < x1;) {
+    const Place u = locate(prefix, H, x, b);
+    b = u.b;
+    const int n = (int)min((int64_t)(u.atoms - u.off), x1 - x);
+    const int a0 = u.off + (int)((int64_t)n * warp / kRowWarps);
+    const int a1 = u.off + (int)((int64_t)n * (warp + 1) / kRowWarps);
+    const int row0 = p.cu[b], tokens = p.cu[b + 1] - row0, rows = tokens * p.rg;
+    const int64_t cap = p.width * p.page;
+    const int len = (int)min((int64_t)max(p.lens[b], 0), cap);
+    // newest position row r may see; every row's is below len
+    const int64_t pos0 = (int64_t)p.lens[b] - tokens;
+
+    // queries: lane (g, j) holds, of row 8*nt + g, channels 32*G + 8*j .. + 7,
+    // scaled so that the row's largest is in [2^8, 2^9)
+    uint32_t qf[NT][NG][4], qsum[NT];
+    float F[NT][2];
+    int limit[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      const bool in = r < rows;
+      const uint16_t *src = a.q + (int64_t)(row0 + (in ? r / p.rg : 0)) * a.qs +
+                            (int64_t)(u.h * p.rg + (in ? r % p.rg : 0)) * D + 8 * j;
+      float f[NG][8], big = 0.0f;
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 32 * G));
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (p.bf16) {
+            f[G][2 * i] = __uint_as_float(ww[i] << 16);
+            f[G][2 * i + 1] = __uint_as_float(ww[i] & 0xffff0000u);
+          } else {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&ww[i]));
+            f[G][2 * i] = v.x;
+            f[G][2 * i + 1] = v.y;
+          }
+          if (!in) f[G][2 * i] = f[G][2 * i + 1] = 0.0f;
+          big = fmaxf(big, fmaxf(fabsf(f[G][2 * i]), fabsf(f[G][2 * i + 1])));
+        }
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      int ex = ((__float_as_int(big) >> 23) & 255) - 127;
+      ex = big == 0.0f ? 0 : max(min(ex, 90), -90);
+      const float mul = __int_as_float((127 + 8 - ex) << 23);
+      float gs[NG];
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        gs[G] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int o = ((G * 4 + i) * BITS) % 8;  // position of this pair's codes
+          const float pos = __int_as_float((127 - o) << 23);
+          // (bf16 queries round here, to fp16 relative to the row's largest)
+          const __half2 v = __floats2half2_rn(f[G][2 * i] * mul, f[G][2 * i + 1] * mul);
+          const float2 vf = __half22float2(v);
+          gs[G] += vf.x + vf.y;
+          qf[nt][G][i] = h2u(__floats2half2_rn(vf.x * pos, vf.y * pos));
+        }
+        gs[G] += __shfl_xor_sync(0xffffffffu, gs[G], 1);
+        gs[G] += __shfl_xor_sync(0xffffffffu, gs[G], 2);
+      }
+      // zero-point operand: k = group for the hi parts, then for the lo parts
+      uint32_t hi, lo;
+      if (NG == 4) {
+        const bool up = j & 1;
+        split2(up ? gs[2 % NG] : gs[0], up ? gs[3 % NG] : gs[1], hi, lo);
+        qsum[nt] = j < 2 ? hi : lo;
+      } else {
+        split2(gs[0], gs[1], hi, lo);
+        qsum[nt] = j == 0 ? hi : j == 1 ? lo : 0u;
+      }
+      // per-row factors move to the lanes that hold the row's scores
+      const float mine = a.scale_log2 * __int_as_float((127 + 24 + ex - 8) << 23);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int rr = 8 * nt + 2 * j + s;
+        F[nt][s] = __shfl_sync(0xffffffffu, mine, (2 * j + s) * 4);
+        const int64_t see = pos0 + rr / p.rg;
+        limit[nt][s] = rr < rows ? (int)min(see, (int64_t)len - 1) : len - 1;
+      }
+    }
+    const int least = (int)min(pos0, (int64_t)len - 1);  // newest position every row sees
+
+    float o[NG][2][NT][4] = {}, za[NG][NT][2] = {}, l[NT][2] = {}, rf[NT][2], lim[NT][2];
+    uint32_t e2 = 0;  // largest value scale covered by the reference, in both halves
+    int E = -24;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) rf[nt][s] = kNoRef, lim[nt][s] = kNoRef;
+
+    for (int at = a0; at < a1; ++at) {
+      if (dead) break;
+      const int slot = used % S;
+      if (!bar_wait(&bars[slot], (used / S) & 1, kRowWaitLimit)) {
+        if (lane == 0) paged_error(p, KVQ_ETIMEOUT);
+        dead = true;
+        break;
+      }
+      ++used;
+      const uint8_t *at_s = ring + slot * C::AB;
+      if (at * kAtom >= len) {
+        // the one atom of a sequence without tokens
+      } else if (skip >> slot & 1) {
+        if (lane == 0) paged_error(p, KVQ_EPAGE);
+      } else {
+        // token of fragment row r < 8: (r >> 1) + 4 * (r & 1); rows 8.. 8 more
+        const int t0 = (g >> 1) + 4 * (g & 1);
+        uint32_t k0[KW], k1[KW], ks[2][NG], vs[2][NG];
+        lds_words(at_s + t0 * RB + j * (RB / 4), k0);
+        lds_words(at_s + (t0 + 8) * RB + j * (RB / 4), k1);
+        // statistics of a token: NG scales then NG zeros, as pairs
+        const uint8_t *st = at_s + 2 * kAtom * RB;
+        lds_words(st + t0 * SB, ks[0]);
+        lds_words(st + (t0 + 8) * SB, ks[1]);
+        lds_words(st + kAtom * SB + t0 * SB, vs[0]);
+        lds_words(st + kAtom * SB + (t0 + 8) * SB, vs[1]);
+        const int pos = at * kAtom;
+        const bool masked = pos + kAtom - 1 > least;
+        if (masked) {
+          // slots behind the last token hold anything
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (pos + t0 + 8 * i >= len) {
+#pragma unroll
+              for (int n2 = 0; n2 < NG; ++n2) ks[i][n2] = vs[i][n2] = 0u;
+            }
+        }
+        // ---- scores
+        float t[NT][4];
+        {
+          const uint32_t z0 = NG == 4 ? (j & 1 ? ks[0][3 % NG] : ks[0][2 % NG]) : ks[0][1];
+          const uint32_t z1 = NG == 4 ? (j & 1 ? ks[1][3 % NG] : ks[1][2 % NG]) : ks[1][1];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float zt[4] = {};
+            mma1688(zt, z0, z1, qsum[nt]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[nt][i] = zt[i] * (1.0f / kSub);
+          }
+        }
+        uint32_t k08[KW], k18[KW];
+#pragma unroll
+        for (int i = 0; i < KW; ++i) k08[i] = k0[i] >> 8, k18[i] = k1[i] >> 8;
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+          float c[NT][4] = {};
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const int pa = (G * 4 + 2 * m) * BITS, pb = pa + BITS;  // bit offsets of two pairs
+            const uint32_t x0_ = codes_at<BITS>(k0[pa / 16], k08[pa / 16], pa % 16);
+            const uint32_t x1_ = codes_at<BITS>(k1[pa / 16], k18[pa / 16], pa % 16);
+            const uint32_t x2_ = codes_at<BITS>(k0[pb / 16], k08[pb / 16], pb % 16);
+            const uint32_t x3_ = codes_at<BITS>(k1[pb / 16], k18[pb / 16], pb % 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(c[nt], x0_, x1_, x2_, x3_, qf[nt][G][2 * m], qf[nt][G][2 * m + 1]);
+          }
+          const float2 s0 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[0][G / 2]));
+          const float2 s1 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[1][G / 2]));
+          const float f0_ = G & 1 ? s0.y : s0.x, f1_ = G & 1 ? s1.y : s1.x;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            t[nt][0] += f0_ * c[nt][0];
+            t[nt][1] += f0_ * c[nt][1];
+            t[nt][2] += f1_ * c[nt][2];
+            t[nt][3] += f1_ * c[nt][3];
+          }
+        }
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            t[nt][i] *= F[nt][i & 1];
+            if (masked && pos + t0 + 8 * (i >> 1) > limit[nt][i & 1]) t[nt][i] = -INFINITY;
+            over |= t[nt][i] > lim[nt][i & 1];
+          }
+        {
+          __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&vs[0][0]),
+                              *reinterpret_cast<const __half2 *>(&vs[1][0]));
+          if (NG == 4)
+            m = __hmax2(m, __hmax2(*reinterpret_cast<const __half2 *>(&vs[0][1]),
+                                   *reinterpret_cast<const __half2 *>(&vs[1][1])));
+          over |= !__hble2(m, *reinterpret_cast<const __half2 *>(&e2));
+          if (__any_sync(0xffffffffu, over)) {
+            // move the reference: to the largest score, and E to the scales
+            float sm = fmaxf(__low2float(m), __high2float(m));
+#pragma unroll
+            for (int s = 16; s; s >>= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, s));
+            const int En = sm > 0.0f ? max(E, ((__float_as_int(sm) >> 23) & 255) - 126) : E;
+            const uint32_t top = h2u(__float2half2_rn(__int_as_float((127 + En) << 23)));
+            e2 = En > 15 ? 0x7bff7bffu : top;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                float mx = fmaxf(t[nt][s], t[nt][2 + s]);
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1)
+                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+                const float ref = fmaxf(rf[nt][s] - (float)E, mx);
+                // (before the first score, a row's reference stays at kNoRef)
+                const float nrf = rf[nt][s] == kNoRef && mx < kNoRef ? kNoRef : ref + (float)En;
+                const float f = exp2_approx(rf[nt][s] - nrf);
+                rf[nt][s] = nrf;
+                lim[nt][s] = nrf == kNoRef ? kNoRef : ref + kSlack;
+                l[nt][s] *= f;
+#pragma unroll
+                for (int G = 0; G < NG; ++G) {
+                  za[G][nt][s] *= f;
+                  o[G][0][nt][s] *= f;
+                  o[G][0][nt][2 + s] *= f;
+                  o[G][1][nt][s] *= f;
+                  o[G][1][nt][2 + s] *= f;
+                }
+              }
+            E = En;
+          }
+        }
+        // ---- weights
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[nt][i] = exp2_approx(t[nt][i] - rf[nt][i & 1]);
+          l[nt][0] += t[nt][0] + t[nt][2];
+          l[nt][1] += t[nt][1] + t[nt][3];
+        }
+        uint32_t w[NG][NT][2];
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+          const float2 s0 = __half22float2(*reinterpret_cast<const __half2 *>(&vs[0][G / 2]));
+          const float2 s1 = __half22float2(*reinterpret_cast<const __half2 *>(&vs[1][G / 2]));
+          const float2 z0 =
+              __half22float2(*reinterpret_cast<const __half2 *>(&vs[0][NG / 2 + G / 2]));
+          const float2 z1 =
+              __half22float2(*reinterpret_cast<const __half2 *>(&vs[1][NG / 2 + G / 2]));
+          const float sa = G & 1 ? s0.y : s0.x, sb = G & 1 ? s1.y : s1.x;
+          const float ya = G & 1 ? z0.y : z0.x, yb = G & 1 ? z1.y : z1.x;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            w[G][nt][0] = movm(h2u(__floats2half2_rn(t[nt][0] * sa, t[nt][1] * sa)));
+            w[G][nt][1] = movm(h2u(__floats2half2_rn(t[nt][2] * sb, t[nt][3] * sb)));
+            za[G][nt][0] += t[nt][0] * ya + t[nt][2] * yb;
+            za[G][nt][1] += t[nt][1] * ya + t[nt][3] * yb;
+          }
+        }
+        // ---- values: tokens (j, j + 4) and (j + 8, j + 12), eighth g
+        const uint8_t *vc = at_s + kAtom * RB + g * (RB / 8);
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (RB / 8 == 2)
+            v[i][0] = *reinterpret_cast<const uint16_t *>(vc + (j + 4 * i) * RB);
+          else
+            lds_words(vc + (j + 4 * i) * RB, v[i]);
+        }
+        // bits of a half: 16, or 8 for the two-byte eighths of d = 64, 2 bits
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t xa[VW], xb[VW], xa8[VW], xb8[VW];
+#pragma unroll
+          for (int i = 0; i < VW; ++i) {
+            const uint32_t sel = RB / 8 == 2 ? 0x5410u : e ? 0x7632u : 0x5410u;
+            xa[i] = __byte_perm(v[0][i], v[1][i], sel);
+            xb[i] = __byte_perm(v[2][i], v[3][i], sel);
+            xa8[i] = xa[i] >> 8;
+            xb8[i] = xb[i] >> 8;
+          }
+#pragma unroll
+          for (int h2 = 0; h2 < NG / 2; ++h2) {
+            const int G = 2 * h2 + e;
+#pragma unroll
+            for (int ii = 0; ii < 2; ++ii) {
+              const int pa = (h2 * 4 + 2 * ii) * BITS + (RB / 8 == 2 ? 8 * e : 0), pb = pa + BITS;
+              const uint32_t y0 = codes_at<BITS>(xa[pa / 16], xa8[pa / 16], pa % 16);
+              const uint32_t y1 = codes_at<BITS>(xa[pb / 16], xa8[pb / 16], pb % 16);
+              const uint32_t y2 = codes_at<BITS>(xb[pa / 16], xb8[pa / 16], pa % 16);
+              const uint32_t y3 = codes_at<BITS>(xb[pb / 16], xb8[pb / 16], pb % 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(o[G][ii][nt], y0, y1, y2, y3, w[G][nt][0], w[G][nt][1]);
+            }
+          }
+        }
+      }
+      // the slot is free once every lane has read it
+      __syncwarp();
+      if (more) issue();
+    }
+
+    // ---- the block's state of this segment: every warp's (reference, l, o)
+    // to shared memory, joined slice by slice
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) l[nt][s] += __shfl_xor_sync(0xffffffffu, l[nt][s], k);
+        const int r = 8 * nt + 2 * j + s;
+        uint8_t *row = smem + C::off_merge + (warp * kRows + r) * C::ROWB;
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+          float z = za[G][nt][s];
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
+          float4 v;
+          float *vf = &v.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int off = (((G >> 1) * 4 + i) * BITS + (RB / 8 == 2 ? 8 * (G & 1) : 0)) % 8;
+            vf[i] = o[G][i >> 1][nt][2 * (i & 1) + s] * __int_as_float((127 + 24 - off) << 23) + z;
+          }
+          *reinterpret_cast<float4 *>(row + (G * 8 + g) * 16) = v;
+        }
+        if (g == 0)
+          *reinterpret_cast<float2 *>(smem + C::off_ml + (warp * kRows + r) * 8) =
+              make_float2(rf[nt][s], l[nt][s]);
+      }
+    __syncthreads();
+    // which blocks share the pair
+    const int64_t pair0 = x - u.off, pair1 = pair0 + u.atoms;
+    const bool whole = pair0 >= x0 && pair1 <= x1;
+    constexpr int kQuads = D / 4;
+    int c_first = 0, c_last = 0;
+    if (!whole) {
+      // (a border moves by less than a range's length, and never past a pair's)
+      c_first = (int)(pair0 / U);
+      if (border(prefix, p.B, H, total, U, a.snap, c_first + 1) <= pair0) ++c_first;
+      c_last = (int)((pair1 - 1) / U);
+      if (border(prefix, p.B, H, total, U, a.snap, c_last) >= pair1) --c_last;
+    }
+    auto store = [&](int r, int quad, float4 v, float sum) {
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      uint2 w2;
+      if (p.bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        w2 = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                        *reinterpret_cast<const uint32_t *>(&hi));
+      } else {
+        w2 = make_uint2(h2u(__floats2half2_rn(v.x * inv, v.y * inv)),
+                        h2u(__floats2half2_rn(v.z * inv, v.w * inv)));
+      }
+      const int64_t t = row0 + r / p.rg;
+      if (t < p.T)
+        *reinterpret_cast<uint2 *>(a.out + (t * p.Hq + u.h * p.rg + r % p.rg) * D + 4 * quad) = w2;
+    };
+    const int my_slot = 2 * blockIdx.x + (pair0 >= x0 ? 1 : 0);
+    for (int i = tid; i < rows * kQuads; i += kRowThreads) {
+      const int r = i / kQuads, quad = i % kQuads;
+      float m = kNoRef;
+      float2 ml[kRowWarps];
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) {
+        ml[w] = *reinterpret_cast<const float2 *>(smem + C::off_ml + (w * kRows + r) * 8);
+        m = fmaxf(m, ml[w].x);
+      }
+      float sum = 0.0f;
+      float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) {
+        const float f = exp2_approx(ml[w].x - m);
+        const float4 y = *reinterpret_cast<const float4 *>(
+            smem + C::off_merge + (w * kRows + r) * C::ROWB + quad * 16);
+        sum += f * ml[w].y;
+        v.x += f * y.x;
+        v.y += f * y.y;
+        v.z += f * y.z;
+        v.w += f * y.w;
+      }
+      if (whole) {
+        store(r, quad, v, sum);
+      } else {
+        *reinterpret_cast<float4 *>(a.ws_o + ((int64_t)my_slot * kRows + r) * D + 4 * quad) = v;
+        if (quad == 0)
+          *reinterpret_cast<float2 *>(a.ws_ml + ((int64_t)my_slot * kRows + r) * 2) =
+              make_float2(m, sum);
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int before = atomicAdd(&a.ws_count[c_first], 1);
+        sh_flag = before == c_last - c_first;
+        if (sh_flag) a.ws_count[c_first] = 0;
+      }
+      __syncthreads();
+      if (sh_flag) {
+        __threadfence();
+        for (int i = tid; i < rows * kQuads; i += kRowThreads) {
+          const int r = i / kQuads, quad = i % kQuads;
+          float m = kNoRef, sum = 0.0f;
+          float4 v = make_float4(0, 0, 0, 0);
+          for (int c = c_first; c <= c_last; ++c) {
+            const int64_t at = (int64_t)(2 * c + (c == c_first)) * kRows + r;
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ws_ml + at * 2));
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + at * D + 4 * quad));
+            const float nm = fmaxf(m, ml.x), f = exp2_approx(m - nm), f2 = exp2_approx(ml.x - nm);
+            m = nm;
+            sum = sum * f + f2 * ml.y;
+            v.x = v.x * f + f2 * y.x;
+            v.y = v.y * f + f2 * y.y;
+            v.z = v.z * f + f2 * y.z;
+            v.w = v.w * f + f2 * y.w;
+          }
+          store(r, quad, v, sum);
+        }
+      }
+    }
+    __syncthreads();  // the merge buffer is free for the next segment
+    x += n;
+  }
+  // a warp that gave up leaves no copy of its own in flight
+  if (dead)
+    for (; used < issued; ++used) bar_wait(&bars[used % S], (used / S) & 1, kDrainLimit);
+}
+
+template <int D, int BITS, int NT>
+cudaError_t launch_as(RowsArgs &a, int num_sms, cudaStream_t st) {
+  using C = RowsCfg<D, BITS, NT>;
+  static KernelSetup setup;
+  const int smem = C::smem(a.p.B);
+  int occ = 0;
+  auto kern = paged_rows_kernel<D, BITS, NT>;
+  cudaError_t e = kernel_setup(setup, kern, kRowThreads, smem, &occ);
+  if (e != cudaSuccess) return e;
+  int blocks = num_sms * occ;
+  if (blocks > kPagedRowBlocks) blocks = kPagedRowBlocks;
+  kern<<<blocks, kRowThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
+                              void *ws, int num_sms, cudaStream_t st) {
+  RowsArgs a;
+  a.p = p;
+  a.q = static_cast<const uint16_t *>(q);
+  a.qs = qs;
+  a.out = static_cast<uint16_t *>(out);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  a.ws_count = reinterpret_cast<int *>(w);
+  a.ws_ml = reinterpret_cast<float *>(w + kPagedRowBlocks * 4);
+  a.ws_o = reinterpret_cast<float *>(w + kPagedRowBlocks * 4 +
+                                     2 * kPagedRowBlocks * kPagedFewRows * 8);
+  a.min_units = 32;
+  a.snap = 8;
+  a.stall_limit = debug_stall_limit();
+  const int64_t most = (int64_t)p.max_tokens * p.rg;
+  // one tile of 8 rows when no sequence has more, two otherwise
+  if (p.d == 128) {
+    if (most <= 8)
+      return p.bits == 2   ? launch_as<128, 2, 1>(a, num_sms, st)
+             : p.bits == 4 ? launch_as<128, 4, 1>(a, num_sms, st)
+                           : launch_as<128, 8, 1>(a, num_sms, st);
+    return p.bits == 2   ? launch_as<128, 2, 2>(a, num_sms, st)
+           : p.bits == 4 ? launch_as<128, 4, 2>(a, num_sms, st)
+                         : launch_as<128, 8, 2>(a, num_sms, st);
+  }
+  if (most <= 8)
+    return p.bits == 2   ? launch_as<64, 2, 1>(a, num_sms, st)
+           : p.bits == 4 ? launch_as<64, 4, 1>(a, num_sms, st)
+                         : launch_as<64, 8, 1>(a, num_sms, st);
+  return p.bits == 2   ? launch_as<64, 2, 2>(a, num_sms, st)
+         : p.bits == 4 ? launch_as<64, 4, 2>(a, num_sms, st)
+                       : launch_as<64, 8, 2>(a, num_sms, st);
+}
+
+size_t paged_rows_workspace() {
+  return kPagedRowBlocks * 4 + 2 * kPagedRowBlocks * kPagedFewRows * (8 + 4 * kMaxHeadDim);
+}
+
+}  // namespace kvq
