@@ -1,0 +1,999 @@
+// Paged cache: attention of chunks of new tokens, on tcgen05.
+//
+// Rows: the query tokens of a sequence times the query heads of one KV head,
+// token-major, so that grouped heads share the keys and values read for them.
+// A block works on 256 of them (two MMA tiles of 128) against 128 cached tokens
+// at a time:
+//   S_i = Q_i K^T                      tcgen05.mma, both operands in shared memory
+//   P_i = 2^(S_i F - ref)              one thread per row; fp16, back into tensor memory
+//   O_i (+)= P_i V                     tcgen05.mma, P from tensor memory
+// S, P and O stay in tensor memory (S and P share columns).  The reference of
+// a row moves only when a score passes it by more than 8 (log2 units), so O is
+// rescaled a few times per row at most, by the row's own thread.
+//
+// Bound: 4*128*256*d operations per step on the tensor core against 128*256
+// exponentials and the dequantization of 128 keys and values: four producer
+// warps read codes and statistics into registers one step ahead, turn codes
+// into fp16 (1024 + code by one LOP3, the code by one HFMA2, code * scale +
+// zero by a second: exact but for one rounding) and store the swizzled operand
+// tiles, which both query tiles use.
+//
+//   warps 0-3, 4-7: softmax and output of query tiles 0 and 1
+//   warps 8-11: producers    warp 12: MMA issue (one thread)
+//
+// Split: every (sequence, head, 256-row tile) is a list of its visible 128-token
+// steps plus kOver for its start and end; the concatenated list is cut into
+// equal ranges, one per block.  A tile cut by a border leaves partials, joined
+// in block order by the block that finishes last.
+#include "kvq_paged.cuh"
+#include "kvq_tc_common.cuh"
+
+namespace kvq {
+
+int debug_stall_limit();
+
+namespace {
+
+constexpr int kChunkThreads = 512;
+constexpr int kStep = 128;       // cached tokens per step
+constexpr int kTileRows = 256;   // query rows per block
+constexpr int kOver = 2;         // units of a tile's start and end
+constexpr int kMinUnits = 8;
+constexpr int kMaxChunkBlocks = 160;
+constexpr int kChunkWait = 1 << 22;
+constexpr float kChunkSlack = 8.0f;
+constexpr float kNoRef = -1e30f;
+
+struct ChunkArgs {
+  Paged p;
+  const uint16_t *q;
+  int64_t qs;
+  uint16_t *out;
+  float scale_log2;  // >= 0
+  float sign;        // of the softmax scale, folded into the queries
+  int few;           // sequences with at most this many rows are not this kernel's
+  float *ws_ml;      // [2 * blocks][2 tiles][128][2]
+  float *ws_o;       // [2 * blocks][2 tiles][d / 4][128] float4
+  int *ws_count;     // [blocks][2 tiles], zero between calls
+  int stall_limit;
+};
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int kTile = kStep * D * 2;  // bytes of a 128-row operand tile
+  static constexpr int off_q = 0;
+  static constexpr int off_k = 2 * kTile;
+  static constexpr int off_v = off_k + 2 * kTile;
+  static constexpr int off_f = off_v + 2 * kTile;          // float [256] row factors
+  static constexpr int off_bad = off_f + kTileRows * 4;    // bytes [4][8]: atoms without a page
+  static constexpr int off_bar = off_bad + 32;
+  static constexpr int kBars = 19;
+  static constexpr int off_misc = off_bar + kBars * 8;     // tensor memory base, dead flag, flags
+  static constexpr int off_prefix = off_misc + 64;
+  static constexpr int smem(int seqs) { return off_prefix + (seqs + 1) * 8 + 1024; }
+};
+
+// ---- PTX ------------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A poll that suspends the thread for a microsecond at most.
+__device__ __forceinline__ bool bar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void async_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 32 consecutive 32-bit columns of the warp's lanes.
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Shared-memory matrix descriptor: 128-byte swizzle, strides in bytes.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 |
+         (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// Instruction descriptor: fp16 operands, fp32 accumulator, M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major) {
+  return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__host__ __device__ constexpr uint32_t dup16(uint32_t h) { return h | h << 16; }
+
+// Codes at bit `off` (0 .. 7) of both halves of w, as exact fp16 numbers:
+// (code << off) | 1024.0, times 2^-off, minus 1024 * 2^-off.
+template <int BITS>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int off) {
+  const uint32_t mask = dup16(((1u << BITS) - 1) << off);
+  const uint32_t h = and_or(w, mask, 0x64006400u);
+  // 2^-off and -1024 * 2^-off as fp16
+  const uint32_t mul = dup16((uint32_t)(15 - off) << 10);
+  const uint32_t sub = dup16(0x8000u | (uint32_t)(25 - off) << 10);
+  return hfma2(h, mul, sub);
+}
+
+// ---- the list of work -------------------------------------------------------
+// Tokens, rows and visible length of sequence b; rows = 0 when it is not this
+// kernel's.
+struct Seq {
+  int row0, tokens, rows, len;
+  int64_t pos0;
+};
+__device__ __forceinline__ Seq seq_of(const ChunkArgs &a, int b) {
+  const Paged &p = a.p;
+  Seq s;
+  s.row0 = p.cu[b];
+  s.tokens = p.cu[b + 1] - s.row0;
+  const int64_t cap = p.width * p.page;
+  s.len = (int)min((int64_t)max(p.lens[b], 0), cap);
+  s.pos0 = (int64_t)p.lens[b] - s.tokens;
+  const bool ok = s.tokens <= p.max_tokens && s.row0 >= 0 && p.cu[b + 1] <= p.T;
+  const int64_t rows = (int64_t)s.tokens * p.rg;
+  s.rows = ok && rows > a.few ? (int)rows : 0;
+  return s;
+}
+// Visible steps of 256-row tile t.
+__device__ __forceinline__ int steps_of(const ChunkArgs &a, const Seq &s, int t) {
+  const int last = min((t + 1) * kTileRows, s.rows) - 1;
+  const int64_t see = min(s.pos0 + last / a.p.rg, (int64_t)s.len - 1) + 1;
+  return see < 1 ? 1 : (int)((see + kStep - 1) / kStep);
+}
+
+struct Item {
+  int b, h, t;     // sequence, KV head, tile
+  int j0, j1;      // steps [j0, j1) of it
+  int steps;       // of the whole tile
+  int64_t x_tile;  // first unit of the tile
+};
+
+// Walks the items of a block's range; the same for every role.
+struct Walk {
+  int b, h, t, off;
+  int64_t x, x1;
+  int tiles;
+  Seq s;
+  __device__ __forceinline__ bool next(const ChunkArgs &a, Item &it) {
+    if (x >= x1) return false;
+    while (t >= tiles) {
+      t = 0;
+      if (tiles > 0 && ++h < a.p.H) break;
+      h = 0;
+      do {
+        ++b;
+        s = seq_of(a, b);
+      } while (s.rows == 0);
+      tiles = (s.rows + kTileRows - 1) / kTileRows;
+    }
+    it.b = b, it.h = h, it.t = t;
+    it.steps = steps_of(a, s, t);
+    const int cost = it.steps + kOver;
+    const int n = (int)min((int64_t)(cost - off), x1 - x);
+    it.x_tile = x - off;
+    it.j0 = off > kOver ? off - kOver : 0;
+    it.j1 = off + n - kOver;
+    x += n;
+    off = 0;
+    ++t;
+    return true;
+  }
+};
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
+  using C = ChunkCfg<D>;
+  constexpr int RB = D * BITS / 8, SB = 4 * D / kPagedGroup, NG = D / kPagedGroup;
+  constexpr int AB = 2 * kAtom * (RB + SB);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t smem_s = smem_u32(smem);
+  const Paged &p = a.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // barriers
+  const uint32_t bars = smem_s + C::off_bar;
+  auto bar_q = [&](int i) { return bars + 8u * i; };             // queries of tile i are in
+  auto bar_s = [&](int i) { return bars + 8u * (2 + i); };       // scores of tile i are in
+  auto bar_p = [&](int i) { return bars + 8u * (4 + i); };       // weights of tile i are in
+  auto bar_o = [&](int i) { return bars + 8u * (6 + i); };       // output of tile i added
+  auto bar_kf = [&](int s) { return bars + 8u * (8 + s); };      // key stage full / empty
+  auto bar_ke = [&](int s) { return bars + 8u * (10 + s); };
+  auto bar_vf = [&](int s) { return bars + 8u * (12 + s); };
+  auto bar_ve = [&](int s) { return bars + 8u * (14 + s); };
+  const uint32_t bar_end = bars + 8u * 16;                       // everything issued is done
+  auto bar_g = [&](int i) { return bars + 8u * (17 + i); };      // the 128 threads of tile i
+  uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::off_misc);
+  volatile uint32_t *dead = misc + 1;
+  int64_t *prefix = reinterpret_cast<int64_t *>(smem + C::off_prefix);
+  int64_t *sh_x = reinterpret_cast<int64_t *>(misc + 4);  // borders of the block's range
+  int *sh_at = reinterpret_cast<int *>(misc + 8);         // b, h, t, off of its first unit
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 2 + i, 1);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 4 + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 6 + i, 1);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 8 + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 10 + i, 1);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 12 + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 14 + i, 1);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 17 + i, 128);
+    }
+    bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 16, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    misc[1] = 0;
+    prefix[0] = 0;
+  }
+
+  // ---- prefix[b + 1]: units of one head of sequences 0 .. b
+  for (int b = warp; b < p.B; b += kChunkThreads / 32) {
+    const Seq s = seq_of(a, b);
+    if (lane == 0 && blockIdx.x == 0) {
+      if (s.tokens > p.max_tokens || s.row0 < 0 || p.cu[b + 1] > p.T) paged_error(p, KVQ_EINVAL);
+      if (s.rows > 0 && p.lens[b] > p.width * p.page) paged_error(p, KVQ_EPAGE);
+    }
+    const int tiles = (s.rows + kTileRows - 1) / kTileRows;
+    int64_t sum = 0;
+    for (int t = lane; t < tiles; t += 32) sum += steps_of(a, s, t) + kOver;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) prefix[b + 1] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {  // running sums, 32 sequences at a time
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      int64_t v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += up;
+      }
+      v += before;
+      if (b0 + lane < p.B) prefix[b0 + lane + 1] = v;
+      before = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+  const int64_t total = p.H * prefix[p.B];
+  const int64_t U = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kMinUnits);
+  // ---- the block's borders: warp 0 its first unit, warp 1 the next block's.
+  // A border inside a tile's first units moves to its start, one at its last
+  // step to its end, so every item has steps of its own.
+  if (warp < 2) {
+    int64_t x = (blockIdx.x + warp) * U;
+    int b = 0, h = 0, t = 0, off = 0;
+    if (x >= total) {
+      x = total;
+    } else {
+      int lo = 0, hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.H * prefix[mid] <= x) lo = mid; else hi = mid;
+      }
+      b = lo;
+      const Seq s = seq_of(a, b);
+      const int64_t per = prefix[b + 1] - prefix[b], r = x - p.H * prefix[b];
+      h = (int)(r / per);
+      int64_t y = r - h * per;  // unit inside the head
+      const int tiles = (s.rows + kTileRows - 1) / kTileRows;
+      for (int t0 = 0;; t0 += 32) {
+        int64_t cost = t0 + lane < tiles ? steps_of(a, s, t0 + lane) + kOver : 0, run = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += up;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, run > y);
+        if (hit) {
+          const int w = __ffs(hit) - 1;
+          t = t0 + w;
+          const int64_t end = __shfl_sync(0xffffffffu, run, w);
+          cost = __shfl_sync(0xffffffffu, cost, w);
+          off = (int)(y - (end - cost));
+          if (off <= kOver + 1) {
+            x -= off;
+            off = 0;
+          } else if (cost - off <= 1) {
+            x += cost - off;
+            ++t;
+            off = 0;
+          }
+          break;
+        }
+        y -= __shfl_sync(0xffffffffu, run, 31);
+        if (t0 + 32 >= tiles) break;  // (not reached: y is inside the head)
+      }
+    }
+    if (lane == 0) {
+      sh_x[warp] = x;
+      if (warp == 0) sh_at[0] = b, sh_at[1] = h, sh_at[2] = t, sh_at[3] = off;
+    }
+  }
+  __syncthreads();
+  const int64_t x0 = sh_x[0], x1 = sh_x[1];
+  if (x0 >= x1) return;
+
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_s + C::off_misc)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  auto tm_s = [&](int i) { return tmem + 128u * i; };
+  auto tm_o = [&](int i) { return tmem + 256u + 128u * i; };
+
+  Walk walk;
+  walk.b = sh_at[0], walk.h = sh_at[1], walk.t = sh_at[2], walk.off = sh_at[3];
+  walk.x = x0, walk.x1 = x1;
+  walk.s = seq_of(a, walk.b);
+  walk.tiles = (walk.s.rows + kTileRows - 1) / kTileRows;
+
+  // Bounded waits: one that runs out records KVQ_ETIMEOUT and ends every role.
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (bar_poll(bar, parity)) return true;
+    for (int i = 0; i < kChunkWait; ++i) {
+      if (bar_poll(bar, parity)) return true;
+      if (*dead) return false;
+    }
+    *dead = 1;
+    paged_error(p, KVQ_ETIMEOUT);
+    return false;
+  };
+  // the same for a whole warp, with one answer (tcgen05.ld / st need it whole)
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+    return (bool)__all_sync(0xffffffffu, wait(bar, parity));
+  };
+  if (a.stall_limit > 0 && tid == 0) {
+    bool ok = false;
+    for (int i = 0; i < a.stall_limit && !ok; ++i) ok = bar_poll(bar_end, 0);
+    if (!ok) {
+      *dead = 1;
+      paged_error(p, KVQ_ETIMEOUT);
+    }
+  }
+
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 12 && lane == 0) {
+      // ---- MMA issue
+      constexpr uint32_t kQK = mma_desc(kStep, false), kPV = mma_desc(D, true);
+      auto scores = [&](int i, int stage) {
+        const uint32_t qa = smem_s + C::off_q + i * C::kTile, ka = smem_s + C::off_k + stage * C::kTile;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          // 16 channels: 32 bytes inside a 128-byte row, 64 channels per subtile
+          const uint32_t o = (k / 4) * (kStep * 128) + (k % 4) * 32;
+          mma_ss(tm_s(i), smem_desc(qa + o, 16, 1024), smem_desc(ka + o, 16, 1024), kQK, k > 0);
+        }
+        tc_commit(bar_s(i));
+      };
+      auto outputs = [&](int i, int stage, bool first) {
+        const uint32_t va = smem_s + C::off_v + stage * C::kTile;
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k)
+          mma_ts(tm_o(i), tm_s(i) + 8 * k, smem_desc(va + k * 2048, kStep * 128, 1024), kPV,
+                 !(first && k == 0));
+        tc_commit(bar_o(i));
+      };
+      uint32_t kn = 0, vn = 0;          // key / value steps taken
+      uint32_t qn[2] = {}, pn[2] = {};  // query tiles, weight tiles
+      Item it;
+      bool ok = true;
+      while (ok && walk.next(a, it)) {
+        const int nt = walk.s.rows - it.t * kTileRows > 128 ? 2 : 1, n = it.j1 - it.j0;
+        for (int i = 0; i < nt && ok; ++i) ok = wait(bar_q(i), qn[i]++ & 1);
+        ok = ok && wait(bar_kf(kn & 1), kn >> 1 & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = 0; i < nt; ++i) scores(i, kn & 1);
+        tc_commit(bar_ke(kn & 1));
+        ++kn;
+        for (int j = 0; j < n && ok; ++j) {
+          for (int i = 0; i < nt && ok; ++i) {
+            if (i == 0) ok = wait(bar_vf(vn & 1), vn >> 1 & 1);
+            ok = ok && wait(bar_p(i), pn[i]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            outputs(i, vn & 1, j == 0);
+            if (i == nt - 1) tc_commit(bar_ve(vn & 1));
+            if (j + 1 < n) {
+              if (i == 0) ok = wait(bar_kf(kn & 1), kn >> 1 & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(i, kn & 1);
+              if (i == nt - 1) tc_commit(bar_ke(kn & 1));
+            }
+          }
+          ++vn;
+          if (j + 1 < n) ++kn;
+        }
+      }
+      // whatever was issued ends before tensor memory is freed
+      tc_commit(bar_end);
+      bool done = false;
+      for (int i = 0; i < kChunkWait && !done; ++i) done = bar_poll(bar_end, 0);
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    // ---- producers: thread (quarter jq, token t8 of eight), four tokens a step
+    constexpr int QW = RB / 16;        // words of a quarter row
+    constexpr int kUnits = 4;
+    const int pw = warp - 8, t8 = lane & 7, jq = lane >> 3;
+    const int apage_log = __ffs(p.page / kAtom) - 1;
+    uint32_t kraw[kUnits][QW], kst[kUnits][NG], vraw[kUnits][QW], vst[kUnits][NG];
+    int id[kUnits];
+    // three walks: page numbers two steps ahead, codes one step ahead
+    struct Cursor {
+      int b, h, j, len;
+      bool on;
+    };
+    Item it;
+    Cursor far = {};
+    int far_j1 = 0;
+    auto far_next = [&]() {
+      if (far.on && far.j + 1 < far_j1) {
+        ++far.j;
+        return;
+      }
+      far.on = walk.next(a, it);
+      if (far.on) {
+        far.b = it.b, far.h = it.h, far.j = it.j0, far.len = walk.s.len;
+        far_j1 = it.j1;
+      }
+    };
+    auto read_ids = [&]() {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int atom = far.j * (kStep / kAtom) + 2 * u + (pw >> 1);
+        id[u] = -2;  // behind the sequence
+        if (far.on && atom * kAtom < far.len)
+          id[u] = max(__ldg(p.table + far.b * p.width + (atom >> apage_log)), -1);
+      }
+    };
+    // codes and statistics of the keys (or values) of step c, pages `pid`
+    auto fetch = [&](const Cursor &c, const int (&pid)[kUnits], bool value,
+                     uint32_t (&raw)[kUnits][QW], uint32_t (&st)[kUnits][NG]) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int token = c.j * kStep + 32 * u + 8 * pw + t8;
+        const bool ok = pid[u] >= 0 && (int64_t)pid[u] < p.n_pages && token < c.len;
+        if (ok) {
+          const int row = token % kAtom;
+          const uint8_t *at = p.pages + pid[u] * p.page_bytes + c.h * p.head_bytes +
+                              (int64_t)((token / kAtom) & ((1 << apage_log) - 1)) * AB;
+          const uint8_t *src = at + (value ? kAtom * RB : 0) + row * RB + jq * (RB / 4);
+          if constexpr (QW % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < QW; i += 4) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 4 * i));
+              raw[u][i] = v.x, raw[u][i + 1] = v.y, raw[u][i + 2] = v.z, raw[u][i + 3] = v.w;
+            }
+          } else if constexpr (QW == 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+            raw[u][0] = v.x, raw[u][1] = v.y;
+          } else {
+            raw[u][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+          }
+          const uint8_t *ss = at + 2 * kAtom * RB + (value ? kAtom * SB : 0) + row * SB;
+          if constexpr (NG == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(ss));
+            st[u][0] = v.x, st[u][1] = v.y, st[u][2 % NG] = v.z, st[u][3 % NG] = v.w;
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(ss));
+            st[u][0] = v.x, st[u][1] = v.y;
+          }
+        } else {
+          // zeros: nothing there may reach an output
+#pragma unroll
+          for (int i = 0; i < QW; ++i) raw[u][i] = 0;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) st[u][i] = 0;
+        }
+      }
+    };
+    auto store_keys = [&](uint32_t tile) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int row = 32 * u + 8 * pw + t8;
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+          const uint32_t sel = G & 1 ? 0x3232u : 0x1010u;
+          const uint32_t s = __byte_perm(kst[u][G / 2], 0, sel);
+          const uint32_t z = __byte_perm(kst[u][NG / 2 + G / 2], 0, sel);
+          uint32_t x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int bit = (4 * G + i) * BITS, w = bit / 16, off = bit % 16;
+            x[i] = hfma2(code_pair<BITS>(off & 8 ? kraw[u][w] >> 8 : kraw[u][w], off & 7), s, z);
+          }
+          // channels 32G + 8jq .. + 7
+          const int unit = (G & 1) * 4 + jq;
+          const uint32_t at = tile + (G / 2) * (kStep * 128) + row * 128 + ((unit ^ t8) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]),
+                       "r"(x[2]), "r"(x[3])
+                       : "memory");
+        }
+      }
+    };
+    auto store_values = [&](uint32_t tile) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int row = 32 * u + 8 * pw + t8;
+#pragma unroll
+        for (int e8 = 0; e8 < 2; ++e8) {  // eighths 2jq, 2jq + 1
+#pragma unroll
+          for (int h = 0; h < NG / 2; ++h) {
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w;
+              int off;
+              if (RB / 8 == 2) {  // two bytes an eighth: spread them over two halves
+                w = __byte_perm(vraw[u][0], 0, e8 ? 0x4342u : 0x4140u);
+                off = i * BITS;
+              } else {
+                const int bit = (4 * h + i) * BITS;
+                w = vraw[u][(e8 * (RB / 8) / 4 + bit / 16) % QW];
+                off = bit % 16;
+              }
+              x[i] = hfma2(code_pair<BITS>(off & 8 ? w >> 8 : w, off & 7), vst[u][h],
+                           vst[u][NG / 2 + h]);
+            }
+            // columns ((eighth * NG/2 + h) * 4 + i) * 2 + e hold channel
+            // 32 * (2h + e) + 4 * eighth + i
+            const int unit = (2 * jq + e8) * (NG / 2) + h;
+            const uint32_t at =
+                tile + (unit >> 3) * (kStep * 128) + row * 128 + (((unit & 7) ^ t8) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]),
+                         "r"(x[1]), "r"(x[2]), "r"(x[3])
+                         : "memory");
+          }
+        }
+      }
+    };
+    // prime: ids of the first step, its codes, ids of the second
+    Cursor nxt;
+    int pid[kUnits];
+    far_next();
+    read_ids();
+    nxt = far;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) pid[u] = id[u];
+    fetch(nxt, pid, false, kraw, kst);
+    fetch(nxt, pid, true, vraw, vst);
+    uint32_t bad = 0;
+    auto bad_of = [&]() {
+      bad = 0;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        if (pid[u] != -2 && (pid[u] < 0 || (int64_t)pid[u] >= p.n_pages)) bad |= 1u << u;
+    };
+    far_next();
+    read_ids();
+    uint32_t n = 0;
+    while (nxt.on) {
+      bad_of();
+      if (bad && lane == 0) paged_error(p, KVQ_EPAGE);
+      nxt = far;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) pid[u] = id[u];
+      const int stage = n & 1;
+      // (a stage's first use waits for nothing)
+      if (n >= 2 && !wait_warp(bar_ke(stage), ((n >> 1) - 1) & 1)) break;
+      if (lane == 0 && !(pw & 1)) {
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+          smem[C::off_bad + (n & 3) * 8 + 2 * u + (pw >> 1)] = bad >> u & 1;
+      }
+      store_keys(smem_s + C::off_k + stage * C::kTile);
+      async_fence();
+      bar_arrive(bar_kf(stage));
+      if (nxt.on) fetch(nxt, pid, false, kraw, kst);
+      if (n >= 2 && !wait_warp(bar_ve(stage), ((n >> 1) - 1) & 1)) break;
+      store_values(smem_s + C::off_v + stage * C::kTile);
+      async_fence();
+      bar_arrive(bar_vf(stage));
+      if (nxt.on) {
+        fetch(nxt, pid, true, vraw, vst);
+        far_next();
+        read_ids();
+      }
+      ++n;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // ---- softmax and output: one thread per row
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = (uint32_t)(warp & 3) * 32u << 16;
+    const uint32_t ts = tm_s(i) + lane_base, to = tm_o(i) + lane_base;
+    float *fs = reinterpret_cast<float *>(smem + C::off_f) + i * 128;
+    uint32_t sn = 0, step = 0;  // score tiles taken; steps of the block (for the bad-page bytes)
+    uint32_t gn = 0;            // meetings of the tile's threads
+    Item it;
+    bool ok = true;
+    while (ok && walk.next(a, it)) {
+      const Seq s = walk.s;
+      const int n = it.j1 - it.j0;
+      const int row_first = it.t * kTileRows + i * 128;
+      if (row_first >= s.rows) {  // one tile only
+        step += n;
+        continue;
+      }
+      // queries: 16 lanes (d = 128) or 8 to a row; scaled so that the row's
+      // largest is in [2^8, 2^9), which bf16 queries need to fit fp16
+      {
+        constexpr int LR = D / 8;
+        const int l = lane % LR;
+#pragma unroll 4
+        for (int k = 0; k < LR; ++k) {
+          const int rr = (warp & 3) * 32 + k * (32 / LR) + lane / LR, row = row_first + rr;
+          const bool in = row < s.rows;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (in)
+            w = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.row0 + row / p.rg) * a.qs +
+                                                      (int64_t)(it.h * p.rg + row % p.rg) * D) +
+                      l);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          float f[8], big = 0.0f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (p.bf16) {
+              f[2 * c] = __uint_as_float(ww[c] << 16);
+              f[2 * c + 1] = __uint_as_float(ww[c] & 0xffff0000u);
+            } else {
+              const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&ww[c]));
+              f[2 * c] = v.x;
+              f[2 * c + 1] = v.y;
+            }
+            big = fmaxf(big, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
+          }
+#pragma unroll
+          for (int o = 1; o < LR; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          int ex = ((__float_as_int(big) >> 23) & 255) - 127;
+          ex = big == 0.0f ? 0 : max(min(ex, 90), -90);
+          const float mul = a.sign * __int_as_float((127 + 8 - ex) << 23);
+          uint32_t o4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            o4[c] = h2u(__floats2half2_rn(f[2 * c] * mul, f[2 * c + 1] * mul));
+          const uint32_t at = smem_s + C::off_q + i * C::kTile + (l >> 3) * (kStep * 128) +
+                              rr * 128 + (((l & 7) ^ (rr & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o4[0]),
+                       "r"(o4[1]), "r"(o4[2]), "r"(o4[3])
+                       : "memory");
+          // (never 0: a hidden column's -inf stays -inf)
+          if (l == 0)
+            fs[rr] = fmaxf(a.scale_log2 * __int_as_float((127 + ex - 8) << 23), 1e-30f);
+        }
+        async_fence();
+        __syncwarp();
+      }
+      const float F = fs[r];  // (rows of this warp: written by this warp)
+      tc_fence_before();
+      bar_arrive(bar_q(i));
+
+      const int row = row_first + r;
+      const bool in = row < s.rows;
+      const int limit = in ? (int)min(s.pos0 + row / p.rg, (int64_t)s.len - 1) : -1;
+      // newest position every row of the tile sees (its first row's)
+      const int least = (int)min(s.pos0 + row_first / p.rg, (int64_t)s.len - 1);
+      float ref = kNoRef, l = 0.0f;
+      for (int j = it.j0; j < it.j1; ++j, ++step) {
+        if (!(ok = wait_warp(bar_s(i), sn & 1))) break;
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc_ld32(ts + 32 * c, x + 32 * c);
+        tc_wait_ld();
+        uint2 bad;  // a byte per 16 tokens
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(bad.x), "=r"(bad.y)
+                     : "r"(smem_s + C::off_bad + (step & 3) * 8)
+                     : "memory");
+        if (j * kStep + kStep - 1 > least || !in) {
+          const int seen = limit - j * kStep;  // columns 0 .. seen
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > seen) x[c] = 0xff800000u;
+        }
+        if (bad.x | bad.y) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if ((c < 64 ? bad.x : bad.y) >> (c / 16 % 4 * 8) & 1) x[c] = 0xff800000u;
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          m0 = fmaxf(m0, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+          m1 = fmaxf(m1, fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])));
+          m2 = fmaxf(m2, fmaxf(__uint_as_float(x[c + 4]), __uint_as_float(x[c + 5])));
+          m3 = fmaxf(m3, fmaxf(__uint_as_float(x[c + 6]), __uint_as_float(x[c + 7])));
+        }
+        float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+        // (a row without visible columns keeps kNoRef)
+        top = top == -INFINITY ? kNoRef : top * F;
+        const bool move = top > ref + (ref == kNoRef ? 0.0f : kChunkSlack);
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move ? exp2_approx(ref - top) : 1.0f;
+          if (move) ref = top, l *= f;
+          if (j > it.j0) {
+            // the sum of the earlier steps has to be complete
+            if (!(ok = wait_warp(bar_o(i), (sn - 1) & 1))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t y[32];
+              tc_ld32(to + c, y);
+              tc_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+              tc_st32(to + c, y);
+            }
+          }
+        }
+        float s0 = 0, s1 = 0, s2 = 0, s3 = 0;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+          const float p0 = exp2_approx(fmaf(__uint_as_float(x[c]), F, -ref));
+          const float p1 = exp2_approx(fmaf(__uint_as_float(x[c + 1]), F, -ref));
+          const float p2 = exp2_approx(fmaf(__uint_as_float(x[c + 2]), F, -ref));
+          const float p3 = exp2_approx(fmaf(__uint_as_float(x[c + 3]), F, -ref));
+          s0 += p0, s1 += p1, s2 += p2, s3 += p3;
+          x[c / 2] = h2u(__floats2half2_rn(p0, p1));
+          x[c / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+        }
+        l += (s0 + s1) + (s2 + s3);
+        tc_st32(ts, x);
+        tc_st32(ts + 32, x + 32);
+        tc_wait_st();
+        tc_fence_before();
+        bar_arrive(bar_p(i));
+        ++sn;
+      }
+      if (!ok) break;
+
+      // ---- output of the tile's steps [j0, j1)
+      if (!(ok = wait_warp(bar_o(i), (sn - 1) & 1))) break;
+      tc_fence_after();
+      const bool whole = it.j0 == 0 && it.j1 == it.steps;
+      const int64_t t = s.row0 + (in ? row / p.rg : 0);
+      uint16_t *dst = a.out + (t * p.Hq + it.h * p.rg + row % p.rg) * D;
+      // 32 columns of the output row, scaled, to their channels
+      auto put = [&](int c32, const float (&v)[32], float inv) {
+#pragma unroll
+        for (int G = 0; G < NG; ++G) {
+          // column ((g * NG/2 + h) * 4 + i) * 2 + e, channel 32 * (2h + e) + 4 * g + i
+          constexpr int kG = 16 / NG * 2;   // channels of one group in 32 columns
+          uint32_t w[kG / 2];
+#pragma unroll
+          for (int c = 0; c < kG; c += 2) {
+            const int n0 = ((c / 4 * (NG / 2) + G / 2) * 4 + c % 4) * 2 + (G & 1);
+            if (p.bf16) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(v[n0] * inv, v[n0 + 2] * inv);
+              w[c / 2] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+              w[c / 2] = h2u(__floats2half2_rn(v[n0] * inv, v[n0 + 2] * inv));
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < kG / 2; c += 4)
+            *reinterpret_cast<uint4 *>(dst + 32 * G + c32 / 32 * kG + 2 * c) =
+                make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+        }
+      };
+      if (whole) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t y[32];
+          __syncwarp();
+          tc_ld32(to + c, y);
+          tc_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(y[k]);
+          if (in) put(c, v, inv);
+        }
+      } else {
+        const int64_t e = it.x_tile + it.steps + kOver;
+        int c0 = (int)(it.x_tile / U);
+        if ((c0 + 1) * U - it.x_tile <= kOver + 1) ++c0;
+        int c1 = (int)((e - 1) / U);
+        if (e - c1 * U <= 1) --c1;
+        const int slot = 2 * blockIdx.x + (it.j0 == 0 ? 1 : 0);
+        float4 *wo = reinterpret_cast<float4 *>(a.ws_o) + (int64_t)(slot * 2 + i) * (D / 4) * 128 + r;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t y[32];
+          __syncwarp();
+          tc_ld32(to + c, y);
+          tc_wait_ld();
+          if (in) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              wo[(c + k) / 4 * 128] = make_float4(__uint_as_float(y[k]), __uint_as_float(y[k + 1]),
+                                                  __uint_as_float(y[k + 2]),
+                                                  __uint_as_float(y[k + 3]));
+          }
+        }
+        float2 *wm = reinterpret_cast<float2 *>(a.ws_ml) + (slot * 2 + i) * 128 + r;
+        *wm = make_float2(ref, l);
+        __threadfence();
+        bar_arrive(bar_g(i));
+        if (!(ok = wait_warp(bar_g(i), gn++ & 1))) break;
+        volatile uint32_t *flag = misc + 12 + i;
+        if (r == 0) {
+          int *count = a.ws_count + c0 * 2 + i;
+          const int last = atomicAdd(count, 1) == c1 - c0;
+          if (last) *count = 0;
+          *flag = last;
+        }
+        bar_arrive(bar_g(i));
+        if (!(ok = wait_warp(bar_g(i), gn++ & 1))) break;
+        if (*flag) {
+          __threadfence();
+          const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml);
+          float m = kNoRef, sum = 0.0f;
+          for (int c = c0; c <= c1; ++c)
+            m = fmaxf(m, __ldcg(ml + ((2 * c + (c == c0)) * 2 + i) * 128 + r).x);
+          for (int c = c0; c <= c1; ++c) {
+            const float2 y = __ldcg(ml + ((2 * c + (c == c0)) * 2 + i) * 128 + r);
+            sum += y.y * exp2_approx(y.x - m);
+          }
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          if (in) {
+#pragma unroll 1
+            for (int c32 = 0; c32 < D; c32 += 32) {
+              float v[32] = {};
+#pragma unroll 1
+              for (int c = c0; c <= c1; ++c) {
+                const int at = (2 * c + (c == c0)) * 2 + i;
+                const float2 y = __ldcg(ml + at * 128 + r);
+                // (a part without weight left nothing that counts)
+                const float f = y.y == 0.0f ? 0.0f : exp2_approx(y.x - m);
+                if (f == 0.0f) continue;
+                const float4 *src = reinterpret_cast<const float4 *>(a.ws_o) +
+                                    (int64_t)at * (D / 4) * 128 + c32 / 4 * 128 + r;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float4 w = __ldcg(src + k * 128);
+                  v[4 * k] += f * w.x;
+                  v[4 * k + 1] += f * w.y;
+                  v[4 * k + 2] += f * w.z;
+                  v[4 * k + 3] += f * w.w;
+                }
+              }
+              put(c32, v, inv);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+template <int D, int BITS>
+cudaError_t chunk_as(const ChunkArgs &a, int num_sms, cudaStream_t st) {
+  static KernelSetup setup;
+  const int smem = ChunkCfg<D>::smem(a.p.B);
+  auto kern = paged_chunk_kernel<D, BITS>;
+  const cudaError_t e = kernel_setup(setup, kern, kChunkThreads, smem, nullptr);
+  if (e != cudaSuccess) return e;
+  const int blocks = num_sms < kMaxChunkBlocks ? num_sms : kMaxChunkBlocks;
+  kern<<<blocks, kChunkThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+constexpr size_t kCountBytes = 2 * kMaxChunkBlocks * 4;
+constexpr size_t kMlBytes = (size_t)2 * kMaxChunkBlocks * kTileRows * 8;
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *out, float scale,
+                               int few, void *ws, int num_sms, cudaStream_t st) {
+  ChunkArgs a;
+  a.p = p;
+  a.q = static_cast<const uint16_t *>(q);
+  a.qs = qs;
+  a.out = static_cast<uint16_t *>(out);
+  a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+  a.sign = scale < 0.0f ? -1.0f : 1.0f;
+  a.few = few;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  a.ws_count = reinterpret_cast<int *>(w);
+  a.ws_ml = reinterpret_cast<float *>(w + kCountBytes);
+  a.ws_o = reinterpret_cast<float *>(w + kCountBytes + kMlBytes);
+  a.stall_limit = debug_stall_limit();
+  if (p.d == 128)
+    return p.bits == 2   ? chunk_as<128, 2>(a, num_sms, st)
+           : p.bits == 4 ? chunk_as<128, 4>(a, num_sms, st)
+                         : chunk_as<128, 8>(a, num_sms, st);
+  return p.bits == 2   ? chunk_as<64, 2>(a, num_sms, st)
+         : p.bits == 4 ? chunk_as<64, 4>(a, num_sms, st)
+                       : chunk_as<64, 8>(a, num_sms, st);
+}
+
+size_t paged_chunk_workspace() {
+  return kCountBytes + kMlBytes + (size_t)2 * kMaxChunkBlocks * kTileRows * kMaxHeadDim * 4;
+}
+
+}  // namespace kvq

@@ -53,6 +53,7 @@ struct RowsArgs {
   float *ws_o;     // [2 * blocks][rows][d]
   int *ws_count;   // [blocks], zero between calls
   int min_units, snap;
+  int few;         // sequences with more rows are not this kernel's
   int stall_limit;
 };
 
@@ -174,7 +175,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       int64_t atoms = 0;
       if (n > p.max_tokens || p.cu[b] < 0 || p.cu[b + 1] > p.T) {
         if (blockIdx.x == 0) paged_error(p, KVQ_EINVAL);
-      } else if (n > 0 && (int64_t)n * p.rg <= kPagedFewRows) {
+      } else if (n > 0 && (int64_t)n * p.rg <= a.few) {
         const int64_t cap = p.width * p.page, len = p.lens[b];
         if (len > cap && blockIdx.x == 0) paged_error(p, KVQ_EPAGE);
         atoms = (min(len, cap) + kAtom - 1) / kAtom;
@@ -601,7 +602,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       if (border(prefix, p.B, H, total, U, a.snap, c_last) >= pair1) --c_last;
     }
     auto store = [&](int r, int quad, float4 v, float sum) {
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       uint2 w2;
       if (p.bf16) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
@@ -705,7 +706,7 @@ cudaError_t launch_as(RowsArgs &a, int num_sms, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                              void *ws, int num_sms, cudaStream_t st) {
+                              int few, void *ws, int num_sms, cudaStream_t st) {
   RowsArgs a;
   a.p = p;
   a.q = static_cast<const uint16_t *>(q);
@@ -720,7 +721,8 @@ cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *o
   a.min_units = 32;
   a.snap = 8;
   a.stall_limit = debug_stall_limit();
-  const int64_t most = (int64_t)p.max_tokens * p.rg;
+  a.few = few;
+  const int64_t most = few;
   // one tile of 8 rows when no sequence has more, two otherwise
   if (p.d == 128) {
     if (most <= 8)
