@@ -12,14 +12,15 @@
 // rescaled a few times per row at most, by the row's own thread.
 //
 // Bound: 4*128*256*d operations per step on the tensor core against 128*256
-// exponentials and the dequantization of 128 keys and values: four producer
+// exponentials and the dequantization of 128 keys and values: eight producer
 // warps read codes and statistics into registers one step ahead, turn codes
 // into fp16 (1024 + code by one LOP3, the code by one HFMA2, code * scale +
 // zero by a second: exact but for one rounding) and store the swizzled operand
 // tiles, which both query tiles use.
 //
 //   warps 0-3, 4-7: softmax and output of query tiles 0 and 1
-//   warps 8-11: producers    warp 12: MMA issue (one thread)
+//   warps 8-15: producers    warp 16: MMA issue    warp 17: the list of items
+//   (warps 18, 19 only give up registers)
 //
 // Split: every (sequence, head, 256-row tile) is a list of its visible 128-token
 // steps plus kOver for its start and end; the concatenated list is cut into
@@ -34,13 +35,17 @@ int debug_stall_limit();
 
 namespace {
 
-constexpr int kChunkThreads = 512;
+constexpr int kChunkThreads = 640;
+// registers a thread: 640 * 96 at launch >= 256 * 120 + 256 * 80 + 128 * 64
+constexpr int kProducerWarp = 8, kMmaWarp = 16, kItemWarp = 17;
+constexpr int kItems = 4;  // items on their way to the roles
+constexpr int kPWarps = kMmaWarp - kProducerWarp;
 constexpr int kStep = 128;       // cached tokens per step
 constexpr int kTileRows = 256;   // query rows per block
 constexpr int kOver = 2;         // units of a tile's start and end
 constexpr int kMinUnits = 8;
 constexpr int kMaxChunkBlocks = 160;
-constexpr int kChunkWait = 1 << 22;
+constexpr int kChunkWait = 1 << 17;  // times 32 polls
 constexpr float kChunkSlack = 8.0f;
 constexpr float kNoRef = -1e30f;
 
@@ -67,13 +72,19 @@ struct ChunkCfg {
   static constexpr int off_f = off_v + 2 * kTile;          // float [256] row factors
   static constexpr int off_bad = off_f + kTileRows * 4;    // bytes [4][8]: atoms without a page
   static constexpr int off_bar = off_bad + 32;
-  static constexpr int kBars = 19;
-  static constexpr int off_misc = off_bar + kBars * 8;     // tensor memory base, dead flag, flags
+  static constexpr int kBars = 19 + 2 * kItems;
+  static constexpr int off_item = (off_bar + kBars * 8 + 15) / 16 * 16;
+  static constexpr int off_misc = off_item + kItems * 64;  // tensor memory base, dead flag, flags
   static constexpr int off_prefix = off_misc + 64;
   static constexpr int smem(int seqs) { return off_prefix + (seqs + 1) * 8 + 1024; }
 };
 
 // ---- PTX ------------------------------------------------------------------
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -90,15 +101,21 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+// One arrival for the warp, after every lane's earlier work.
+__device__ __forceinline__ void bar_arrive_warp(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// A poll that suspends the thread for a microsecond at most.
-__device__ __forceinline__ bool bar_poll(uint32_t bar, uint32_t parity) {
+// Up to 32 polls in a loop of four instructions: the waiting warps share their
+// schedulers with the working ones.
+__device__ __forceinline__ bool bar_try_32(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 32;\n"
+      "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
+      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
@@ -121,20 +138,33 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t *r) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31, %32};" ::"r"(addr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
 
-// Shared-memory matrix descriptor: 128-byte swizzle, strides in bytes.
+// Shared-memory matrix descriptor: 128-byte swizzle, strides in bytes.  Adding
+// n to it moves the address by 16 * n bytes.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
   return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 |
          (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
@@ -163,6 +193,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __host__ __device__ constexpr uint32_t dup16(uint32_t h) { return h | h << 16; }
@@ -206,44 +241,18 @@ __device__ __forceinline__ int steps_of(const ChunkArgs &a, const Seq &s, int t)
   return see < 1 ? 1 : (int)((see + kStep - 1) / kStep);
 }
 
-struct Item {
-  int b, h, t;     // sequence, KV head, tile
-  int j0, j1;      // steps [j0, j1) of it
-  int steps;       // of the whole tile
-  int64_t x_tile;  // first unit of the tile
+// One block's share of one tile, as the roles read it from shared memory.
+struct __align__(16) Item {
+  int b, h;             // sequence (-1: no more items), KV head
+  int j0, j1;           // steps [j0, j1) of the tile
+  int row0, row_first;  // the sequence's first packed row; the tile's first row in it
+  int rows, len;        // rows and visible length of the sequence
+  int64_t pos0;         // position of the sequence's first row
+  int steps;            // of the whole tile
+  int c0, c1;           // first and last block with a share
+  int pad[3];
 };
-
-// Walks the items of a block's range; the same for every role.
-struct Walk {
-  int b, h, t, off;
-  int64_t x, x1;
-  int tiles;
-  Seq s;
-  __device__ __forceinline__ bool next(const ChunkArgs &a, Item &it) {
-    if (x >= x1) return false;
-    while (t >= tiles) {
-      t = 0;
-      if (tiles > 0 && ++h < a.p.H) break;
-      h = 0;
-      do {
-        ++b;
-        s = seq_of(a, b);
-      } while (s.rows == 0);
-      tiles = (s.rows + kTileRows - 1) / kTileRows;
-    }
-    it.b = b, it.h = h, it.t = t;
-    it.steps = steps_of(a, s, t);
-    const int cost = it.steps + kOver;
-    const int n = (int)min((int64_t)(cost - off), x1 - x);
-    it.x_tile = x - off;
-    it.j0 = off > kOver ? off - kOver : 0;
-    it.j1 = off + n - kOver;
-    x += n;
-    off = 0;
-    ++t;
-    return true;
-  }
-};
+static_assert(sizeof(Item) == 64, "layout of the item ring");
 
 template <int D, int BITS>
 __global__ void __launch_bounds__(kChunkThreads, 1)
@@ -255,14 +264,15 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t smem_s = smem_u32(smem);
   const Paged &p = a.p;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (through a shuffle, so that the compiler knows it to be uniform)
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   // barriers
   const uint32_t bars = smem_s + C::off_bar;
   auto bar_q = [&](int i) { return bars + 8u * i; };             // queries of tile i are in
   auto bar_s = [&](int i) { return bars + 8u * (2 + i); };       // scores of tile i are in
   auto bar_p = [&](int i) { return bars + 8u * (4 + i); };       // weights of tile i are in
-  auto bar_o = [&](int i) { return bars + 8u * (6 + i); };       // output of tile i added
+  auto bar_o = [&](int i) { return bars + 8u * (6 + i); };       // output of tile i complete
   auto bar_kf = [&](int s) { return bars + 8u * (8 + s); };      // key stage full / empty
   auto bar_ke = [&](int s) { return bars + 8u * (10 + s); };
   auto bar_vf = [&](int s) { return bars + 8u * (12 + s); };
@@ -276,16 +286,20 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   int *sh_at = reinterpret_cast<int *>(misc + 8);         // b, h, t, off of its first unit
 
   if (tid == 0) {
+    for (int i = 0; i < kItems; ++i) {
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 19 + i, 1);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 19 + kItems + i, kMmaWarp + 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + i, 4);
       bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 2 + i, 1);
-      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 4 + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 4 + i, 4);
       bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 6 + i, 1);
-      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 8 + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 8 + i, kPWarps);
       bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 10 + i, 1);
-      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 12 + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 12 + i, kPWarps);
       bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 14 + i, 1);
-      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 17 + i, 128);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 17 + i, 4);
     }
     bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 16, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -382,7 +396,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   const int64_t x0 = sh_x[0], x1 = sh_x[1];
   if (x0 >= x1) return;
 
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_s + C::off_misc)
                  : "memory");
@@ -395,129 +409,208 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   auto tm_s = [&](int i) { return tmem + 128u * i; };
   auto tm_o = [&](int i) { return tmem + 256u + 128u * i; };
 
-  Walk walk;
-  walk.b = sh_at[0], walk.h = sh_at[1], walk.t = sh_at[2], walk.off = sh_at[3];
-  walk.x = x0, walk.x1 = x1;
-  walk.s = seq_of(a, walk.b);
-  walk.tiles = (walk.s.rows + kTileRows - 1) / kTileRows;
-
   // Bounded waits: one that runs out records KVQ_ETIMEOUT and ends every role.
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (bar_poll(bar, parity)) return true;
     for (int i = 0; i < kChunkWait; ++i) {
-      if (bar_poll(bar, parity)) return true;
+      if (bar_try_32(bar, parity)) return true;
       if (*dead) return false;
     }
     *dead = 1;
     paged_error(p, KVQ_ETIMEOUT);
     return false;
   };
+  // item n of the block (b < 0: there are no more, or a wait ran out), and its
+  // release once the warp has taken what it needs
+  const Item *items = reinterpret_cast<const Item *>(smem + C::off_item);
+  auto bar_if = [&](uint32_t n) { return bars + 8u * (19 + (n % kItems)); };
+  auto bar_ie = [&](uint32_t n) { return bars + 8u * (19 + kItems + (n % kItems)); };
   // the same for a whole warp, with one answer (tcgen05.ld / st need it whole)
   auto wait_warp = [&](uint32_t bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, wait(bar, parity));
   };
+  auto take_item = [&](uint32_t n) -> const Item * {
+    if (!wait_warp(bar_if(n), n / kItems & 1)) return nullptr;
+    const Item *it = items + n % kItems;
+    return it->b < 0 ? nullptr : it;
+  };
   if (a.stall_limit > 0 && tid == 0) {
     bool ok = false;
-    for (int i = 0; i < a.stall_limit && !ok; ++i) ok = bar_poll(bar_end, 0);
+    for (int i = 0; i < a.stall_limit && !ok; ++i) ok = bar_try_wait(bar_end, 0);
     if (!ok) {
       *dead = 1;
       paged_error(p, KVQ_ETIMEOUT);
     }
   }
 
-  if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 12 && lane == 0) {
-      // ---- MMA issue
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kMmaWarp) {
+      // ---- MMA issue: the whole warp keeps step, one lane issues
       constexpr uint32_t kQK = mma_desc(kStep, false), kPV = mma_desc(D, true);
-      auto scores = [&](int i, int stage) {
-        const uint32_t qa = smem_s + C::off_q + i * C::kTile, ka = smem_s + C::off_k + stage * C::kTile;
+      const uint64_t q_desc = smem_desc(smem_s + C::off_q, 16, 1024);
+      const uint64_t k_desc = smem_desc(smem_s + C::off_k, 16, 1024);
+      const uint64_t v_desc = smem_desc(smem_s + C::off_v, kStep * 128, 1024);
+      const bool leader = elect_one();
+      auto scores = [&](int i, uint32_t stage) {
+        if (leader) {
+          const uint64_t qd = q_desc + i * (C::kTile / 16), kd = k_desc + stage * (C::kTile / 16);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          // 16 channels: 32 bytes inside a 128-byte row, 64 channels per subtile
-          const uint32_t o = (k / 4) * (kStep * 128) + (k % 4) * 32;
-          mma_ss(tm_s(i), smem_desc(qa + o, 16, 1024), smem_desc(ka + o, 16, 1024), kQK, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            // 16 channels: 32 bytes inside a 128-byte row, 64 channels a subtile
+            const uint32_t o = ((k / 4) * (kStep * 128) + (k % 4) * 32) / 16;
+            mma_ss(tm_s(i), qd + o, kd + o, kQK, k > 0);
+          }
+          tc_commit(bar_s(i));
         }
-        tc_commit(bar_s(i));
+        __syncwarp();
       };
-      auto outputs = [&](int i, int stage, bool first) {
-        const uint32_t va = smem_s + C::off_v + stage * C::kTile;
+      auto outputs = [&](int i, uint32_t stage, bool first, bool last) {
+        if (leader) {
+          const uint64_t vd = v_desc + stage * (C::kTile / 16);
+          mma_ts(tm_o(i), tm_s(i), vd, kPV, !first);
 #pragma unroll
-        for (int k = 0; k < kStep / 16; ++k)
-          mma_ts(tm_o(i), tm_s(i) + 8 * k, smem_desc(va + k * 2048, kStep * 128, 1024), kPV,
-                 !(first && k == 0));
-        tc_commit(bar_o(i));
+          for (int k = 1; k < kStep / 16; ++k)
+            mma_ts(tm_o(i), tm_s(i) + 8 * k, vd + k * (2048 / 16), kPV, true);
+          if (last) tc_commit(bar_o(i));
+        }
+        __syncwarp();
       };
-      uint32_t kn = 0, vn = 0;          // key / value steps taken
-      uint32_t qn[2] = {}, pn[2] = {};  // query tiles, weight tiles
-      Item it;
+      auto commit = [&](uint32_t bar) {
+        if (leader) tc_commit(bar);
+        __syncwarp();
+      };
+      uint32_t kn = 0, vn = 0;  // key / value steps taken
+      uint32_t qn = 0, pn = 0;  // parities: bit i for tile i
       bool ok = true;
-      while (ok && walk.next(a, it)) {
-        const int nt = walk.s.rows - it.t * kTileRows > 128 ? 2 : 1, n = it.j1 - it.j0;
-        for (int i = 0; i < nt && ok; ++i) ok = wait(bar_q(i), qn[i]++ & 1);
-        ok = ok && wait(bar_kf(kn & 1), kn >> 1 & 1);
+      for (uint32_t in = 0; ok; ++in) {
+        const Item *it = take_item(in);
+        if (!it) break;
+        const bool two = __shfl_sync(0xffffffffu, it->rows - it->row_first, 0) > 128;
+        const int n = __shfl_sync(0xffffffffu, it->j1 - it->j0, 0);
+        bar_arrive_warp(bar_ie(in));
+        ok = wait_warp(bar_q(0), qn & 1);
+        if (ok && two) ok = wait_warp(bar_q(1), qn >> 1);
+        qn ^= two ? 3u : 1u;
+        ok = ok && wait_warp(bar_kf(kn & 1), kn >> 1 & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int i = 0; i < nt; ++i) scores(i, kn & 1);
-        tc_commit(bar_ke(kn & 1));
+        scores(0, kn & 1);
+        if (two) scores(1, kn & 1);
+        commit(bar_ke(kn & 1));
         ++kn;
-        for (int j = 0; j < n && ok; ++j) {
-          for (int i = 0; i < nt && ok; ++i) {
-            if (i == 0) ok = wait(bar_vf(vn & 1), vn >> 1 & 1);
-            ok = ok && wait(bar_p(i), pn[i]++ & 1);
-            if (!ok) break;
+        for (int j = 0; j < n; ++j, ++vn) {
+          const bool more = j + 1 < n;
+          ok = wait_warp(bar_vf(vn & 1), vn >> 1 & 1) && wait_warp(bar_p(0), pn & 1);
+          if (!ok) break;
+          tc_fence_after();
+          outputs(0, vn & 1, j == 0, !more);
+          if (!two) commit(bar_ve(vn & 1));
+          if (more) {
+            if (!(ok = wait_warp(bar_kf(kn & 1), kn >> 1 & 1))) break;
             tc_fence_after();
-            outputs(i, vn & 1, j == 0);
-            if (i == nt - 1) tc_commit(bar_ve(vn & 1));
-            if (j + 1 < n) {
-              if (i == 0) ok = wait(bar_kf(kn & 1), kn >> 1 & 1);
-              if (!ok) break;
-              tc_fence_after();
-              scores(i, kn & 1);
-              if (i == nt - 1) tc_commit(bar_ke(kn & 1));
-            }
+            scores(0, kn & 1);
           }
-          ++vn;
-          if (j + 1 < n) ++kn;
+          if (two) {
+            if (!(ok = wait_warp(bar_p(1), pn >> 1))) break;
+            tc_fence_after();
+            outputs(1, vn & 1, j == 0, !more);
+            commit(bar_ve(vn & 1));
+            if (more) scores(1, kn & 1);
+          }
+          pn ^= two ? 3u : 1u;
+          if (more) {
+            commit(bar_ke(kn & 1));
+            ++kn;
+          }
         }
       }
       // whatever was issued ends before tensor memory is freed
-      tc_commit(bar_end);
+      commit(bar_end);
       bool done = false;
-      for (int i = 0; i < kChunkWait && !done; ++i) done = bar_poll(bar_end, 0);
+      for (int i = 0; i < kChunkWait && !done; ++i) done = bar_try_32(bar_end, 0);
+      __syncwarp();
+    } else if (warp == kItemWarp) {
+      // ---- the items of [x0, x1), in turn
+      int b = sh_at[0], h = sh_at[1], t = sh_at[2], off = sh_at[3];
+      int64_t x = x0;
+      Seq s = seq_of(a, b);
+      int tiles = (s.rows + kTileRows - 1) / kTileRows;
+      for (uint32_t in = 0;; ++in) {
+        if (in >= kItems && !wait_warp(bar_ie(in), (in / kItems - 1) & 1)) break;
+        Item *it = const_cast<Item *>(items) + in % kItems;
+        if (x >= x1) {
+          if (lane == 0) it->b = -1;
+          bar_arrive_warp(bar_if(in));
+          break;
+        }
+        while (t >= tiles) {
+          t = 0;
+          if (tiles > 0 && ++h < p.H) break;
+          h = 0;
+          do {
+            ++b;
+            s = seq_of(a, b);
+          } while (s.rows == 0);
+          tiles = (s.rows + kTileRows - 1) / kTileRows;
+        }
+        const int steps = steps_of(a, s, t), cost = steps + kOver;
+        const int n = (int)min((int64_t)(cost - off), x1 - x);
+        const int64_t first = x - off, end = first + cost;
+        if (lane == 0) {
+          it->b = b, it->h = h;
+          it->j0 = off > kOver ? off - kOver : 0;
+          it->j1 = off + n - kOver;
+          it->row0 = s.row0, it->row_first = t * kTileRows;
+          it->rows = s.rows, it->len = s.len;
+          it->pos0 = s.pos0;
+          it->steps = steps;
+          // (the borders as they were moved, above)
+          int c0 = (int)(first / U), c1 = (int)((end - 1) / U);
+          if ((c0 + 1) * U - first <= kOver + 1) ++c0;
+          if (end - c1 * U <= 1) --c1;
+          it->c0 = c0, it->c1 = c1;
+        }
+        bar_arrive_warp(bar_if(in));
+        x += n;
+        off = 0;
+        ++t;
+      }
     }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
-    // ---- producers: thread (quarter jq, token t8 of eight), four tokens a step
+  } else if (warp >= kProducerWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ---- producers: thread (quarter jq, token t8 of eight), two tokens a step
     constexpr int QW = RB / 16;        // words of a quarter row
-    constexpr int kUnits = 4;
-    const int pw = warp - 8, t8 = lane & 7, jq = lane >> 3;
+    constexpr int kUnits = kStep / (8 * kPWarps);  // tokens of a thread
+    const int pw = warp - kProducerWarp, t8 = lane & 7, jq = lane >> 3;
     const int apage_log = __ffs(p.page / kAtom) - 1;
     uint32_t kraw[kUnits][QW], kst[kUnits][NG], vraw[kUnits][QW], vst[kUnits][NG];
     int id[kUnits];
-    // three walks: page numbers two steps ahead, codes one step ahead
+    // two cursors: page numbers are read two steps ahead, codes one
     struct Cursor {
       int b, h, j, len;
       bool on;
     };
-    Item it;
     Cursor far = {};
     int far_j1 = 0;
+    uint32_t in = 0;
     auto far_next = [&]() {
       if (far.on && far.j + 1 < far_j1) {
         ++far.j;
         return;
       }
-      far.on = walk.next(a, it);
+      const Item *it = take_item(in);
+      far.on = it != nullptr;
       if (far.on) {
-        far.b = it.b, far.h = it.h, far.j = it.j0, far.len = walk.s.len;
-        far_j1 = it.j1;
+        far.b = it->b, far.h = it->h, far.j = it->j0, far.len = it->len;
+        far_j1 = it->j1;
+        bar_arrive_warp(bar_ie(in));
+        ++in;
       }
     };
     auto read_ids = [&]() {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int atom = far.j * (kStep / kAtom) + 2 * u + (pw >> 1);
+        const int atom = far.j * (kStep / kAtom) + kPWarps / 2 * u + (pw >> 1);
         id[u] = -2;  // behind the sequence
         if (far.on && atom * kAtom < far.len)
           id[u] = max(__ldg(p.table + far.b * p.width + (atom >> apage_log)), -1);
@@ -528,7 +621,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
                      uint32_t (&raw)[kUnits][QW], uint32_t (&st)[kUnits][NG]) {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int token = c.j * kStep + 32 * u + 8 * pw + t8;
+        const int token = c.j * kStep + 8 * (kPWarps * u + pw) + t8;
         const bool ok = pid[u] >= 0 && (int64_t)pid[u] < p.n_pages && token < c.len;
         if (ok) {
           const int row = token % kAtom;
@@ -567,7 +660,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     auto store_keys = [&](uint32_t tile) {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int row = 32 * u + 8 * pw + t8;
+        const int row = 8 * (kPWarps * u + pw) + t8;
 #pragma unroll
         for (int G = 0; G < NG; ++G) {
           const uint32_t sel = G & 1 ? 0x3232u : 0x1010u;
@@ -591,7 +684,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     auto store_values = [&](uint32_t tile) {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int row = 32 * u + 8 * pw + t8;
+        const int row = 8 * (kPWarps * u + pw) + t8;
 #pragma unroll
         for (int e8 = 0; e8 < 2; ++e8) {  // eighths 2jq, 2jq + 1
 #pragma unroll
@@ -656,16 +749,16 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       if (lane == 0 && !(pw & 1)) {
 #pragma unroll
         for (int u = 0; u < kUnits; ++u)
-          smem[C::off_bad + (n & 3) * 8 + 2 * u + (pw >> 1)] = bad >> u & 1;
+          smem[C::off_bad + (n & 3) * 8 + kPWarps / 2 * u + (pw >> 1)] = bad >> u & 1;
       }
       store_keys(smem_s + C::off_k + stage * C::kTile);
       async_fence();
-      bar_arrive(bar_kf(stage));
+      bar_arrive_warp(bar_kf(stage));
       if (nxt.on) fetch(nxt, pid, false, kraw, kst);
       if (n >= 2 && !wait_warp(bar_ve(stage), ((n >> 1) - 1) & 1)) break;
       store_values(smem_s + C::off_v + stage * C::kTile);
       async_fence();
-      bar_arrive(bar_vf(stage));
+      bar_arrive_warp(bar_vf(stage));
       if (nxt.on) {
         fetch(nxt, pid, true, vraw, vst);
         far_next();
@@ -674,22 +767,23 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       ++n;
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ---- softmax and output: one thread per row
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lane_base = (uint32_t)(warp & 3) * 32u << 16;
     const uint32_t ts = tm_s(i) + lane_base, to = tm_o(i) + lane_base;
     float *fs = reinterpret_cast<float *>(smem + C::off_f) + i * 128;
     uint32_t sn = 0, step = 0;  // score tiles taken; steps of the block (for the bad-page bytes)
-    uint32_t gn = 0;            // meetings of the tile's threads
-    Item it;
+    uint32_t on = 0, gn = 0;    // tiles finished; meetings of the tile's threads
     bool ok = true;
-    while (ok && walk.next(a, it)) {
-      const Seq s = walk.s;
-      const int n = it.j1 - it.j0;
-      const int row_first = it.t * kTileRows + i * 128;
-      if (row_first >= s.rows) {  // one tile only
-        step += n;
+    for (uint32_t item = 0; ok; ++item) {
+      const Item *it = take_item(item);
+      if (!it) break;
+      const int row_first = it->row_first + i * 128, rows = it->rows;
+      const int j0 = it->j0, j1 = it->j1;
+      if (row_first >= rows) {  // one tile only
+        step += j1 - j0;
+        bar_arrive_warp(bar_ie(item));
         continue;
       }
       // queries: 16 lanes (d = 128) or 8 to a row; scaled so that the row's
@@ -700,11 +794,11 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
 #pragma unroll 4
         for (int k = 0; k < LR; ++k) {
           const int rr = (warp & 3) * 32 + k * (32 / LR) + lane / LR, row = row_first + rr;
-          const bool in = row < s.rows;
+          const bool in = row < rows;
           uint4 w = make_uint4(0, 0, 0, 0);
           if (in)
-            w = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.row0 + row / p.rg) * a.qs +
-                                                      (int64_t)(it.h * p.rg + row % p.rg) * D) +
+            w = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(it->row0 + row / p.rg) * a.qs +
+                                                      (int64_t)(it->h * p.rg + row % p.rg) * D) +
                       l);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
           float f[8], big = 0.0f;
@@ -743,94 +837,116 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       }
       const float F = fs[r];  // (rows of this warp: written by this warp)
       tc_fence_before();
-      bar_arrive(bar_q(i));
+      bar_arrive_warp(bar_q(i));
 
       const int row = row_first + r;
-      const bool in = row < s.rows;
-      const int limit = in ? (int)min(s.pos0 + row / p.rg, (int64_t)s.len - 1) : -1;
+      const bool in = row < rows;
+      const int limit = in ? (int)min(it->pos0 + row / p.rg, (int64_t)it->len - 1) : -1;
       // newest position every row of the tile sees (its first row's)
-      const int least = (int)min(s.pos0 + row_first / p.rg, (int64_t)s.len - 1);
+      const int least = (int)min(it->pos0 + row_first / p.rg, (int64_t)it->len - 1);
+      const bool ragged = __any_sync(0xffffffffu, !in);
       float ref = kNoRef, l = 0.0f;
-      for (int j = it.j0; j < it.j1; ++j, ++step) {
+      for (int j = j0; j < j1; ++j, ++step) {
         if (!(ok = wait_warp(bar_s(i), sn & 1))) break;
         tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc_ld32(ts + 32 * c, x + 32 * c);
-        tc_wait_ld();
         uint2 bad;  // a byte per 16 tokens
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                      : "=r"(bad.x), "=r"(bad.y)
                      : "r"(smem_s + C::off_bad + (step & 3) * 8)
                      : "memory");
-        if (j * kStep + kStep - 1 > least || !in) {
-          const int seen = limit - j * kStep;  // columns 0 .. seen
+        const bool masked = j * kStep + kStep - 1 > least || ragged || (bad.x | bad.y) != 0;
+        // The scores stay in tensor memory and are read twice, for the maximum
+        // and for the weights: registers for a row of 128 would spill.
+        uint32_t x[2][16];
+        auto hide = [&](uint32_t (&y)[16], int c) {
+          int seen = limit - j * kStep - 16 * c;  // columns 0 .. seen
+          if ((c < 4 ? bad.x : bad.y) >> (c & 3) * 8 & 1) seen = -1;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > seen) x[c] = 0xff800000u;
-        }
-        if (bad.x | bad.y) {
+          for (int k = 0; k < 16; ++k)
+            if (k > seen) y[k] = 0xff800000u;
+        };
+        float m0 = -INFINITY, m1 = -INFINITY;
+        tc_ld16(ts, x[0]);
+        // (rolled loops: straight-line code for a whole row runs out of the
+        // instruction caches that five roles share)
+#pragma unroll 1
+        for (int c2 = 0; c2 < 8; c2 += 2) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if ((c < 64 ? bad.x : bad.y) >> (c / 16 % 4 * 8) & 1) x[c] = 0xff800000u;
-        }
-        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+          for (int e = 0; e < 2; ++e) {
+            const int c = c2 + e;
+            uint32_t (&y)[16] = x[e];
+            tc_wait_ld();
+            tc_ld16(ts + 16 * ((c + 1) & 7), x[e ^ 1]);
+            if (masked) hide(y, c);
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          m0 = fmaxf(m0, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
-          m1 = fmaxf(m1, fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])));
-          m2 = fmaxf(m2, fmaxf(__uint_as_float(x[c + 4]), __uint_as_float(x[c + 5])));
-          m3 = fmaxf(m3, fmaxf(__uint_as_float(x[c + 6]), __uint_as_float(x[c + 7])));
+            for (int k = 0; k < 16; k += 4) {
+              m0 = max3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+              m1 = max3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
+            }
+          }
         }
-        float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+        float top = fmaxf(m0, m1);
         // (a row without visible columns keeps kNoRef)
         top = top == -INFINITY ? kNoRef : top * F;
         const bool move = top > ref + (ref == kNoRef ? 0.0f : kChunkSlack);
         if (__any_sync(0xffffffffu, move)) {
           const float f = move ? exp2_approx(ref - top) : 1.0f;
           if (move) ref = top, l *= f;
-          if (j > it.j0) {
-            // the sum of the earlier steps has to be complete
-            if (!(ok = wait_warp(bar_o(i), (sn - 1) & 1))) break;
-            tc_fence_after();
+          if (j > j0) {
+            // (these scores were issued after the sums of the earlier steps and
+            // are here, so those are complete)
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t y[32];
-              tc_ld32(to + c, y);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t y[16];
+              tc_ld16(to + c, y);
               tc_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-              tc_st32(to + c, y);
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+              tc_st16(to + c, y);
             }
+            tc_wait_st();
           }
         }
-        float s0 = 0, s1 = 0, s2 = 0, s3 = 0;
+        float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll 1
+        for (int c2 = 0; c2 < 8; c2 += 2) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          const float p0 = exp2_approx(fmaf(__uint_as_float(x[c]), F, -ref));
-          const float p1 = exp2_approx(fmaf(__uint_as_float(x[c + 1]), F, -ref));
-          const float p2 = exp2_approx(fmaf(__uint_as_float(x[c + 2]), F, -ref));
-          const float p3 = exp2_approx(fmaf(__uint_as_float(x[c + 3]), F, -ref));
-          s0 += p0, s1 += p1, s2 += p2, s3 += p3;
-          x[c / 2] = h2u(__floats2half2_rn(p0, p1));
-          x[c / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+          for (int e = 0; e < 2; ++e) {
+          const int c = c2 + e;
+          uint32_t (&y)[16] = x[e];
+          tc_wait_ld();
+          if (c < 7) tc_ld16(ts + 16 * (c + 1), x[e ^ 1]);
+          if (masked) hide(y, c);
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            const float p0 = exp2_approx(fmaf(__uint_as_float(y[k]), F, -ref));
+            const float p1 = exp2_approx(fmaf(__uint_as_float(y[k + 1]), F, -ref));
+            const float p2 = exp2_approx(fmaf(__uint_as_float(y[k + 2]), F, -ref));
+            const float p3 = exp2_approx(fmaf(__uint_as_float(y[k + 3]), F, -ref));
+            sum0 += p0 + p1;
+            sum1 += p2 + p3;
+            w[k / 2] = h2u(__floats2half2_rn(p0, p1));
+            w[k / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+          }
+          // columns 8c .. 8c + 7: read already, 16c and up are not touched
+          tc_st8(ts + 8 * c, w);
+          }
         }
-        l += (s0 + s1) + (s2 + s3);
-        tc_st32(ts, x);
-        tc_st32(ts + 32, x + 32);
+        l += sum0 + sum1;
         tc_wait_st();
         tc_fence_before();
-        bar_arrive(bar_p(i));
+        bar_arrive_warp(bar_p(i));
         ++sn;
       }
       if (!ok) break;
 
       // ---- output of the tile's steps [j0, j1)
-      if (!(ok = wait_warp(bar_o(i), (sn - 1) & 1))) break;
+      if (!(ok = wait_warp(bar_o(i), on++ & 1))) break;
       tc_fence_after();
-      const bool whole = it.j0 == 0 && it.j1 == it.steps;
-      const int64_t t = s.row0 + (in ? row / p.rg : 0);
-      uint16_t *dst = a.out + (t * p.Hq + it.h * p.rg + row % p.rg) * D;
+      const bool whole = j0 == 0 && j1 == it->steps;
+      const int64_t t = it->row0 + (in ? row / p.rg : 0);
+      uint16_t *dst = a.out + (t * p.Hq + it->h * p.rg + row % p.rg) * D;
       // 32 columns of the output row, scaled, to their channels
       auto put = [&](int c32, const float (&v)[32], float inv) {
 #pragma unroll
@@ -868,12 +984,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           if (in) put(c, v, inv);
         }
       } else {
-        const int64_t e = it.x_tile + it.steps + kOver;
-        int c0 = (int)(it.x_tile / U);
-        if ((c0 + 1) * U - it.x_tile <= kOver + 1) ++c0;
-        int c1 = (int)((e - 1) / U);
-        if (e - c1 * U <= 1) --c1;
-        const int slot = 2 * blockIdx.x + (it.j0 == 0 ? 1 : 0);
+        const int c0 = it->c0, c1 = it->c1;
+        const int slot = 2 * blockIdx.x + (j0 == 0 ? 1 : 0);
         float4 *wo = reinterpret_cast<float4 *>(a.ws_o) + (int64_t)(slot * 2 + i) * (D / 4) * 128 + r;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -892,7 +1004,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
         float2 *wm = reinterpret_cast<float2 *>(a.ws_ml) + (slot * 2 + i) * 128 + r;
         *wm = make_float2(ref, l);
         __threadfence();
-        bar_arrive(bar_g(i));
+        bar_arrive_warp(bar_g(i));
         if (!(ok = wait_warp(bar_g(i), gn++ & 1))) break;
         volatile uint32_t *flag = misc + 12 + i;
         if (r == 0) {
@@ -901,7 +1013,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           if (last) *count = 0;
           *flag = last;
         }
-        bar_arrive(bar_g(i));
+        bar_arrive_warp(bar_g(i));
         if (!(ok = wait_warp(bar_g(i), gn++ & 1))) break;
         if (*flag) {
           __threadfence();
@@ -941,11 +1053,12 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           }
         }
       }
+      bar_arrive_warp(bar_ie(item));
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
