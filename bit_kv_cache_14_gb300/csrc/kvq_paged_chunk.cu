@@ -8,8 +8,10 @@
 //   P_i = 2^(S_i F - ref)              one thread per row; fp16, back into tensor memory
 //   O_i (+)= P_i V                     tcgen05.mma, P from tensor memory
 // S, P and O stay in tensor memory (S and P share columns).  The reference of
-// a row moves only when a score passes it by more than 8 (log2 units), so O is
-// rescaled a few times per row at most, by the row's own thread.
+// a row is the maximum of earlier steps and moves only when a score passes it by
+// more than 8 (log2 units), so the weights need no pass over the scores for the
+// maximum first, and O is rescaled a few times per row at most, by the row's
+// own thread.
 //
 // Bound: 4*128*256*d operations per step on the tensor core against 128*256
 // exponentials and the dequantization of 128 keys and values: eight producer
@@ -19,7 +21,8 @@
 // tiles, which both query tiles use.
 //
 //   warps 0-3, 4-7: softmax and output of query tiles 0 and 1
-//   warps 8-15: producers    warp 16: MMA issue    warp 17: the list of items
+//   warps 8-15: producers    warp 16: MMA issue    warp 17: lists of items and
+//   of steps (the addresses of their pages)
 //   (warps 18, 19 only give up registers)
 //
 // Split: every (sequence, head, 256-row tile) is a list of its visible 128-token
@@ -36,9 +39,11 @@ int debug_stall_limit();
 namespace {
 
 constexpr int kChunkThreads = 640;
-// registers a thread: 640 * 96 at launch >= 256 * 120 + 256 * 80 + 128 * 64
+// registers a thread: 640 * 96 at launch >= 256 * 128 + 256 * 80 + 128 * 56
 constexpr int kProducerWarp = 8, kMmaWarp = 16, kItemWarp = 17;
-constexpr int kItems = 4;  // items on their way to the roles
+constexpr int kItems = 4;   // items on their way to the roles
+constexpr int kSteps = 16;  // steps known to the producers and the softmax warps
+constexpr int kAhead = 8;   // steps the list runs ahead of the producers' loads
 constexpr int kPWarps = kMmaWarp - kProducerWarp;
 constexpr int kStep = 128;       // cached tokens per step
 constexpr int kTileRows = 256;   // query rows per block
@@ -46,7 +51,8 @@ constexpr int kOver = 2;         // units of a tile's start and end
 constexpr int kMinUnits = 8;
 constexpr int kMaxChunkBlocks = 160;
 constexpr int kChunkWait = 1 << 17;  // times 32 polls
-constexpr float kChunkSlack = 8.0f;
+constexpr float kChunkSlack = 8.0f;  // log2 units a score may pass the reference by
+constexpr float kChunkTop = 15.0f;   // ... within a step: weights up to 2^15 fit fp16
 constexpr float kNoRef = -1e30f;
 
 struct ChunkArgs {
@@ -70,9 +76,9 @@ struct ChunkCfg {
   static constexpr int off_k = 2 * kTile;
   static constexpr int off_v = off_k + 2 * kTile;
   static constexpr int off_f = off_v + 2 * kTile;          // float [256] row factors
-  static constexpr int off_bad = off_f + kTileRows * 4;    // bytes [4][8]: atoms without a page
-  static constexpr int off_bar = off_bad + 32;
-  static constexpr int kBars = 19 + 2 * kItems;
+  static constexpr int off_step = off_f + kTileRows * 4;   // Step [kSteps]
+  static constexpr int off_bar = off_step + kSteps * 80;
+  static constexpr int kBars = 19 + 2 * kItems + 2 * kAhead;
   static constexpr int off_item = (off_bar + kBars * 8 + 15) / 16 * 16;
   static constexpr int off_misc = off_item + kItems * 64;  // tensor memory base, dead flag, flags
   static constexpr int off_prefix = off_misc + 64;
@@ -147,6 +153,18 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *r) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -155,14 +173,6 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-                   addr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-               "r"(r[7])
-               : "memory");
-}
-
 // Shared-memory matrix descriptor: 128-byte swizzle, strides in bytes.  Adding
 // n to it moves the address by 16 * n bytes.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -254,6 +264,17 @@ struct __align__(16) Item {
 };
 static_assert(sizeof(Item) == 64, "layout of the item ring");
 
+// One step, as the producers read it: where its eight atoms are (0: nowhere),
+// how many of its tokens exist (-1: no more steps), and which atoms belong to
+// the sequence but have no page.
+struct __align__(16) Step {
+  uint64_t atom[kStep / kAtom];
+  int tokens;
+  uint32_t bad;
+  int pad[2];
+};
+static_assert(sizeof(Step) == 80, "layout of the step ring");
+
 template <int D, int BITS>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
@@ -288,7 +309,12 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   if (tid == 0) {
     for (int i = 0; i < kItems; ++i) {
       bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 19 + i, 1);
-      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 19 + kItems + i, kMmaWarp + 1);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 19 + kItems + i, kProducerWarp + 1);
+    }
+    for (int i = 0; i < kAhead; ++i) {
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 19 + 2 * kItems + i, 1);
+      bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 19 + 2 * kItems + kAhead + i,
+               kPWarps);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + i, 4);
@@ -422,6 +448,9 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   // item n of the block (b < 0: there are no more, or a wait ran out), and its
   // release once the warp has taken what it needs
   const Item *items = reinterpret_cast<const Item *>(smem + C::off_item);
+  const Step *steps = reinterpret_cast<const Step *>(smem + C::off_step);
+  auto bar_sf = [&](uint32_t n) { return bars + 8u * (19 + 2 * kItems + (n % kAhead)); };
+  auto bar_se = [&](uint32_t n) { return bars + 8u * (19 + 2 * kItems + kAhead + (n % kAhead)); };
   auto bar_if = [&](uint32_t n) { return bars + 8u * (19 + (n % kItems)); };
   auto bar_ie = [&](uint32_t n) { return bars + 8u * (19 + kItems + (n % kItems)); };
   // the same for a whole warp, with one answer (tcgen05.ld / st need it whole)
@@ -443,7 +472,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   }
 
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kMmaWarp) {
       // ---- MMA issue: the whole warp keeps step, one lane issues
       constexpr uint32_t kQK = mma_desc(kStep, false), kPV = mma_desc(D, true);
@@ -530,50 +559,93 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       for (int i = 0; i < kChunkWait && !done; ++i) done = bar_try_32(bar_end, 0);
       __syncwarp();
     } else if (warp == kItemWarp) {
-      // ---- the items of [x0, x1), in turn
+      // ---- the items of [x0, x1), in turn, and their steps.  (Polls of this
+      // warp pause: it is never the one that is waited for long.)
       int b = sh_at[0], h = sh_at[1], t = sh_at[2], off = sh_at[3];
       int64_t x = x0;
       Seq s = seq_of(a, b);
       int tiles = (s.rows + kTileRows - 1) / kTileRows;
+      const int apage_log = __ffs(p.page / kAtom) - 1;
+      uint32_t sn = 0;  // steps listed
+      auto wait_idle = [&](uint32_t bar, uint32_t parity) {
+        for (int i = 0; i < (kChunkWait << 3); ++i) {
+          if (__all_sync(0xffffffffu, bar_try_wait(bar, parity))) return true;
+          if (__any_sync(0xffffffffu, *dead)) return false;
+          __nanosleep(100);
+        }
+        *dead = 1;
+        paged_error(p, KVQ_ETIMEOUT);
+        return false;
+      };
       for (uint32_t in = 0;; ++in) {
-        if (in >= kItems && !wait_warp(bar_ie(in), (in / kItems - 1) & 1)) break;
+        if (in >= kItems && !wait_idle(bar_ie(in), (in / kItems - 1) & 1)) break;
         Item *it = const_cast<Item *>(items) + in % kItems;
-        if (x >= x1) {
+        const bool end = x >= x1;
+        int j0 = 0, j1 = 0;
+        if (end) {
           if (lane == 0) it->b = -1;
-          bar_arrive_warp(bar_if(in));
-          break;
-        }
-        while (t >= tiles) {
-          t = 0;
-          if (tiles > 0 && ++h < p.H) break;
-          h = 0;
-          do {
-            ++b;
-            s = seq_of(a, b);
-          } while (s.rows == 0);
-          tiles = (s.rows + kTileRows - 1) / kTileRows;
-        }
-        const int steps = steps_of(a, s, t), cost = steps + kOver;
-        const int n = (int)min((int64_t)(cost - off), x1 - x);
-        const int64_t first = x - off, end = first + cost;
-        if (lane == 0) {
-          it->b = b, it->h = h;
-          it->j0 = off > kOver ? off - kOver : 0;
-          it->j1 = off + n - kOver;
-          it->row0 = s.row0, it->row_first = t * kTileRows;
-          it->rows = s.rows, it->len = s.len;
-          it->pos0 = s.pos0;
-          it->steps = steps;
-          // (the borders as they were moved, above)
-          int c0 = (int)(first / U), c1 = (int)((end - 1) / U);
-          if ((c0 + 1) * U - first <= kOver + 1) ++c0;
-          if (end - c1 * U <= 1) --c1;
-          it->c0 = c0, it->c1 = c1;
+        } else {
+          while (t >= tiles) {
+            t = 0;
+            if (tiles > 0 && ++h < p.H) break;
+            h = 0;
+            do {
+              ++b;
+              s = seq_of(a, b);
+            } while (s.rows == 0);
+            tiles = (s.rows + kTileRows - 1) / kTileRows;
+          }
+          const int nsteps = steps_of(a, s, t), cost = nsteps + kOver;
+          const int n = (int)min((int64_t)(cost - off), x1 - x);
+          const int64_t first = x - off, last = first + cost;
+          j0 = off > kOver ? off - kOver : 0;
+          j1 = off + n - kOver;
+          if (lane == 0) {
+            it->b = b, it->h = h;
+            it->j0 = j0, it->j1 = j1;
+            it->row0 = s.row0, it->row_first = t * kTileRows;
+            it->rows = s.rows, it->len = s.len;
+            it->pos0 = s.pos0;
+            it->steps = nsteps;
+            // (the borders as they were moved, above)
+            int c0 = (int)(first / U), c1 = (int)((last - 1) / U);
+            if ((c0 + 1) * U - first <= kOver + 1) ++c0;
+            if (last - c1 * U <= 1) --c1;
+            it->c0 = c0, it->c1 = c1;
+          }
+          x += n;
+          off = 0;
+          ++t;
         }
         bar_arrive_warp(bar_if(in));
-        x += n;
-        off = 0;
-        ++t;
+        // its steps (at the end: one that says so)
+        bool ok = true;
+        const int64_t head_at = (int64_t)h * p.head_bytes;
+        for (int j = j0; j < j1 + (end ? 1 : 0); ++j, ++sn) {
+          if (sn >= kAhead && !(ok = wait_idle(bar_se(sn), (sn / kAhead - 1) & 1))) break;
+          Step *st = const_cast<Step *>(steps) + sn % kSteps;
+          bool bad = false;
+          if (lane < kStep / kAtom && !end) {
+            const int atom = j * (kStep / kAtom) + lane;
+            uint64_t at = 0;
+            if (atom * kAtom < s.len) {
+              const int64_t id = __ldg(p.table + (int64_t)b * p.width + (atom >> apage_log));
+              bad = id < 0 || id >= p.n_pages;
+              if (!bad)
+                at = reinterpret_cast<uint64_t>(p.pages) + id * p.page_bytes + head_at +
+                     (atom & ((1 << apage_log) - 1)) * AB;
+            }
+            st->atom[lane] = at;
+          }
+          const uint32_t all_bad = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) {
+            st->tokens = end ? -1 : s.len - j * kStep;
+            st->bad = all_bad;
+            if (all_bad) paged_error(p, KVQ_EPAGE);
+          }
+          bar_arrive_warp(bar_sf(sn));
+        }
+        if (end || !ok) break;
       }
     }
   } else if (warp >= kProducerWarp) {
@@ -582,85 +654,67 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     constexpr int QW = RB / 16;        // words of a quarter row
     constexpr int kUnits = kStep / (8 * kPWarps);  // tokens of a thread
     const int pw = warp - kProducerWarp, t8 = lane & 7, jq = lane >> 3;
-    const int apage_log = __ffs(p.page / kAtom) - 1;
     uint32_t kraw[kUnits][QW], kst[kUnits][NG], vraw[kUnits][QW], vst[kUnits][NG];
-    int id[kUnits];
-    // two cursors: page numbers are read two steps ahead, codes one
-    struct Cursor {
-      int b, h, j, len;
-      bool on;
-    };
-    Cursor far = {};
-    int far_j1 = 0;
-    uint32_t in = 0;
-    auto far_next = [&]() {
-      if (far.on && far.j + 1 < far_j1) {
-        ++far.j;
-        return;
-      }
-      const Item *it = take_item(in);
-      far.on = it != nullptr;
-      if (far.on) {
-        far.b = it->b, far.h = it->h, far.j = it->j0, far.len = it->len;
-        far_j1 = it->j1;
-        bar_arrive_warp(bar_ie(in));
-        ++in;
-      }
-    };
-    auto read_ids = [&]() {
+    // the thread's tokens of a step are row 8 * (pw & 1) + t8 of atoms
+    // 4 * u + pw / 2
+    const uint32_t row = 8 * (pw & 1) + t8;
+    const uint32_t code_at = row * RB + jq * (RB / 4), stat_at = 2 * kAtom * RB + row * SB;
+    // codes and statistics of the keys (or values) of a step; statistics 0 where
+    // there is no token: nothing there may reach an output
+    auto fetch = [&](const Step *st, bool value, uint32_t (&raw)[kUnits][QW],
+                     uint32_t (&stat)[kUnits][NG]) {
+      const int tokens = st->tokens;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int atom = far.j * (kStep / kAtom) + kPWarps / 2 * u + (pw >> 1);
-        id[u] = -2;  // behind the sequence
-        if (far.on && atom * kAtom < far.len)
-          id[u] = max(__ldg(p.table + far.b * p.width + (atom >> apage_log)), -1);
-      }
-    };
-    // codes and statistics of the keys (or values) of step c, pages `pid`
-    auto fetch = [&](const Cursor &c, const int (&pid)[kUnits], bool value,
-                     uint32_t (&raw)[kUnits][QW], uint32_t (&st)[kUnits][NG]) {
+        const uint64_t at = st->atom[kPWarps / 2 * u + (pw >> 1)];
+        const bool ok = at != 0 && 8 * (kPWarps * u + pw) + t8 < tokens;
+        const uint8_t *base = ok ? reinterpret_cast<const uint8_t *>(at) : p.pages;
+        const uint8_t *src = base + code_at + (value ? kAtom * RB : 0);
+        if constexpr (QW % 4 == 0) {
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const int token = c.j * kStep + 8 * (kPWarps * u + pw) + t8;
-        const bool ok = pid[u] >= 0 && (int64_t)pid[u] < p.n_pages && token < c.len;
-        if (ok) {
-          const int row = token % kAtom;
-          const uint8_t *at = p.pages + pid[u] * p.page_bytes + c.h * p.head_bytes +
-                              (int64_t)((token / kAtom) & ((1 << apage_log) - 1)) * AB;
-          const uint8_t *src = at + (value ? kAtom * RB : 0) + row * RB + jq * (RB / 4);
-          if constexpr (QW % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < QW; i += 4) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 4 * i));
-              raw[u][i] = v.x, raw[u][i + 1] = v.y, raw[u][i + 2] = v.z, raw[u][i + 3] = v.w;
-            }
-          } else if constexpr (QW == 2) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-            raw[u][0] = v.x, raw[u][1] = v.y;
-          } else {
-            raw[u][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+          for (int i = 0; i < QW; i += 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 4 * i));
+            raw[u][i] = v.x, raw[u][i + 1] = v.y, raw[u][i + 2] = v.z, raw[u][i + 3] = v.w;
           }
-          const uint8_t *ss = at + 2 * kAtom * RB + (value ? kAtom * SB : 0) + row * SB;
-          if constexpr (NG == 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(ss));
-            st[u][0] = v.x, st[u][1] = v.y, st[u][2 % NG] = v.z, st[u][3 % NG] = v.w;
-          } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(ss));
-            st[u][0] = v.x, st[u][1] = v.y;
-          }
+        } else if constexpr (QW == 2) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+          raw[u][0] = v.x, raw[u][1] = v.y;
         } else {
-          // zeros: nothing there may reach an output
-#pragma unroll
-          for (int i = 0; i < QW; ++i) raw[u][i] = 0;
-#pragma unroll
-          for (int i = 0; i < NG; ++i) st[u][i] = 0;
+          raw[u][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+        }
+        const uint8_t *ss = base + stat_at + (value ? kAtom * SB : 0);
+        if constexpr (NG == 4) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(ss));
+          stat[u][0] = v.x, stat[u][1] = v.y, stat[u][2 % NG] = v.z, stat[u][3 % NG] = v.w;
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2 *>(ss));
+          stat[u][0] = v.x, stat[u][1] = v.y;
         }
       }
+    };
+    // which of the thread's tokens a step has
+    auto present = [&](const Step *st) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        if (st->atom[kPWarps / 2 * u + (pw >> 1)] != 0 &&
+            8 * (kPWarps * u + pw) + t8 < st->tokens)
+          m |= 1u << u;
+      return m;
+    };
+    auto clear = [&](uint32_t m, uint32_t (&stat)[kUnits][NG]) {
+      if (__all_sync(0xffffffffu, m == (1u << kUnits) - 1)) return;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        if (!(m >> u & 1)) {
+#pragma unroll
+          for (int i = 0; i < NG; ++i) stat[u][i] = 0;
+        }
     };
     auto store_keys = [&](uint32_t tile) {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int row = 8 * (kPWarps * u + pw) + t8;
+        const int trow = 8 * (kPWarps * u + pw) + t8;
 #pragma unroll
         for (int G = 0; G < NG; ++G) {
           const uint32_t sel = G & 1 ? 0x3232u : 0x1010u;
@@ -674,7 +728,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           }
           // channels 32G + 8jq .. + 7
           const int unit = (G & 1) * 4 + jq;
-          const uint32_t at = tile + (G / 2) * (kStep * 128) + row * 128 + ((unit ^ t8) << 4);
+          const uint32_t at = tile + (G / 2) * (kStep * 128) + trow * 128 + ((unit ^ t8) << 4);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]),
                        "r"(x[2]), "r"(x[3])
                        : "memory");
@@ -684,7 +738,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     auto store_values = [&](uint32_t tile) {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int row = 8 * (kPWarps * u + pw) + t8;
+        const int trow = 8 * (kPWarps * u + pw) + t8;
 #pragma unroll
         for (int e8 = 0; e8 < 2; ++e8) {  // eighths 2jq, 2jq + 1
 #pragma unroll
@@ -709,7 +763,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
             // 32 * (2h + e) + 4 * eighth + i
             const int unit = (2 * jq + e8) * (NG / 2) + h;
             const uint32_t at =
-                tile + (unit >> 3) * (kStep * 128) + row * 128 + (((unit & 7) ^ t8) << 4);
+                tile + (unit >> 3) * (kStep * 128) + trow * 128 + (((unit & 7) ^ t8) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]),
                          "r"(x[1]), "r"(x[2]), "r"(x[3])
                          : "memory");
@@ -717,57 +771,42 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
         }
       }
     };
-    // prime: ids of the first step, its codes, ids of the second
-    Cursor nxt;
-    int pid[kUnits];
-    far_next();
-    read_ids();
-    nxt = far;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) pid[u] = id[u];
-    fetch(nxt, pid, false, kraw, kst);
-    fetch(nxt, pid, true, vraw, vst);
-    uint32_t bad = 0;
-    auto bad_of = [&]() {
-      bad = 0;
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-        if (pid[u] != -2 && (pid[u] < 0 || (int64_t)pid[u] >= p.n_pages)) bad |= 1u << u;
-    };
-    far_next();
-    read_ids();
-    uint32_t n = 0;
-    while (nxt.on) {
-      bad_of();
-      if (bad && lane == 0) paged_error(p, KVQ_EPAGE);
-      nxt = far;
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) pid[u] = id[u];
-      const int stage = n & 1;
+    auto step_at = [&](uint32_t k) { return steps + k % kSteps; };
+    bool go = wait_warp(bar_sf(0), 0) && step_at(0)->tokens >= 0;
+    uint32_t have = 0;
+    if (go) {
+      fetch(step_at(0), false, kraw, kst);
+      fetch(step_at(0), true, vraw, vst);
+      have = present(step_at(0));
+      bar_arrive_warp(bar_se(0));
+    }
+    for (uint32_t n = 0; go; ++n) {
+      const uint32_t stage = n & 1, now = have;
+      clear(now, kst);
       // (a stage's first use waits for nothing)
       if (n >= 2 && !wait_warp(bar_ke(stage), ((n >> 1) - 1) & 1)) break;
-      if (lane == 0 && !(pw & 1)) {
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-          smem[C::off_bad + (n & 3) * 8 + kPWarps / 2 * u + (pw >> 1)] = bad >> u & 1;
-      }
       store_keys(smem_s + C::off_k + stage * C::kTile);
       async_fence();
       bar_arrive_warp(bar_kf(stage));
-      if (nxt.on) fetch(nxt, pid, false, kraw, kst);
+      const Step *next = step_at(n + 1);
+      if (!wait_warp(bar_sf(n + 1), (n + 1) / kAhead & 1)) break;
+      go = next->tokens >= 0;
+      if (go) {
+        fetch(next, false, kraw, kst);
+        have = present(next);
+      }
+      clear(now, vst);
       if (n >= 2 && !wait_warp(bar_ve(stage), ((n >> 1) - 1) & 1)) break;
       store_values(smem_s + C::off_v + stage * C::kTile);
       async_fence();
       bar_arrive_warp(bar_vf(stage));
-      if (nxt.on) {
-        fetch(nxt, pid, true, vraw, vst);
-        far_next();
-        read_ids();
+      if (go) {
+        fetch(next, true, vraw, vst);
+        bar_arrive_warp(bar_se(n + 1));
       }
-      ++n;
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // ---- softmax and output: one thread per row
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lane_base = (uint32_t)(warp & 3) * 32u << 16;
@@ -845,56 +884,18 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       // newest position every row of the tile sees (its first row's)
       const int least = (int)min(it->pos0 + row_first / p.rg, (int64_t)it->len - 1);
       const bool ragged = __any_sync(0xffffffffu, !in);
-      float ref = kNoRef, l = 0.0f;
+      float ref = kNoRef, l = 0.0f;  // reference and sum of the row's weights
+      float over = 0.0f;             // by how much the last step's scores passed it
       for (int j = j0; j < j1; ++j, ++step) {
         if (!(ok = wait_warp(bar_s(i), sn & 1))) break;
         tc_fence_after();
-        uint2 bad;  // a byte per 16 tokens
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                     : "=r"(bad.x), "=r"(bad.y)
-                     : "r"(smem_s + C::off_bad + (step & 3) * 8)
-                     : "memory");
-        const bool masked = j * kStep + kStep - 1 > least || ragged || (bad.x | bad.y) != 0;
-        // The scores stay in tensor memory and are read twice, for the maximum
-        // and for the weights: registers for a row of 128 would spill.
-        uint32_t x[2][16];
-        auto hide = [&](uint32_t (&y)[16], int c) {
-          int seen = limit - j * kStep - 16 * c;  // columns 0 .. seen
-          if ((c < 4 ? bad.x : bad.y) >> (c & 3) * 8 & 1) seen = -1;
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (k > seen) y[k] = 0xff800000u;
-        };
-        float m0 = -INFINITY, m1 = -INFINITY;
-        tc_ld16(ts, x[0]);
-        // (rolled loops: straight-line code for a whole row runs out of the
-        // instruction caches that five roles share)
-#pragma unroll 1
-        for (int c2 = 0; c2 < 8; c2 += 2) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = c2 + e;
-            uint32_t (&y)[16] = x[e];
-            tc_wait_ld();
-            tc_ld16(ts + 16 * ((c + 1) & 7), x[e ^ 1]);
-            if (masked) hide(y, c);
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              m0 = max3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-              m1 = max3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
-            }
-          }
-        }
-        float top = fmaxf(m0, m1);
-        // (a row without visible columns keeps kNoRef)
-        top = top == -INFINITY ? kNoRef : top * F;
-        const bool move = top > ref + (ref == kNoRef ? 0.0f : kChunkSlack);
-        if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? exp2_approx(ref - top) : 1.0f;
-          if (move) ref = top, l *= f;
+        const uint32_t bad = steps[step % kSteps].bad;  // a bit per 16 tokens
+        const bool masked = j * kStep + kStep - 1 > least || ragged || bad != 0;
+        // these scores were issued after the sums of the earlier steps and are
+        // here, so those are complete and O may be scaled
+        auto rescale = [&](float f) {
+          l *= f;
           if (j > j0) {
-            // (these scores were issued after the sums of the earlier steps and
-            // are here, so those are complete)
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t y[16];
@@ -906,32 +907,127 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
             }
             tc_wait_st();
           }
+        };
+        // the reference moves where the last step's scores passed it by more
+        // than the slack
+        if (__any_sync(0xffffffffu, over > kChunkSlack)) {
+          const float by = over > kChunkSlack ? over : 0.0f;
+          rescale(exp2_approx(-by));
+          ref += by;
         }
+        over = 0.0f;
+        auto hide = [&](uint32_t (&y)[32], int c) {
+          const int seen = limit - j * kStep - 32 * c;  // columns 0 .. seen
+          const uint32_t b2 = bad >> (2 * c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (k > seen || (b2 >> (k / 16) & 1)) y[k] = 0xff800000u;
+        };
         float sum0 = 0.0f, sum1 = 0.0f;
+        // The usual step: nothing to hide and no weight beyond fp16.  Straight
+        // code without a branch, the weights kept in registers until the
+        // maximum is known; where they turn out too large the scores are still
+        // there for the careful loop below.
+        bool done = false;
+        if (!masked && j > j0) {
+          uint32_t w[64], x[2][16];
+          float m0 = -INFINITY, m1 = -INFINITY;
+          tc_ld16(ts, x[0]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t (&y)[16] = x[c & 1];
+            tc_wait_ld();
+            if (c < 7) tc_ld16(ts + 16 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              m0 = max3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+              m1 = max3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
+              const float p0 = exp2_approx(fmaf(__uint_as_float(y[k]), F, -ref));
+              const float p1 = exp2_approx(fmaf(__uint_as_float(y[k + 1]), F, -ref));
+              const float p2 = exp2_approx(fmaf(__uint_as_float(y[k + 2]), F, -ref));
+              const float p3 = exp2_approx(fmaf(__uint_as_float(y[k + 3]), F, -ref));
+              sum0 += p0 + p1;
+              sum1 += p2 + p3;
+              w[8 * c + k / 2] = h2u(__floats2half2_rn(p0, p1));
+              w[8 * c + k / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+            }
+          }
+          const float top = fmaf(fmaxf(m0, m1), F, -ref);
+          done = !__any_sync(0xffffffffu, top > kChunkTop);
+          if (done) {
+            over = fmaxf(top, 0.0f);
+            tc_st32(ts, w);
+            tc_st32(ts + 32, w + 32);
+          } else {
+            sum0 = sum1 = 0.0f;
+          }
+        }
+        if (!done) {
+        uint32_t x[2][32];
+        tc_ld32(ts, x[0]);
+        // (rolled: straight-line code for a whole row runs out of the
+        // instruction caches that the roles share)
 #pragma unroll 1
-        for (int c2 = 0; c2 < 8; c2 += 2) {
+        for (int c2 = 0; c2 < 4; c2 += 2) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-          const int c = c2 + e;
-          uint32_t (&y)[16] = x[e];
-          tc_wait_ld();
-          if (c < 7) tc_ld16(ts + 16 * (c + 1), x[e ^ 1]);
-          if (masked) hide(y, c);
-          uint32_t w[8];
+            const int c = c2 + e;
+            uint32_t (&y)[32] = x[e];
+            tc_wait_ld();
+            if (c < 3) tc_ld32(ts + 32 * (c + 1), x[e ^ 1]);
+            if (masked) hide(y, c);
+            float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float p0 = exp2_approx(fmaf(__uint_as_float(y[k]), F, -ref));
-            const float p1 = exp2_approx(fmaf(__uint_as_float(y[k + 1]), F, -ref));
-            const float p2 = exp2_approx(fmaf(__uint_as_float(y[k + 2]), F, -ref));
-            const float p3 = exp2_approx(fmaf(__uint_as_float(y[k + 3]), F, -ref));
-            sum0 += p0 + p1;
-            sum1 += p2 + p3;
-            w[k / 2] = h2u(__floats2half2_rn(p0, p1));
-            w[k / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+            for (int k = 0; k < 32; k += 4) {
+              m0 = max3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+              m1 = max3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
+            }
+            const float m = fmaxf(m0, m1);
+            float top = fmaf(m, F, -ref);
+            if (__any_sync(0xffffffffu, top > kChunkTop)) {
+              // A weight that fp16 could not hold, or a row's first scores: the
+              // reference moves now, and with it the weights stored before (a
+              // power of two, so they stay exact).
+              const bool first = ref == kNoRef, jump = top > kChunkTop;
+              const float by = jump && !first ? ceilf(top) : 0.0f;
+              const float f = jump && first ? 0.0f : exp2_approx(-by);
+              sum0 *= f, sum1 *= f;
+              const uint32_t f2 = h2u(__float2half2_rn(f));
+              tc_wait_st();
+#pragma unroll 1
+              for (int b8 = 0; b8 < 16 * c; b8 += 16) {
+                uint32_t v[16];
+                tc_ld16(ts + b8, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v[k]) : "r"(v[k]), "r"(f2));
+                tc_st16(ts + b8, v);
+              }
+              rescale(f);
+              if (jump) {
+                ref = first ? m * F : ref + by;
+                over = 0.0f;
+              }
+              top = fmaf(m, F, -ref);
+            }
+            over = fmaxf(over, top);
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float p0 = exp2_approx(fmaf(__uint_as_float(y[k]), F, -ref));
+              const float p1 = exp2_approx(fmaf(__uint_as_float(y[k + 1]), F, -ref));
+              const float p2 = exp2_approx(fmaf(__uint_as_float(y[k + 2]), F, -ref));
+              const float p3 = exp2_approx(fmaf(__uint_as_float(y[k + 3]), F, -ref));
+              sum0 += p0 + p1;
+              sum1 += p2 + p3;
+              w[k / 2] = h2u(__floats2half2_rn(p0, p1));
+              w[k / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+            }
+            // columns 16c .. 16c + 15: read already, 32c + 32 and up are not touched
+            tc_st16(ts + 16 * c, w);
           }
-          // columns 8c .. 8c + 7: read already, 16c and up are not touched
-          tc_st8(ts + 8 * c, w);
-          }
+        }
         }
         l += sum0 + sum1;
         tc_wait_st();
