@@ -39,7 +39,10 @@ int debug_stall_limit();
 namespace {
 
 constexpr int kChunkThreads = 640;
-// registers a thread: 640 * 96 at launch >= 256 * 128 + 256 * 80 + 128 * 56
+// Registers a thread, of the 640 * 96 at launch: softmax, producers (which hold
+// a step's codes), the others.  256 * 136 + 256 * 88 + 128 * 32 = 61440.
+constexpr int kSoftRegs = 136, kProducerRegs = 88, kOtherRegs = 32;
+static_assert(256 * kSoftRegs + 256 * kProducerRegs + 128 * kOtherRegs <= 640 * 96, "registers");
 constexpr int kProducerWarp = 8, kMmaWarp = 16, kItemWarp = 17;
 constexpr int kItems = 4;   // items on their way to the roles
 constexpr int kSteps = 16;  // steps known to the producers and the softmax warps
@@ -50,7 +53,7 @@ constexpr int kTileRows = 256;   // query rows per block
 constexpr int kOver = 2;         // units of a tile's start and end
 constexpr int kMinUnits = 8;
 constexpr int kMaxChunkBlocks = 160;
-constexpr int kChunkWait = 1 << 17;  // times 32 polls
+constexpr int kChunkWait = 1 << 25;
 constexpr float kChunkSlack = 8.0f;  // log2 units a score may pass the reference by
 constexpr float kChunkTop = 15.0f;   // ... within a step: weights up to 2^15 fit fp16
 constexpr float kNoRef = -1e30f;
@@ -112,20 +115,6 @@ __device__ __forceinline__ void bar_arrive_warp(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Up to 32 polls in a loop of four instructions: the waiting warps share their
-// schedulers with the working ones.
-__device__ __forceinline__ bool bar_try_32(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 32;\n"
-      "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
-      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
-      "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ void async_fence() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -203,6 +192,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Two fp32 numbers in a 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair64u(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
+  return pair64u(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 unpair64(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -436,10 +449,13 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   auto tm_o = [&](int i) { return tmem + 256u + 128u * i; };
 
   // Bounded waits: one that runs out records KVQ_ETIMEOUT and ends every role.
-  auto wait = [&](uint32_t bar, uint32_t parity) {
+  // (Between polls a warp sleeps a little: waiting warps share their schedulers
+  // with working ones.)
+  auto wait = [&](uint32_t bar, uint32_t parity, int ns = 20) {
     for (int i = 0; i < kChunkWait; ++i) {
-      if (bar_try_32(bar, parity)) return true;
-      if (*dead) return false;
+      if (bar_try_wait(bar, parity)) return true;
+      __nanosleep(ns);
+      if ((i & 63) == 63 && *dead) return false;
     }
     *dead = 1;
     paged_error(p, KVQ_ETIMEOUT);
@@ -454,8 +470,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   auto bar_if = [&](uint32_t n) { return bars + 8u * (19 + (n % kItems)); };
   auto bar_ie = [&](uint32_t n) { return bars + 8u * (19 + kItems + (n % kItems)); };
   // the same for a whole warp, with one answer (tcgen05.ld / st need it whole)
-  auto wait_warp = [&](uint32_t bar, uint32_t parity) {
-    return (bool)__all_sync(0xffffffffu, wait(bar, parity));
+  auto wait_warp = [&](uint32_t bar, uint32_t parity, int ns = 20) {
+    return (bool)__all_sync(0xffffffffu, wait(bar, parity, ns));
   };
   auto take_item = [&](uint32_t n) -> const Item * {
     if (!wait_warp(bar_if(n), n / kItems & 1)) return nullptr;
@@ -472,7 +488,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   }
 
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
       // ---- MMA issue: the whole warp keeps step, one lane issues
       constexpr uint32_t kQK = mma_desc(kStep, false), kPV = mma_desc(D, true);
@@ -556,29 +572,18 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       // whatever was issued ends before tensor memory is freed
       commit(bar_end);
       bool done = false;
-      for (int i = 0; i < kChunkWait && !done; ++i) done = bar_try_32(bar_end, 0);
+      for (int i = 0; i < kChunkWait && !done; ++i) done = bar_try_wait(bar_end, 0);
       __syncwarp();
     } else if (warp == kItemWarp) {
-      // ---- the items of [x0, x1), in turn, and their steps.  (Polls of this
-      // warp pause: it is never the one that is waited for long.)
+      // ---- the items of [x0, x1), in turn, and their steps
       int b = sh_at[0], h = sh_at[1], t = sh_at[2], off = sh_at[3];
       int64_t x = x0;
       Seq s = seq_of(a, b);
       int tiles = (s.rows + kTileRows - 1) / kTileRows;
       const int apage_log = __ffs(p.page / kAtom) - 1;
       uint32_t sn = 0;  // steps listed
-      auto wait_idle = [&](uint32_t bar, uint32_t parity) {
-        for (int i = 0; i < (kChunkWait << 3); ++i) {
-          if (__all_sync(0xffffffffu, bar_try_wait(bar, parity))) return true;
-          if (__any_sync(0xffffffffu, *dead)) return false;
-          __nanosleep(100);
-        }
-        *dead = 1;
-        paged_error(p, KVQ_ETIMEOUT);
-        return false;
-      };
       for (uint32_t in = 0;; ++in) {
-        if (in >= kItems && !wait_idle(bar_ie(in), (in / kItems - 1) & 1)) break;
+        if (in >= kItems && !wait_warp(bar_ie(in), (in / kItems - 1) & 1, 200)) break;
         Item *it = const_cast<Item *>(items) + in % kItems;
         const bool end = x >= x1;
         int j0 = 0, j1 = 0;
@@ -622,7 +627,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
         bool ok = true;
         const int64_t head_at = (int64_t)h * p.head_bytes;
         for (int j = j0; j < j1 + (end ? 1 : 0); ++j, ++sn) {
-          if (sn >= kAhead && !(ok = wait_idle(bar_se(sn), (sn / kAhead - 1) & 1))) break;
+          if (sn >= kAhead && !(ok = wait_warp(bar_se(sn), (sn / kAhead - 1) & 1, 200))) break;
           Step *st = const_cast<Step *>(steps) + sn % kSteps;
           bool bad = false;
           if (lane < kStep / kAtom && !end) {
@@ -649,7 +654,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       }
     }
   } else if (warp >= kProducerWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // ---- producers: thread (quarter jq, token t8 of eight), two tokens a step
     constexpr int QW = RB / 16;        // words of a quarter row
     constexpr int kUnits = kStep / (8 * kPWarps);  // tokens of a thread
@@ -784,7 +789,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       const uint32_t stage = n & 1, now = have;
       clear(now, kst);
       // (a stage's first use waits for nothing)
-      if (n >= 2 && !wait_warp(bar_ke(stage), ((n >> 1) - 1) & 1)) break;
+      if (n >= 2 && !wait_warp(bar_ke(stage), ((n >> 1) - 1) & 1, 60)) break;
       store_keys(smem_s + C::off_k + stage * C::kTile);
       async_fence();
       bar_arrive_warp(bar_kf(stage));
@@ -796,7 +801,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
         have = present(next);
       }
       clear(now, vst);
-      if (n >= 2 && !wait_warp(bar_ve(stage), ((n >> 1) - 1) & 1)) break;
+      if (n >= 2 && !wait_warp(bar_ve(stage), ((n >> 1) - 1) & 1, 60)) break;
       store_values(smem_s + C::off_v + stage * C::kTile);
       async_fence();
       bar_arrive_warp(bar_vf(stage));
@@ -806,7 +811,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---- softmax and output: one thread per row
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lane_base = (uint32_t)(warp & 3) * 32u << 16;
@@ -932,6 +937,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
         if (!masked && j > j0) {
           uint32_t w[64], x[2][16];
           float m0 = -INFINITY, m1 = -INFINITY;
+          const uint64_t F2 = pair64(F, F), R2 = pair64(-ref, -ref);
+          uint64_t sa = 0, sb = 0;
           tc_ld16(ts, x[0]);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -942,12 +949,12 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
             for (int k = 0; k < 16; k += 4) {
               m0 = max3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
               m1 = max3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
-              const float p0 = exp2_approx(fmaf(__uint_as_float(y[k]), F, -ref));
-              const float p1 = exp2_approx(fmaf(__uint_as_float(y[k + 1]), F, -ref));
-              const float p2 = exp2_approx(fmaf(__uint_as_float(y[k + 2]), F, -ref));
-              const float p3 = exp2_approx(fmaf(__uint_as_float(y[k + 3]), F, -ref));
-              sum0 += p0 + p1;
-              sum1 += p2 + p3;
+              const float2 a0 = unpair64(fma2(pair64u(y[k], y[k + 1]), F2, R2));
+              const float2 a1 = unpair64(fma2(pair64u(y[k + 2], y[k + 3]), F2, R2));
+              const float p0 = exp2_approx(a0.x), p1 = exp2_approx(a0.y);
+              const float p2 = exp2_approx(a1.x), p3 = exp2_approx(a1.y);
+              sa = add2(sa, pair64(p0, p1));
+              sb = add2(sb, pair64(p2, p3));
               w[8 * c + k / 2] = h2u(__floats2half2_rn(p0, p1));
               w[8 * c + k / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
             }
@@ -956,10 +963,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           done = !__any_sync(0xffffffffu, top > kChunkTop);
           if (done) {
             over = fmaxf(top, 0.0f);
+            const float2 s0 = unpair64(sa), s1 = unpair64(sb);
+            sum0 = s0.x + s0.y, sum1 = s1.x + s1.y;
             tc_st32(ts, w);
             tc_st32(ts + 32, w + 32);
-          } else {
-            sum0 = sum1 = 0.0f;
           }
         }
         if (!done) {
