@@ -820,69 +820,85 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     uint32_t sn = 0, step = 0;  // score tiles taken; steps of the block (for the bad-page bytes)
     uint32_t on = 0, gn = 0;    // tiles finished; meetings of the tile's threads
     bool ok = true;
-    for (uint32_t item = 0; ok; ++item) {
-      const Item *it = take_item(item);
-      if (!it) break;
-      const int row_first = it->row_first + i * 128, rows = it->rows;
-      const int j0 = it->j0, j1 = it->j1;
-      if (row_first >= rows) {  // one tile only
-        step += j1 - j0;
-        bar_arrive_warp(bar_ie(item));
-        continue;
-      }
-      // queries: 16 lanes (d = 128) or 8 to a row; scaled so that the row's
-      // largest is in [2^8, 2^9), which bf16 queries need to fit fp16
-      {
-        constexpr int LR = D / 8;
-        const int l = lane % LR;
-#pragma unroll 4
-        for (int k = 0; k < LR; ++k) {
-          const int rr = (warp & 3) * 32 + k * (32 / LR) + lane / LR, row = row_first + rr;
-          const bool in = row < rows;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (in)
-            w = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(it->row0 + row / p.rg) * a.qs +
-                                                      (int64_t)(it->h * p.rg + row % p.rg) * D) +
-                      l);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          float f[8], big = 0.0f;
+    // queries: LR lanes to a row, LR rows a lane (in two halves); scaled so that a row's largest
+    // is in [2^8, 2^9), which bf16 queries need to fit fp16
+    constexpr int LR = D / 8;
+    const int ql = lane % LR, qr = (warp & 3) * 32 + lane / LR;
+    auto load_queries = [&](const Item *it, int half, uint4 (&w)[LR / 2]) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (p.bf16) {
-              f[2 * c] = __uint_as_float(ww[c] << 16);
-              f[2 * c + 1] = __uint_as_float(ww[c] & 0xffff0000u);
-            } else {
-              const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&ww[c]));
-              f[2 * c] = v.x;
-              f[2 * c + 1] = v.y;
-            }
-            big = fmaxf(big, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
+      for (int k = 0; k < LR / 2; ++k) {
+        const int row = it->row_first + i * 128 + qr + (k + half * (LR / 2)) * (32 / LR);
+        w[k] = make_uint4(0, 0, 0, 0);
+        if (row < it->rows)
+          w[k] = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(it->row0 + row / p.rg) * a.qs +
+                                                       (int64_t)(it->h * p.rg + row % p.rg) * D) +
+                       ql);
+      }
+    };
+    auto store_queries = [&](int half, const uint4 (&w)[LR / 2]) {
+#pragma unroll
+      for (int k = 0; k < LR / 2; ++k) {
+        const int rr = qr + (k + half * (LR / 2)) * (32 / LR);
+        const uint32_t ww[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        float f[8], big = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (p.bf16) {
+            f[2 * c] = __uint_as_float(ww[c] << 16);
+            f[2 * c + 1] = __uint_as_float(ww[c] & 0xffff0000u);
+          } else {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&ww[c]));
+            f[2 * c] = v.x;
+            f[2 * c + 1] = v.y;
           }
-#pragma unroll
-          for (int o = 1; o < LR; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-          int ex = ((__float_as_int(big) >> 23) & 255) - 127;
-          ex = big == 0.0f ? 0 : max(min(ex, 90), -90);
-          const float mul = a.sign * __int_as_float((127 + 8 - ex) << 23);
-          uint32_t o4[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            o4[c] = h2u(__floats2half2_rn(f[2 * c] * mul, f[2 * c + 1] * mul));
-          const uint32_t at = smem_s + C::off_q + i * C::kTile + (l >> 3) * (kStep * 128) +
-                              rr * 128 + (((l & 7) ^ (rr & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o4[0]),
-                       "r"(o4[1]), "r"(o4[2]), "r"(o4[3])
-                       : "memory");
-          // (never 0: a hidden column's -inf stays -inf)
-          if (l == 0)
-            fs[rr] = fmaxf(a.scale_log2 * __int_as_float((127 + ex - 8) << 23), 1e-30f);
+          big = fmaxf(big, fmaxf(fabsf(f[2 * c]), fabsf(f[2 * c + 1])));
         }
-        async_fence();
-        __syncwarp();
+#pragma unroll
+        for (int o = 1; o < LR; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        int ex = ((__float_as_int(big) >> 23) & 255) - 127;
+        ex = big == 0.0f ? 0 : max(min(ex, 90), -90);
+        const float mul = a.sign * __int_as_float((127 + 8 - ex) << 23);
+        uint32_t o4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          o4[c] = h2u(__floats2half2_rn(f[2 * c] * mul, f[2 * c + 1] * mul));
+        const uint32_t at = smem_s + C::off_q + i * C::kTile + (ql >> 3) * (kStep * 128) +
+                            rr * 128 + (((ql & 7) ^ (rr & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o4[0]), "r"(o4[1]),
+                     "r"(o4[2]), "r"(o4[3])
+                     : "memory");
+        // (never 0: a hidden column's -inf stays -inf)
+        if (ql == 0) fs[rr] = fmaxf(a.scale_log2 * __int_as_float((127 + ex - 8) << 23), 1e-30f);
       }
-      const float F = fs[r];  // (rows of this warp: written by this warp)
+    };
+    auto queries_in = [&]() {
+      async_fence();
       tc_fence_before();
       bar_arrive_warp(bar_q(i));
-
+    };
+    // the block's next item with rows for this tile, from item n on
+    uint32_t item = 0;
+    auto next_item = [&]() -> const Item * {
+      for (;; ++item) {
+        const Item *it = take_item(item);
+        if (!it || it->row_first + i * 128 < it->rows) return it;
+        step += it->j1 - it->j0;
+        bar_arrive_warp(bar_ie(item));
+      }
+    };
+    const Item *it = next_item();
+    if (it) {
+      uint4 w0[LR / 2], w1[LR / 2];
+      load_queries(it, 0, w0);
+      load_queries(it, 1, w1);
+      store_queries(0, w0);
+      store_queries(1, w1);
+      queries_in();
+    }
+    while (it) {
+      const int row_first = it->row_first + i * 128, rows = it->rows;
+      const int j0 = it->j0, j1 = it->j1;
+      const float F = fs[r];  // (rows of this warp: written by this warp)
       const int row = row_first + r;
       const bool in = row < rows;
       const int limit = in ? (int)min(it->pos0 + row / p.rg, (int64_t)it->len - 1) : -1;
@@ -1044,9 +1060,23 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       }
       if (!ok) break;
 
+      // the next item's queries are on their way while the last sums are added,
+      // and its first scores are computed during this item's output
+      const uint32_t this_item = item++;
+      const Item *next = next_item();
+      {
+        uint4 w[LR / 2];
+        if (next) load_queries(next, 0, w);
+        if (!(ok = wait_warp(bar_o(i), on++ & 1))) break;
+        tc_fence_after();
+        if (next) {
+          store_queries(0, w);
+          load_queries(next, 1, w);
+          store_queries(1, w);
+          queries_in();
+        }
+      }
       // ---- output of the tile's steps [j0, j1)
-      if (!(ok = wait_warp(bar_o(i), on++ & 1))) break;
-      tc_fence_after();
       const bool whole = j0 == 0 && j1 == it->steps;
       const int64_t t = it->row0 + (in ? row / p.rg : 0);
       uint16_t *dst = a.out + (t * p.Hq + it->h * p.rg + row % p.rg) * D;
@@ -1156,7 +1186,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           }
         }
       }
-      bar_arrive_warp(bar_ie(item));
+      bar_arrive_warp(bar_ie(this_item));
+      it = next;
     }
   }
   tc_fence_before();
