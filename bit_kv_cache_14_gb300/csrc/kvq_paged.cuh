@@ -44,12 +44,30 @@ cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, vo
                                    float scale, void *ws, cudaStream_t st, int *launches);
 size_t paged_workspace_bytes();
 cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                              int few, void *ws, int num_sms, cudaStream_t st);
+                              int few, bool early, void *ws, int num_sms, cudaStream_t st);
 size_t paged_rows_workspace();
 cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                               int few, void *ws, int num_sms, cudaStream_t st);
+                               int few, bool early, void *ws, int num_sms, cudaStream_t st);
 size_t paged_chunk_workspace();
 int num_sms_cached();
+
+// Launch with or without leave to start while the previous kernel on the stream
+// ends (programmatic dependent launch; the kernel waits itself where it has to).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads, int smem,
+                             cudaStream_t st, bool early, A &&...args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = attr;
+  c.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, static_cast<A &&>(args)...);
+}
 
 namespace {
 

@@ -20,17 +20,16 @@ cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, vo
   // a mixed call's small sequences are decode steps: the 8-row form of the
   // split kernel, where the heads of one token fit it
   const int few = (most <= 8 || (most > kPagedFewRows && p.rg <= 8)) ? 8 : kPagedFewRows;
+  const bool rows = p.rg <= few, chunks = most > few;
   cudaError_t e = cudaSuccess;
-  *launches = 0;
-  if (p.rg <= few) {
-    e = launch_paged_rows(p, q, qs, out, scale, few, ws, sms, st);
-    ++*launches;
-  }
-  if (e == cudaSuccess && most > few) {
-    e = launch_paged_chunk(p, q, qs, out, scale, few,
+  // Alone, the split kernel may start its blocks while the kernel before the
+  // call ends (it waits before it reads).  Together, the split kernel starts
+  // when everything before it is done, and the other one beside it.
+  if (rows) e = launch_paged_rows(p, q, qs, out, scale, few, !chunks, ws, sms, st);
+  if (e == cudaSuccess && chunks)
+    e = launch_paged_chunk(p, q, qs, out, scale, few, rows,
                            static_cast<uint8_t *>(ws) + paged_rows_workspace(), sms, st);
-    ++*launches;
-  }
+  *launches = (int)rows + (int)chunks;
   return e;
 }
 

@@ -70,6 +70,7 @@ struct ChunkArgs {
   float *ws_o;       // [2 * blocks][2 tiles][d / 4][128] float4
   int *ws_count;     // [blocks][2 tiles], zero between calls
   int stall_limit;
+  bool early;        // launched behind the split kernel of the same call, see below
 };
 
 template <int D>
@@ -433,7 +434,14 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   }
   __syncthreads();
   const int64_t x0 = sh_x[0], x1 = sh_x[1];
-  if (x0 >= x1) return;
+  // Behind the split kernel of the same call this one runs as soon as there is
+  // room: that kernel started after everything before the call was done, and
+  // the two write different rows.  Only the end waits, so that this kernel's
+  // completion stands for both.
+  if (x0 >= x1) {
+    grid_dep_wait();
+    return;
+  }
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -1191,6 +1199,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     }
   }
   tc_fence_before();
+  grid_dep_wait();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -1206,8 +1215,7 @@ cudaError_t chunk_as(const ChunkArgs &a, int num_sms, cudaStream_t st) {
   const cudaError_t e = kernel_setup(setup, kern, kChunkThreads, smem, nullptr);
   if (e != cudaSuccess) return e;
   const int blocks = num_sms < kMaxChunkBlocks ? num_sms : kMaxChunkBlocks;
-  kern<<<blocks, kChunkThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kern, (unsigned)blocks, kChunkThreads, smem, st, a.early, a);
 }
 
 constexpr size_t kCountBytes = 2 * kMaxChunkBlocks * 4;
@@ -1216,7 +1224,7 @@ constexpr size_t kMlBytes = (size_t)2 * kMaxChunkBlocks * kTileRows * 8;
 }  // namespace
 
 cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                               int few, void *ws, int num_sms, cudaStream_t st) {
+                               int few, bool early, void *ws, int num_sms, cudaStream_t st) {
   ChunkArgs a;
   a.p = p;
   a.q = static_cast<const uint16_t *>(q);
@@ -1225,6 +1233,7 @@ cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *
   a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.few = few;
+  a.early = early;
   uint8_t *w = static_cast<uint8_t *>(ws);
   a.ws_count = reinterpret_cast<int *>(w);
   a.ws_ml = reinterpret_cast<float *>(w + kCountBytes);

@@ -6,14 +6,15 @@
 // head against 4*d operations per row, so HBM, if the instructions per code stay
 // few enough (at 4 bits about 3.4 lane instructions per element keep up).
 //
-//  * Split: the 16-token atoms of all (sequence, head) pairs form one list, cut
-//    into equal contiguous ranges, one per block; inside a block the eight
-//    warps share each pair's atoms evenly.  Pairs that end up in several
-//    blocks leave partials (m, l, o), and the block that finishes a pair last
-//    joins them in block order, so results do not depend on timing.
-//  * A warp streams its atoms through a ring of shared-memory slots, one
-//    cp.async.bulk per atom (contiguous by layout), page numbers read one atom
-//    ahead of their use.
+//  * Split: the tiles (two 16-token atoms, one at 8 bits) of all (sequence,
+//    head) pairs form one list, cut into equal contiguous ranges, one per block;
+//    inside a block the eight warps share each pair's tiles evenly.  Pairs that
+//    end up in several blocks leave partials (m, l, o), and the block that
+//    finishes a pair last joins them in block order, so results do not depend
+//    on timing.
+//  * A warp streams its tiles through a ring of shared-memory slots, one
+//    cp.async.bulk per tile (contiguous by layout; one per atom where pages hold
+//    one), page numbers read one tile ahead of their use.
 //  * Keys: S^T[token][row] on mma.sync m16n8k16 with the raw codes as the A
 //    operand: a masked code in the low ten bits of a half is the fp16
 //    subnormal code * 2^(bit position) * 2^-24, exactly; the query operand
@@ -52,9 +53,9 @@ struct RowsArgs {
   float *ws_ml;    // [2 * blocks][rows][2]
   float *ws_o;     // [2 * blocks][rows][d]
   int *ws_count;   // [blocks], zero between calls
-  int min_units, snap;
   int few;         // sequences with more rows are not this kernel's
   int stall_limit;
+  bool early;      // the blocks may start while the previous kernel ends
 };
 
 template <int D, int BITS, int NT>
@@ -62,15 +63,17 @@ struct RowsCfg {
   static constexpr int RB = D * BITS / 8, SB = 4 * D / kPagedGroup, NG = D / kPagedGroup;
   static constexpr int AB = 2 * kAtom * (RB + SB);
   static constexpr int kBlocks = NT == 1 ? 2 : 1;  // per SM
-  // ring slots per warp: about 160 KB in flight per SM
-  static constexpr int S = NT == 1 ? (AB > 4000 ? 2 : AB > 2000 ? 3 : AB > 1400 ? 5 : 8)
-                                   : (AB > 4000 ? 3 : AB > 2000 ? 5 : 8);
+  static constexpr int TA = AB > 4000 ? 1 : 2;  // atoms per tile
+  static constexpr int TB = TA * AB;
+  // ring slots per warp: about 150 KB in flight per SM
+  static constexpr int S = NT == 1 ? (TB > 4000 ? 2 : TB > 3000 ? 3 : TB > 2000 ? 4 : 6)
+                                   : (TB > 4000 ? 4 : TB > 3000 ? 6 : 8);
   static constexpr int ROWB = D * 4 + 16;  // padded row of the merge buffer
-  static constexpr int off_merge = kRowWarps * S * AB;
-  static constexpr int off_ml = off_merge + kRowWarps * 8 * NT * ROWB;
-  static constexpr int off_bar = off_ml + kRowWarps * 8 * NT * 8;
+  static constexpr int off_merge = kRowWarps * S * TB;
+  static constexpr int off_ml = off_merge + kRowWarps / 2 * 8 * NT * ROWB;
+  static constexpr int off_bar = off_ml + kRowWarps / 2 * 8 * NT * 8;
   static constexpr int off_prefix = off_bar + kRowWarps * (S + 1) * 8;
-  static constexpr int smem(int seqs) { return off_prefix + (seqs + 1) * 8; }
+  static constexpr int smem(int seqs) { return off_prefix + (seqs + 1) * 12; }
 };
 
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
@@ -79,11 +82,19 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   return y;
 }
 
+// Products that start from zero.
 __device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(b0));
+      "{%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+}
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Codes at bit `off` of both halves of w: code * 2^(off % 8) * 2^-24 as fp16.
@@ -112,16 +123,16 @@ __device__ __forceinline__ void lds_words(const uint8_t *src, uint32_t (&w)[N]) 
 
 // Where a unit index lies: sequence, head, offset inside the pair.
 struct Place {
-  int b, h, off, atoms;
+  int b, h, off, tiles;
 };
 __device__ __forceinline__ Place locate(const int64_t *prefix, int H, int64_t x, int b) {
   while (H * prefix[b + 1] <= x) ++b;
   Place u;
   u.b = b;
-  u.atoms = (int)(prefix[b + 1] - prefix[b]);
+  u.tiles = (int)(prefix[b + 1] - prefix[b]);
   const int64_t r = x - H * prefix[b];
-  u.h = (int)(r / u.atoms);
-  u.off = (int)(r - (int64_t)u.h * u.atoms);
+  u.h = (int)(r / u.tiles);
+  u.off = (int)(r - (int64_t)u.h * u.tiles);
   return u;
 }
 __device__ __forceinline__ int seq_of_unit(const int64_t *prefix, int B, int H, int64_t x) {
@@ -133,16 +144,25 @@ __device__ __forceinline__ int seq_of_unit(const int64_t *prefix, int B, int H, 
   return lo;
 }
 
-// First unit of block c: c * U, moved to a pair's border when one is near.
+// The list is cut in one of two ways.  Joining a pair's parts costs about as
+// much time as kPiece tiles take a block, so when every pair in pieces of about
+// kPiece tiles gives no more pieces than there are blocks, each block takes one
+// piece.  A longer list is cut evenly into ranges of U tiles, though not within
+// kSnap tiles of a pair's border.
+constexpr int kPiece = 16, kSnap = 4;
+__device__ __forceinline__ int pieces_of(int64_t tiles) {
+  return tiles == 0 ? 0 : max(1, (int)((tiles + kPiece / 2) / kPiece));
+}
+// First unit of block c under the even cut.
 __device__ __forceinline__ int64_t border(const int64_t *prefix, int B, int H, int64_t total,
-                                          int64_t U, int snap, int64_t c) {
+                                          int64_t U, int64_t c) {
   const int64_t x = c * U;
   if (x >= total) return total;
   if (x == 0) return 0;
   const Place u = locate(prefix, H, x, seq_of_unit(prefix, B, H, x));
-  if (u.off <= snap && u.off <= u.atoms - u.off) return x - u.off;
-  if (u.atoms - u.off <= snap) return x + u.atoms - u.off;
-  return x;
+  const int rest = u.tiles - u.off;
+  if (u.off <= kSnap && u.off <= rest) return x - u.off;
+  return rest <= kSnap ? x + rest : x;
 }
 
 template <int D, int BITS, int NT>
@@ -150,60 +170,96 @@ __global__ void __launch_bounds__(kRowThreads, RowsCfg<D, BITS, NT>::kBlocks)
 paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   using C = RowsCfg<D, BITS, NT>;
   constexpr int RB = C::RB, SB = C::SB, NG = C::NG, S = C::S;
+  constexpr int TA = C::TA, TB = C::TB, kTile = TA * kAtom;
   constexpr int KW = RB / 16, VW = (RB / 8 + 3) / 4;  // words of a key quarter, a value eighth
   constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int sh_flag;
+  __shared__ int sh_flag, sh_first, sh_last;
   const Paged &p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
-  uint8_t *ring = smem + warp * S * C::AB;
+  uint8_t *ring = smem + warp * S * TB;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::off_bar) + warp * (S + 1);
   int64_t *prefix = reinterpret_cast<int64_t *>(smem + C::off_prefix);
+  int *pieces = reinterpret_cast<int *>(prefix + p.B + 1);
 
+  grid_dep_trigger();
   if (lane <= S) bar_init(&bars[lane], 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
-  // ---- the list of work: prefix[b] = atoms of one head of the sequences
-  // before b that have between 1 and kMaxRows rows
+  grid_dep_wait();
+  // ---- the list of work: prefix[b] = tiles of one head of the sequences
+  // before b that have between 1 and a.few rows
   {
     __shared__ int64_t warp_sum[kRowWarps];
+    __shared__ int warp_pieces[kRowWarps];
     const int per = (p.B + kRowThreads - 1) / kRowThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     int64_t sum = 0;
+    int psum = 0;
     for (int b = b0; b < b1; ++b) {
       const int n = p.cu[b + 1] - p.cu[b];
-      int64_t atoms = 0;
+      int64_t tiles = 0;
       if (n > p.max_tokens || p.cu[b] < 0 || p.cu[b + 1] > p.T) {
         if (blockIdx.x == 0) paged_error(p, KVQ_EINVAL);
       } else if (n > 0 && (int64_t)n * p.rg <= a.few) {
         const int64_t cap = p.width * p.page, len = p.lens[b];
         if (len > cap && blockIdx.x == 0) paged_error(p, KVQ_EPAGE);
-        atoms = (min(len, cap) + kAtom - 1) / kAtom;
-        if (atoms < 1) atoms = 1;  // rows that see nothing are written too
+        tiles = (min(len, cap) + kTile - 1) / kTile;
+        if (tiles < 1) tiles = 1;  // rows that see nothing are written too
       }
-      sum += atoms;
+      sum += tiles;
+      psum = min(psum + pieces_of(tiles), 1 << 20);  // (beyond any grid)
       prefix[b + 1] = sum;
+      pieces[b + 1] = psum;
     }
     int64_t inc = sum;
+    int pinc = psum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
+      const int pup = __shfl_up_sync(0xffffffffu, pinc, o);
+      if (lane >= o) inc += up, pinc = min(pinc + pup, 1 << 20);
     }
-    if (lane == 31) warp_sum[warp] = inc;
+    if (lane == 31) warp_sum[warp] = inc, warp_pieces[warp] = pinc;
     __syncthreads();
     int64_t before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    for (int b = b0; b < b1; ++b) prefix[b + 1] += before;
-    if (tid == 0) prefix[0] = 0;
+    int pbefore = pinc - psum;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w], pbefore += warp_pieces[w];
+    for (int b = b0; b < b1; ++b) {
+      prefix[b + 1] += before;
+      pieces[b + 1] = min(pieces[b + 1] + pbefore, 1 << 20);
+    }
+    if (tid == 0) prefix[0] = 0, pieces[0] = 0;
     __syncthreads();
   }
   const int H = p.H;
   const int64_t total = H * prefix[p.B];
-  const int64_t U = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)a.min_units);
-  const int64_t x0 = border(prefix, p.B, H, total, U, a.snap, blockIdx.x);
-  const int64_t x1 = border(prefix, p.B, H, total, U, a.snap, blockIdx.x + 1);
-  if (x0 >= x1) return;
+  const int64_t U = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)(2 * kSnap + 1));
+  const bool by_piece = (int64_t)H * pieces[p.B] <= gridDim.x;
+  int64_t x0, x1;
+  int first_b, c_first = blockIdx.x, c_last = blockIdx.x;  // by_piece: the blocks of the pair
+  if (by_piece) {
+    const int c = blockIdx.x;
+    if (c >= H * pieces[p.B]) return;
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (H * pieces[mid] <= c) lo = mid; else hi = mid;
+    }
+    first_b = lo;
+    const int n = pieces[lo + 1] - pieces[lo], r = c - H * pieces[lo], k = r % n;
+    const int64_t tiles = prefix[lo + 1] - prefix[lo];
+    const int64_t pair = H * prefix[lo] + r / n * tiles;
+    x0 = pair + (int64_t)k * kPiece;
+    x1 = k == n - 1 ? pair + tiles : x0 + kPiece;
+    c_first = c - k;
+    c_last = c_first + n - 1;
+  } else {
+    x0 = border(prefix, p.B, H, total, U, blockIdx.x);
+    x1 = border(prefix, p.B, H, total, U, blockIdx.x + 1);
+    if (x0 >= x1) return;
+    first_b = seq_of_unit(prefix, p.B, H, x0);
+  }
 
   const uint64_t policy = l2_evict_first();
   bool dead = false;
@@ -211,55 +267,79 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     if (lane == 0) paged_error(p, KVQ_ETIMEOUT);
     dead = true;
   }
-  const int first_b = seq_of_unit(prefix, p.B, H, x0);
 
-  // ---- fetch side: this warp's atoms of every segment of [x0, x1) in turn.
-  // (fb, fh): the pair being fetched; f0: next atom; pid: its page, read ahead
+  // ---- fetch side: this warp's tiles of every segment of [x0, x1) in turn.
+  // (fb, fh): the pair being fetched; f0: next tile; pid: its pages, read ahead
   int64_t fx = x0;
-  int fb = first_b, fh = 0, f0 = 0, f1 = 0;
-  const int apage_log = __ffs(p.page / kAtom) - 1;
-  int pid = -1;
-  auto fetch_next = [&]() {  // moves to the next atom; false at the end
+  int fb = first_b, fh = 0, f0 = 0, f1 = 0, flen = 0;
+  const int page_log = __ffs(p.page) - 1;
+  int pid[TA];
+  const int32_t *row = nullptr;  // the sequence's block table
+  auto fetch_next = [&]() {  // moves to the next tile; false at the end
     while (f0 == f1) {
       if (fx >= x1) return false;
       const Place u = locate(prefix, H, fx, fb);
-      const int n = (int)min((int64_t)(u.atoms - u.off), x1 - fx);
+      const int n = (int)min((int64_t)(u.tiles - u.off), x1 - fx);
       fb = u.b, fh = u.h;
       f0 = u.off + (int)((int64_t)n * warp / kRowWarps);
       f1 = u.off + (int)((int64_t)n * (warp + 1) / kRowWarps);
       fx += n;
+      row = p.table + fb * p.width;
+      flen = (int)min((int64_t)max(p.lens[fb], 0), p.width * p.page);
     }
     return true;
   };
   auto read_pid = [&]() {
-    // (a pair that holds no tokens has one atom without a page: any entry)
-    pid = __ldg(p.table + fb * p.width + (f0 >> apage_log));
+    // (a pair that holds no tokens has one tile without a page: any entry)
+    const int t = f0 * kTile;
+    pid[0] = __ldg(row + (t >> page_log));
+    if (TA == 2) {
+      pid[TA - 1] = pid[0];
+      if (p.page == kAtom) pid[TA - 1] = t + kAtom < flen ? __ldg(row + (t >> page_log) + 1) : -1;
+    }
   };
-  int issued = 0, used = 0;
-  uint32_t skip = 0;  // bit per slot: the atom's page does not exist
+  int issue_slot = 0, in_flight = 0, slot = 0;
+  uint32_t phase = 0, skip = 0;  // skip: TA bits per slot, the atom's page does not exist
   bool more = fetch_next();
   if (more) read_pid();
   auto issue = [&]() {
-    const int slot = issued % S;
-    const int at = f0 & ((1 << apage_log) - 1), head = fh;
-    const int64_t id = pid;
-    const bool ok = id >= 0 && id < p.n_pages;
-    // the next atom's page number is on its way while this one's copy starts
+    const uint8_t *src[TA];
+    uint32_t gone = 0;
+    const int64_t in_page = fh * p.head_bytes +
+                            (int64_t)(((f0 * kTile) & (p.page - 1)) / kAtom) * C::AB;
+#pragma unroll
+    for (int i = 0; i < TA; ++i) {
+      const int64_t id = pid[i];
+      if (id < 0 || id >= p.n_pages) gone |= 1u << i;
+      src[i] = p.pages + id * p.page_bytes + in_page;
+    }
+    const bool paired = TA == 1 || p.page > kAtom;  // one copy for the tile
+    // the next tile's page numbers are on their way while this one's copy starts
     ++f0;
     more = fetch_next();
     if (more) read_pid();
-    if (ok) {
-      skip &= ~(1u << slot);
-      if (lane == 0) {
-        bulk_g2s_pred(true, smem_u32(&bars[slot]), C::AB, smem_u32(ring + slot * C::AB),
-                      p.pages + id * p.page_bytes + head * p.head_bytes + (int64_t)at * C::AB,
-                      C::AB, policy);
+    skip = (skip & ~(((1u << TA) - 1) << (TA * issue_slot))) | gone << (TA * issue_slot);
+    if (lane == 0) {
+      uint64_t *bar = &bars[issue_slot];
+      const uint32_t dst = smem_u32(ring + issue_slot * TB);
+      if (paired && !gone) {
+        bulk_g2s_pred(true, smem_u32(bar), TB, dst, src[0], TB, policy);
+      } else if (paired || gone == (1u << TA) - 1) {
+        bar_expect_tx(bar, 0);
+      } else {
+        // pages of one atom: the copies that exist, one arrival
+        const uint32_t both = gone ? C::AB : TB;
+        if (!(gone & 1)) bulk_g2s_pred(true, smem_u32(bar), both, dst, src[0], C::AB, policy);
+        if (!(gone & 2)) {
+          if (gone & 1)
+            bulk_g2s_pred(true, smem_u32(bar), both, dst + C::AB, src[TA - 1], C::AB, policy);
+          else
+            bulk_g2s(ring + issue_slot * TB + C::AB, src[TA - 1], C::AB, bar);
+        }
       }
-    } else {
-      skip |= 1u << slot;
-      if (lane == 0) bar_expect_tx(&bars[slot], 0);
     }
-    ++issued;
+    issue_slot = issue_slot + 1 == S ? 0 : issue_slot + 1;
+    ++in_flight;
   };
   if (!dead)
     for (int i = 0; i < S && more; ++i) issue();
@@ -269,7 +349,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   for (int64_t x = x0; x < x1;) {
     const Place u = locate(prefix, H, x, b);
     b = u.b;
-    const int n = (int)min((int64_t)(u.atoms - u.off), x1 - x);
+    const int n = (int)min((int64_t)(u.tiles - u.off), x1 - x);
     const int a0 = u.off + (int)((int64_t)n * warp / kRowWarps);
     const int a1 = u.off + (int)((int64_t)n * (warp + 1) / kRowWarps);
     const int row0 = p.cu[b], tokens = p.cu[b + 1] - row0, rows = tokens * p.rg;
@@ -352,29 +432,33 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     }
     const int least = (int)min(pos0, (int64_t)len - 1);  // newest position every row sees
 
-    float o[NG][2][NT][4] = {}, za[NG][NT][2] = {}, l[NT][2] = {}, rf[NT][2], lim[NT][2];
+    float o[NG][2][NT][4] = {}, za[NG][NT][2] = {}, l[NT][2] = {}, rf[NT][2];
     uint32_t e2 = 0;  // largest value scale covered by the reference, in both halves
     int E = -24;
+    float slack = kSlack - (float)E;  // how far a score may pass the reference
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) rf[nt][s] = kNoRef, lim[nt][s] = kNoRef;
+      for (int s = 0; s < 2; ++s) rf[nt][s] = 0.0f;
+    uint32_t fresh = (1u << (2 * NT)) - 1;  // rows that have seen no score: no reference yet
 
     for (int at = a0; at < a1; ++at) {
       if (dead) break;
-      const int slot = used % S;
-      if (!bar_wait(&bars[slot], (used / S) & 1, kRowWaitLimit)) {
+      if (!bar_wait(&bars[slot], phase, kRowWaitLimit)) {
         if (lane == 0) paged_error(p, KVQ_ETIMEOUT);
         dead = true;
         break;
       }
-      ++used;
-      const uint8_t *at_s = ring + slot * C::AB;
-      if (at * kAtom >= len) {
-        // the one atom of a sequence without tokens
-      } else if (skip >> slot & 1) {
-        if (lane == 0) paged_error(p, KVQ_EPAGE);
-      } else {
+      const uint8_t *at_s = ring + slot * TB;
+      const uint32_t gone = skip >> (TA * slot);
+#pragma unroll 1
+      for (int sub = 0; sub < TA; ++sub, at_s += C::AB) {
+        const int pos = at * kTile + sub * kAtom;
+        if (pos >= len) break;  // (or the one tile of a sequence without tokens)
+        if (gone >> sub & 1) {
+          if (lane == 0) paged_error(p, KVQ_EPAGE);
+          continue;
+        }
         // token of fragment row r < 8: (r >> 1) + 4 * (r & 1); rows 8.. 8 more
         const int t0 = (g >> 1) + 4 * (g & 1);
         uint32_t k0[KW], k1[KW], ks[2][NG], vs[2][NG];
@@ -386,7 +470,6 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
         lds_words(st + (t0 + 8) * SB, ks[1]);
         lds_words(st + kAtom * SB + t0 * SB, vs[0]);
         lds_words(st + kAtom * SB + (t0 + 8) * SB, vs[1]);
-        const int pos = at * kAtom;
         const bool masked = pos + kAtom - 1 > least;
         if (masked) {
           // slots behind the last token hold anything
@@ -404,7 +487,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
           const uint32_t z1 = NG == 4 ? (j & 1 ? ks[1][3 % NG] : ks[1][2 % NG]) : ks[1][1];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float zt[4] = {};
+            float zt[4];
             mma1688(zt, z0, z1, qsum[nt]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) t[nt][i] = zt[i] * (1.0f / kSub);
@@ -415,7 +498,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
         for (int i = 0; i < KW; ++i) k08[i] = k0[i] >> 8, k18[i] = k1[i] >> 8;
 #pragma unroll
         for (int G = 0; G < NG; ++G) {
-          float c[NT][4] = {};
+          float c[NT][4];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             const int pa = (G * 4 + 2 * m) * BITS, pb = pa + BITS;  // bit offsets of two pairs
@@ -425,27 +508,31 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
             const uint32_t x3_ = codes_at<BITS>(k1[pb / 16], k18[pb / 16], pb % 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma16816(c[nt], x0_, x1_, x2_, x3_, qf[nt][G][2 * m], qf[nt][G][2 * m + 1]);
+              if (m == 0)
+                mma16816_first(c[nt], x0_, x1_, x2_, x3_, qf[nt][G][0], qf[nt][G][1]);
+              else
+                mma16816(c[nt], x0_, x1_, x2_, x3_, qf[nt][G][2], qf[nt][G][3]);
           }
           const float2 s0 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[0][G / 2]));
           const float2 s1 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[1][G / 2]));
           const float f0_ = G & 1 ? s0.y : s0.x, f1_ = G & 1 ? s1.y : s1.x;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            t[nt][0] += f0_ * c[nt][0];
-            t[nt][1] += f0_ * c[nt][1];
-            t[nt][2] += f1_ * c[nt][2];
-            t[nt][3] += f1_ * c[nt][3];
+            t[nt][0] = fmaf(f0_, c[nt][0], t[nt][0]);
+            t[nt][1] = fmaf(f0_, c[nt][1], t[nt][1]);
+            t[nt][2] = fmaf(f1_, c[nt][2], t[nt][2]);
+            t[nt][3] = fmaf(f1_, c[nt][3], t[nt][3]);
           }
         }
-        bool over = false;
+        bool over = fresh != 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            t[nt][i] *= F[nt][i & 1];
+            // relative to the reference
+            t[nt][i] = fmaf(t[nt][i], F[nt][i & 1], -rf[nt][i & 1]);
             if (masked && pos + t0 + 8 * (i >> 1) > limit[nt][i & 1]) t[nt][i] = -INFINITY;
-            over |= t[nt][i] > lim[nt][i & 1];
+            over |= t[nt][i] > slack;
           }
         {
           __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&vs[0][0]),
@@ -470,12 +557,16 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1)
                   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-                const float ref = fmaxf(rf[nt][s] - (float)E, mx);
-                // (before the first score, a row's reference stays at kNoRef)
-                const float nrf = rf[nt][s] == kNoRef && mx < kNoRef ? kNoRef : ref + (float)En;
-                const float f = exp2_approx(rf[nt][s] - nrf);
-                rf[nt][s] = nrf;
-                lim[nt][s] = nrf == kNoRef ? kNoRef : ref + kSlack;
+                // from the reference to the larger of itself and the scores, and
+                // from the old E to the new; a row without scores stays
+                const bool first = fresh >> (2 * nt + s) & 1;
+                float by = fmaxf(mx + (float)E, 0.0f) + (float)(En - E);
+                if (first) by = mx == -INFINITY ? 0.0f : mx + (float)En;
+                if (mx != -INFINITY) fresh &= ~(1u << (2 * nt + s));
+                const float f = first ? 0.0f : exp2_approx(-by);
+                rf[nt][s] += by;
+                t[nt][s] -= by;
+                t[nt][2 + s] -= by;
                 l[nt][s] *= f;
 #pragma unroll
                 for (int G = 0; G < NG; ++G) {
@@ -487,13 +578,14 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
                 }
               }
             E = En;
+            slack = kSlack - (float)E;
           }
         }
         // ---- weights
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t[nt][i] = exp2_approx(t[nt][i] - rf[nt][i & 1]);
+          for (int i = 0; i < 4; ++i) t[nt][i] = exp2_approx(t[nt][i]);
           l[nt][0] += t[nt][0] + t[nt][2];
           l[nt][1] += t[nt][1] + t[nt][3];
         }
@@ -512,8 +604,8 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
           for (int nt = 0; nt < NT; ++nt) {
             w[G][nt][0] = movm(h2u(__floats2half2_rn(t[nt][0] * sa, t[nt][1] * sa)));
             w[G][nt][1] = movm(h2u(__floats2half2_rn(t[nt][2] * sb, t[nt][3] * sb)));
-            za[G][nt][0] += t[nt][0] * ya + t[nt][2] * yb;
-            za[G][nt][1] += t[nt][1] * ya + t[nt][3] * yb;
+            za[G][nt][0] = fmaf(t[nt][0], ya, fmaf(t[nt][2], yb, za[G][nt][0]));
+            za[G][nt][1] = fmaf(t[nt][1], ya, fmaf(t[nt][3], yb, za[G][nt][1]));
           }
         }
         // ---- values: tokens (j, j + 4) and (j + 8, j + 12), eighth g
@@ -557,49 +649,89 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       }
       // the slot is free once every lane has read it
       __syncwarp();
+      --in_flight;
+      if (++slot == S) slot = 0, phase ^= 1;
       if (more) issue();
     }
 
-    // ---- the block's state of this segment: every warp's (reference, l, o)
-    // to shared memory, joined slice by slice
+    // ---- the block's state of this segment: warps 4-7 leave (reference, l, o)
+    // in shared memory, warps 0-3 join theirs to it, and the four are then
+    // joined slice by slice
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) l[nt][s] += __shfl_xor_sync(0xffffffffu, l[nt][s], k);
-        const int r = 8 * nt + 2 * j + s;
-        uint8_t *row = smem + C::off_merge + (warp * kRows + r) * C::ROWB;
+        if (fresh >> (2 * nt + s) & 1) rf[nt][s] = kNoRef;
 #pragma unroll
         for (int G = 0; G < NG; ++G) {
           float z = za[G][nt][s];
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
-          float4 v;
-          float *vf = &v.x;
+          // the accumulators hold code sums at their codes' positions
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int off = (((G >> 1) * 4 + i) * BITS + (RB / 8 == 2 ? 8 * (G & 1) : 0)) % 8;
-            vf[i] = o[G][i >> 1][nt][2 * (i & 1) + s] * __int_as_float((127 + 24 - off) << 23) + z;
+            float &v = o[G][i >> 1][nt][2 * (i & 1) + s];
+            v = fmaf(v, __int_as_float((127 + 24 - off) << 23), z);
           }
-          *reinterpret_cast<float4 *>(row + (G * 8 + g) * 16) = v;
         }
-        if (g == 0)
-          *reinterpret_cast<float2 *>(smem + C::off_ml + (warp * kRows + r) * 8) =
-              make_float2(rf[nt][s], l[nt][s]);
       }
-    __syncthreads();
+    constexpr int kHalf = kRowWarps / 2;
+#pragma unroll
+    for (int round = 0; round < 2; ++round) {
+      if ((warp >= kHalf) == (round == 0)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int r = (warp % kHalf) * kRows + 8 * nt + 2 * j + s;
+            uint8_t *row = smem + C::off_merge + r * C::ROWB;
+            float2 *ml = reinterpret_cast<float2 *>(smem + C::off_ml + r * 8);
+            float f = 1.0f, fy = 0.0f;
+            if (round == 1) {
+              const float2 y = *ml;
+              const float m = fmaxf(rf[nt][s], y.x);
+              f = exp2_approx(rf[nt][s] - m), fy = exp2_approx(y.x - m);
+              rf[nt][s] = m;
+              l[nt][s] = l[nt][s] * f + y.y * fy;
+            }
+#pragma unroll
+            for (int G = 0; G < NG; ++G) {
+              float4 *at = reinterpret_cast<float4 *>(row + (G * 8 + g) * 16);
+              float4 v = make_float4(o[G][0][nt][s], o[G][0][nt][2 + s], o[G][1][nt][s],
+                                     o[G][1][nt][2 + s]);
+              if (round == 1) {
+                const float4 y = *at;
+                v = make_float4(v.x * f + y.x * fy, v.y * f + y.y * fy, v.z * f + y.z * fy,
+                                v.w * f + y.w * fy);
+              }
+              *at = v;
+            }
+            if (round == 1) __syncwarp();
+            if (g == 0) *ml = make_float2(rf[nt][s], l[nt][s]);
+          }
+      }
+      __syncthreads();
+    }
     // which blocks share the pair
-    const int64_t pair0 = x - u.off, pair1 = pair0 + u.atoms;
+    const int64_t pair0 = x - u.off, pair1 = pair0 + u.tiles;
     const bool whole = pair0 >= x0 && pair1 <= x1;
     constexpr int kQuads = D / 4;
-    int c_first = 0, c_last = 0;
-    if (!whole) {
-      // (a border moves by less than a range's length, and never past a pair's)
-      c_first = (int)(pair0 / U);
-      if (border(prefix, p.B, H, total, U, a.snap, c_first + 1) <= pair0) ++c_first;
-      c_last = (int)((pair1 - 1) / U);
-      if (border(prefix, p.B, H, total, U, a.snap, c_last) >= pair1) --c_last;
+    if (!whole && !by_piece) {
+      if (tid == 0) {
+        int c = (int)(pair0 / U);
+        while (border(prefix, p.B, H, total, U, c) > pair0) --c;
+        while (border(prefix, p.B, H, total, U, c + 1) <= pair0) ++c;
+        sh_first = c;
+        c = (int)((pair1 - 1) / U);
+        while (border(prefix, p.B, H, total, U, c) >= pair1) --c;
+        while (border(prefix, p.B, H, total, U, c + 1) < pair1) ++c;
+        sh_last = c;
+      }
+      __syncthreads();
+      c_first = sh_first, c_last = sh_last;
     }
     auto store = [&](int r, int quad, float4 v, float sum) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -621,16 +753,16 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     for (int i = tid; i < rows * kQuads; i += kRowThreads) {
       const int r = i / kQuads, quad = i % kQuads;
       float m = kNoRef;
-      float2 ml[kRowWarps];
+      float2 ml[kHalf];
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) {
+      for (int w = 0; w < kHalf; ++w) {
         ml[w] = *reinterpret_cast<const float2 *>(smem + C::off_ml + (w * kRows + r) * 8);
         m = fmaxf(m, ml[w].x);
       }
       float sum = 0.0f;
       float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) {
+      for (int w = 0; w < kHalf; ++w) {
         const float f = exp2_approx(ml[w].x - m);
         const float4 y = *reinterpret_cast<const float4 *>(
             smem + C::off_merge + (w * kRows + r) * C::ROWB + quad * 16);
@@ -685,7 +817,10 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   }
   // a warp that gave up leaves no copy of its own in flight
   if (dead)
-    for (; used < issued; ++used) bar_wait(&bars[used % S], (used / S) & 1, kDrainLimit);
+    for (; in_flight > 0; --in_flight) {
+      bar_wait(&bars[slot], phase, kDrainLimit);
+      if (++slot == S) slot = 0, phase ^= 1;
+    }
 }
 
 template <int D, int BITS, int NT>
@@ -699,14 +834,13 @@ cudaError_t launch_as(RowsArgs &a, int num_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   int blocks = num_sms * occ;
   if (blocks > kPagedRowBlocks) blocks = kPagedRowBlocks;
-  kern<<<blocks, kRowThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kern, (unsigned)blocks, kRowThreads, smem, st, a.early, a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                              int few, void *ws, int num_sms, cudaStream_t st) {
+                              int few, bool early, void *ws, int num_sms, cudaStream_t st) {
   RowsArgs a;
   a.p = p;
   a.q = static_cast<const uint16_t *>(q);
@@ -718,10 +852,9 @@ cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *o
   a.ws_ml = reinterpret_cast<float *>(w + kPagedRowBlocks * 4);
   a.ws_o = reinterpret_cast<float *>(w + kPagedRowBlocks * 4 +
                                      2 * kPagedRowBlocks * kPagedFewRows * 8);
-  a.min_units = 32;
-  a.snap = 8;
   a.stall_limit = debug_stall_limit();
   a.few = few;
+  a.early = early;
   const int64_t most = few;
   // one tile of 8 rows when no sequence has more, two otherwise
   if (p.d == 128) {
