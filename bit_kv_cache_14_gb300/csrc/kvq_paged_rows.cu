@@ -8,7 +8,7 @@
 //
 //  * Split: the tiles (two 16-token atoms, one at 8 bits) of all (sequence,
 //    head) pairs form one list, cut into equal contiguous ranges, one per block;
-//    inside a block the eight warps share each pair's tiles evenly.  Pairs that
+//    inside a block the six warps share each pair's tiles evenly.  Pairs that
 //    end up in several blocks leave partials (m, l, o), and the block that
 //    finishes a pair last joins them in block order, so results do not depend
 //    on timing.
@@ -39,7 +39,7 @@ int debug_stall_limit();
 
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 6;
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kRowWaitLimit = 1 << 24;
 constexpr float kNoRef = -1e30f;
@@ -121,6 +121,11 @@ __device__ __forceinline__ void lds_words(const uint8_t *src, uint32_t (&w)[N]) 
 }
 
 
+// 64-bit quotients of numbers that are small almost always.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 // Where a unit index lies: sequence, head, offset inside the pair.
 struct Place {
   int b, h, off, tiles;
@@ -131,7 +136,7 @@ __device__ __forceinline__ Place locate(const int64_t *prefix, int H, int64_t x,
   u.b = b;
   u.tiles = (int)(prefix[b + 1] - prefix[b]);
   const int64_t r = x - H * prefix[b];
-  u.h = (int)(r / u.tiles);
+  u.h = (int)div64(r, u.tiles);
   u.off = (int)(r - (int64_t)u.h * u.tiles);
   return u;
 }
@@ -174,7 +179,14 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   constexpr int KW = RB / 16, VW = (RB / 8 + 3) / 4;  // words of a key quarter, a value eighth
   constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int sh_flag, sh_first, sh_last;
+  // pairs this block shares with others: 0 one that began before it, 1 one that
+  // goes on behind it
+  struct Shared {
+    int64_t pair0, pair1;
+    int row0, rows, h, first, last, join;
+  };
+  __shared__ Shared shared_pair[2];
+  int n_shared = 0;  // bit per entry
   const Paged &p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, j = lane & 3;
   uint8_t *ring = smem + warp * S * TB;
@@ -234,7 +246,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   }
   const int H = p.H;
   const int64_t total = H * prefix[p.B];
-  const int64_t U = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)(2 * kSnap + 1));
+  const int64_t U = max(div64(total + gridDim.x - 1, gridDim.x), (int64_t)(2 * kSnap + 1));
   const bool by_piece = (int64_t)H * pieces[p.B] <= gridDim.x;
   int64_t x0, x1;
   int first_b, c_first = blockIdx.x, c_last = blockIdx.x;  // by_piece: the blocks of the pair
@@ -344,6 +356,24 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   if (!dead)
     for (int i = 0; i < S && more; ++i) issue();
 
+  auto store = [&](int first_row, int h, int r, int quad, float4 v, float sum) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint2 w2;
+    if (p.bf16) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+      w2 = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                      *reinterpret_cast<const uint32_t *>(&hi));
+    } else {
+      w2 = make_uint2(h2u(__floats2half2_rn(v.x * inv, v.y * inv)),
+                      h2u(__floats2half2_rn(v.z * inv, v.w * inv)));
+    }
+    const int64_t t = first_row + r / p.rg;
+    if (t < p.T)
+      *reinterpret_cast<uint2 *>(a.out + (t * p.Hq + h * p.rg + r % p.rg) * D + 4 * quad) = w2;
+  };
+  constexpr int kQuads = D / 4;
+
   // ---- consume side, segment by segment
   int b = first_b;
   for (int64_t x = x0; x < x1;) {
@@ -358,6 +388,15 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     // newest position row r may see; every row's is below len
     const int64_t pos0 = (int64_t)p.lens[b] - tokens;
 
+    // the next pair's queries come to L2 meanwhile
+    if (x + n < x1 && warp == 0) {
+      const Place v = locate(prefix, H, x + n, b);
+      const int rows_v = (p.cu[v.b + 1] - p.cu[v.b]) * p.rg;
+      if (lane < rows_v)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            a.q + (int64_t)(p.cu[v.b] + lane / p.rg) * a.qs +
+            (int64_t)(v.h * p.rg + lane % p.rg) * D));
+    }
     // queries: lane (g, j) holds, of row 8*nt + g, channels 32*G + 8*j .. + 7,
     // scaled so that the row's largest is in [2^8, 2^9)
     uint32_t qf[NT][NG][4], qsum[NT];
@@ -531,9 +570,17 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
           for (int i = 0; i < 4; ++i) {
             // relative to the reference
             t[nt][i] = fmaf(t[nt][i], F[nt][i & 1], -rf[nt][i & 1]);
-            if (masked && pos + t0 + 8 * (i >> 1) > limit[nt][i & 1]) t[nt][i] = -INFINITY;
-            over |= t[nt][i] > slack;
           }
+        if (masked) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (pos + t0 + 8 * (i >> 1) > limit[nt][i & 1]) t[nt][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          over |= fmaxf(fmaxf(t[nt][0], t[nt][1]), fmaxf(t[nt][2], t[nt][3])) > slack;
         {
           __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&vs[0][0]),
                               *reinterpret_cast<const __half2 *>(&vs[1][0]));
@@ -654,8 +701,8 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       if (more) issue();
     }
 
-    // ---- the block's state of this segment: warps 4-7 leave (reference, l, o)
-    // in shared memory, warps 0-3 join theirs to it, and the four are then
+    // ---- the block's state of this segment: half the warps leave (reference,
+    // l, o) in shared memory, the others join theirs to it, and those are then
     // joined slice by slice
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -715,40 +762,8 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       }
       __syncthreads();
     }
-    // which blocks share the pair
     const int64_t pair0 = x - u.off, pair1 = pair0 + u.tiles;
     const bool whole = pair0 >= x0 && pair1 <= x1;
-    constexpr int kQuads = D / 4;
-    if (!whole && !by_piece) {
-      if (tid == 0) {
-        int c = (int)(pair0 / U);
-        while (border(prefix, p.B, H, total, U, c) > pair0) --c;
-        while (border(prefix, p.B, H, total, U, c + 1) <= pair0) ++c;
-        sh_first = c;
-        c = (int)((pair1 - 1) / U);
-        while (border(prefix, p.B, H, total, U, c) >= pair1) --c;
-        while (border(prefix, p.B, H, total, U, c + 1) < pair1) ++c;
-        sh_last = c;
-      }
-      __syncthreads();
-      c_first = sh_first, c_last = sh_last;
-    }
-    auto store = [&](int r, int quad, float4 v, float sum) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      uint2 w2;
-      if (p.bf16) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-        w2 = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                        *reinterpret_cast<const uint32_t *>(&hi));
-      } else {
-        w2 = make_uint2(h2u(__floats2half2_rn(v.x * inv, v.y * inv)),
-                        h2u(__floats2half2_rn(v.z * inv, v.w * inv)));
-      }
-      const int64_t t = row0 + r / p.rg;
-      if (t < p.T)
-        *reinterpret_cast<uint2 *>(a.out + (t * p.Hq + u.h * p.rg + r % p.rg) * D + 4 * quad) = w2;
-    };
     const int my_slot = 2 * blockIdx.x + (pair0 >= x0 ? 1 : 0);
     for (int i = tid; i < rows * kQuads; i += kRowThreads) {
       const int r = i / kQuads, quad = i % kQuads;
@@ -773,7 +788,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
         v.w += f * y.w;
       }
       if (whole) {
-        store(r, quad, v, sum);
+        store(row0, u.h, r, quad, v, sum);
       } else {
         *reinterpret_cast<float4 *>(a.ws_o + ((int64_t)my_slot * kRows + r) * D + 4 * quad) = v;
         if (quad == 0)
@@ -782,38 +797,69 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       }
     }
     if (!whole) {
-      __threadfence();
-      __syncthreads();
+      const int e = pair0 >= x0;
+      n_shared |= 1 << e;
       if (tid == 0) {
-        const int before = atomicAdd(&a.ws_count[c_first], 1);
-        sh_flag = before == c_last - c_first;
-        if (sh_flag) a.ws_count[c_first] = 0;
-      }
-      __syncthreads();
-      if (sh_flag) {
-        __threadfence();
-        for (int i = tid; i < rows * kQuads; i += kRowThreads) {
-          const int r = i / kQuads, quad = i % kQuads;
-          float m = kNoRef, sum = 0.0f;
-          float4 v = make_float4(0, 0, 0, 0);
-          for (int c = c_first; c <= c_last; ++c) {
-            const int64_t at = (int64_t)(2 * c + (c == c_first)) * kRows + r;
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ws_ml + at * 2));
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + at * D + 4 * quad));
-            const float nm = fmaxf(m, ml.x), f = exp2_approx(m - nm), f2 = exp2_approx(ml.x - nm);
-            m = nm;
-            sum = sum * f + f2 * ml.y;
-            v.x = v.x * f + f2 * y.x;
-            v.y = v.y * f + f2 * y.y;
-            v.z = v.z * f + f2 * y.z;
-            v.w = v.w * f + f2 * y.w;
-          }
-          store(r, quad, v, sum);
-        }
+        Shared &sp = shared_pair[e];
+        sp.pair0 = pair0, sp.pair1 = pair1;
+        sp.row0 = row0, sp.rows = rows, sp.h = u.h;
       }
     }
     __syncthreads();  // the merge buffer is free for the next segment
     x += n;
+  }
+
+  // ---- shared pairs, once all of the block's work is done: the block that
+  // arrives last joins the parts, in block order
+  if (n_shared) {
+    __threadfence();
+    __syncthreads();
+    const int e = tid >> 5;
+    if (e < 2 && lane == 0 && (n_shared >> e & 1)) {
+      Shared &sp = shared_pair[e];
+      int first = c_first, last = c_last;
+      if (!by_piece) {
+        // a pair that began here, or ends here, has its first or last part here
+        if (sp.pair0 < x0) {
+          first = (int)div64(sp.pair0, U);
+          while (border(prefix, p.B, H, total, U, first) > sp.pair0) --first;
+          while (border(prefix, p.B, H, total, U, first + 1) <= sp.pair0) ++first;
+        }
+        if (sp.pair1 > x1) {
+          last = (int)div64(sp.pair1 - 1, U);
+          while (border(prefix, p.B, H, total, U, last) >= sp.pair1) --last;
+          while (border(prefix, p.B, H, total, U, last + 1) < sp.pair1) ++last;
+        }
+      }
+      sp.first = first, sp.last = last;
+      sp.join = atomicAdd(&a.ws_count[first], 1) == last - first;
+      if (sp.join) a.ws_count[first] = 0;
+    }
+    __syncthreads();
+    for (int e2 = 0; e2 < 2; ++e2) {
+      if (!(n_shared >> e2 & 1) || !shared_pair[e2].join) continue;
+      const Shared sp = shared_pair[e2];
+      __threadfence();
+      for (int i = tid; i < sp.rows * kQuads; i += kRowThreads) {
+        const int r = i / kQuads, quad = i % kQuads;
+        float m = kNoRef, sum = 0.0f;
+        float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int c = sp.first; c <= sp.last; ++c) {
+          const int64_t at = (int64_t)(2 * c + (c == sp.first)) * kRows + r;
+          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ws_ml + at * 2));
+          const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + at * D + 4 * quad));
+          const float nm = fmaxf(m, ml.x), f = exp2_approx(m - nm), f2 = exp2_approx(ml.x - nm);
+          m = nm;
+          sum = sum * f + f2 * ml.y;
+          v.x = v.x * f + f2 * y.x;
+          v.y = v.y * f + f2 * y.y;
+          v.z = v.z * f + f2 * y.z;
+          v.w = v.w * f + f2 * y.w;
+        }
+        store(sp.row0, sp.h, r, quad, v, sum);
+      }
+    }
   }
   // a warp that gave up leaves no copy of its own in flight
   if (dead)
