@@ -909,17 +909,17 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       const float F = fs[r];  // (rows of this warp: written by this warp)
       const int row = row_first + r;
       const bool in = row < rows;
-      const int limit = in ? (int)min(it->pos0 + row / p.rg, (int64_t)it->len - 1) : -1;
+      // (rows behind the last have queries of 0 and no output: nothing to hide)
+      const int limit = (int)min(in ? it->pos0 + row / p.rg : (int64_t)it->len, (int64_t)it->len - 1);
       // newest position every row of the tile sees (its first row's)
       const int least = (int)min(it->pos0 + row_first / p.rg, (int64_t)it->len - 1);
-      const bool ragged = __any_sync(0xffffffffu, !in);
       float ref = kNoRef, l = 0.0f;  // reference and sum of the row's weights
       float over = 0.0f;             // by how much the last step's scores passed it
       for (int j = j0; j < j1; ++j, ++step) {
         if (!(ok = wait_warp(bar_s(i), sn & 1))) break;
         tc_fence_after();
         const uint32_t bad = steps[step % kSteps].bad;  // a bit per 16 tokens
-        const bool masked = j * kStep + kStep - 1 > least || ragged || bad != 0;
+        const bool masked = j * kStep + kStep - 1 > least || bad != 0;
         // these scores were issued after the sums of the earlier steps and are
         // here, so those are complete and O may be scaled
         auto rescale = [&](float f) {

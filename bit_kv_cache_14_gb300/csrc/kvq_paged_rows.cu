@@ -8,13 +8,13 @@
 //
 //  * Split: the tiles (two 16-token atoms, one at 8 bits) of all (sequence,
 //    head) pairs form one list, cut into equal contiguous ranges, one per block;
-//    inside a block the six warps share each pair's tiles evenly.  Pairs that
+//    inside a block the six or eight warps share each pair's tiles evenly.  Pairs that
 //    end up in several blocks leave partials (m, l, o), and the block that
 //    finishes a pair last joins them in block order, so results do not depend
 //    on timing.
 //  * A warp streams its tiles through a ring of shared-memory slots, one
 //    cp.async.bulk per tile (contiguous by layout; one per atom where pages hold
-//    one), page numbers read one tile ahead of their use.
+//    one), 32 tiles' page numbers read at a time, ahead of their use.
 //  * Keys: S^T[token][row] on mma.sync m16n8k16 with the raw codes as the A
 //    operand: a masked code in the low ten bits of a half is the fp16
 //    subnormal code * 2^(bit position) * 2^-24, exactly; the query operand
@@ -39,8 +39,6 @@ int debug_stall_limit();
 
 namespace {
 
-constexpr int kRowWarps = 6;
-constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kRowWaitLimit = 1 << 24;
 constexpr float kNoRef = -1e30f;
 
@@ -60,6 +58,7 @@ struct RowsArgs {
 
 template <int D, int BITS, int NT>
 struct RowsCfg {
+  static constexpr int kRowWarps = NT == 1 ? 6 : 8, kRowThreads = 32 * kRowWarps;
   static constexpr int RB = D * BITS / 8, SB = 4 * D / kPagedGroup, NG = D / kPagedGroup;
   static constexpr int AB = 2 * kAtom * (RB + SB);
   static constexpr int kBlocks = NT == 1 ? 2 : 1;  // per SM
@@ -171,10 +170,11 @@ __device__ __forceinline__ int64_t border(const int64_t *prefix, int B, int H, i
 }
 
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kRowThreads, RowsCfg<D, BITS, NT>::kBlocks)
+__global__ void __launch_bounds__(RowsCfg<D, BITS, NT>::kRowThreads, RowsCfg<D, BITS, NT>::kBlocks)
 paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   using C = RowsCfg<D, BITS, NT>;
   constexpr int RB = C::RB, SB = C::SB, NG = C::NG, S = C::S;
+  constexpr int kRowWarps = C::kRowWarps, kRowThreads = C::kRowThreads;
   constexpr int TA = C::TA, TB = C::TB, kTile = TA * kAtom;
   constexpr int KW = RB / 16, VW = (RB / 8 + 3) / 4;  // words of a key quarter, a value eighth
   constexpr int kRows = 8 * NT;
@@ -280,40 +280,75 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     dead = true;
   }
 
+  // ---- queries of a pair: lane (g, j) holds, of row 8*nt + g, channels 32*G +
+  // 8*j .. + 7.  Loaded ahead: the first pair's before its tiles, the next
+  // pair's before this one's join.
+  uint4 qraw[NT][NG];
+  auto load_queries = [&](int64_t x, int b) {
+    const Place u = locate(prefix, H, x, b);
+    const int row0 = p.cu[u.b], rows = (p.cu[u.b + 1] - row0) * p.rg;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      const uint16_t *src = a.q + (int64_t)(row0 + r / p.rg) * a.qs +
+                            (int64_t)(u.h * p.rg + r % p.rg) * D + 8 * j;
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        qraw[nt][G] = make_uint4(0, 0, 0, 0);
+        if (r < rows) qraw[nt][G] = __ldg(reinterpret_cast<const uint4 *>(src + 32 * G));
+      }
+    }
+  };
+  load_queries(x0, first_b);
+
   // ---- fetch side: this warp's tiles of every segment of [x0, x1) in turn.
-  // (fb, fh): the pair being fetched; f0: next tile; pid: its pages, read ahead
+  // (fb, fh): the pair being fetched; [f0, f1): its tiles to come
   int64_t fx = x0;
   int fb = first_b, fh = 0, f0 = 0, f1 = 0, flen = 0;
   const int page_log = __ffs(p.page) - 1;
-  int pid[TA];
-  const int32_t *row = nullptr;  // the sequence's block table
+  // Page numbers: lane k holds those of tile pbase + k, the next 32 tiles' are
+  // on their way.  (A pair that holds no tokens has one tile without a page: any
+  // entry.)
+  int pids[TA], pnext[TA], pbase = 0;
+  auto read_pids = [&](int first, int (&to)[TA]) {
+    const int t = (first + lane) * kTile;
+    const int32_t *row = p.table + fb * p.width;
+#pragma unroll
+    for (int i = 0; i < TA; ++i) to[i] = -1;
+    if (first + lane < f1) {
+      to[0] = __ldg(row + (t >> page_log));
+      if (TA == 2) {
+        to[TA - 1] = to[0];
+        if (p.page == kAtom) to[TA - 1] = t + kAtom < flen ? __ldg(row + (t >> page_log) + 1) : -1;
+      }
+    }
+  };
   auto fetch_next = [&]() {  // moves to the next tile; false at the end
-    while (f0 == f1) {
-      if (fx >= x1) return false;
-      const Place u = locate(prefix, H, fx, fb);
-      const int n = (int)min((int64_t)(u.tiles - u.off), x1 - fx);
-      fb = u.b, fh = u.h;
-      f0 = u.off + (int)((int64_t)n * warp / kRowWarps);
-      f1 = u.off + (int)((int64_t)n * (warp + 1) / kRowWarps);
-      fx += n;
-      row = p.table + fb * p.width;
+    if (f0 == f1) {
+      do {
+        if (fx >= x1) return false;
+        const Place u = locate(prefix, H, fx, fb);
+        const int n = (int)min((int64_t)(u.tiles - u.off), x1 - fx);
+        fb = u.b, fh = u.h;
+        f0 = u.off + n * warp / kRowWarps;
+        f1 = u.off + n * (warp + 1) / kRowWarps;
+        fx += n;
+      } while (f0 == f1);
       flen = (int)min((int64_t)max(p.lens[fb], 0), p.width * p.page);
+      pbase = f0;
+      read_pids(f0, pids);
+      read_pids(f0 + 32, pnext);
+    } else if (f0 - pbase == 32) {
+      pbase = f0;
+#pragma unroll
+      for (int i = 0; i < TA; ++i) pids[i] = pnext[i];
+      read_pids(f0 + 32, pnext);
     }
     return true;
-  };
-  auto read_pid = [&]() {
-    // (a pair that holds no tokens has one tile without a page: any entry)
-    const int t = f0 * kTile;
-    pid[0] = __ldg(row + (t >> page_log));
-    if (TA == 2) {
-      pid[TA - 1] = pid[0];
-      if (p.page == kAtom) pid[TA - 1] = t + kAtom < flen ? __ldg(row + (t >> page_log) + 1) : -1;
-    }
   };
   int issue_slot = 0, in_flight = 0, slot = 0;
   uint32_t phase = 0, skip = 0;  // skip: TA bits per slot, the atom's page does not exist
   bool more = fetch_next();
-  if (more) read_pid();
   auto issue = [&]() {
     const uint8_t *src[TA];
     uint32_t gone = 0;
@@ -321,15 +356,13 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
                             (int64_t)(((f0 * kTile) & (p.page - 1)) / kAtom) * C::AB;
 #pragma unroll
     for (int i = 0; i < TA; ++i) {
-      const int64_t id = pid[i];
+      const int64_t id = __shfl_sync(0xffffffffu, pids[i], f0 - pbase);
       if (id < 0 || id >= p.n_pages) gone |= 1u << i;
       src[i] = p.pages + id * p.page_bytes + in_page;
     }
     const bool paired = TA == 1 || p.page > kAtom;  // one copy for the tile
-    // the next tile's page numbers are on their way while this one's copy starts
     ++f0;
     more = fetch_next();
-    if (more) read_pid();
     skip = (skip & ~(((1u << TA) - 1) << (TA * issue_slot))) | gone << (TA * issue_slot);
     if (lane == 0) {
       uint64_t *bar = &bars[issue_slot];
@@ -380,38 +413,24 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     const Place u = locate(prefix, H, x, b);
     b = u.b;
     const int n = (int)min((int64_t)(u.tiles - u.off), x1 - x);
-    const int a0 = u.off + (int)((int64_t)n * warp / kRowWarps);
-    const int a1 = u.off + (int)((int64_t)n * (warp + 1) / kRowWarps);
+    const int a0 = u.off + n * warp / kRowWarps;
+    const int a1 = u.off + n * (warp + 1) / kRowWarps;
     const int row0 = p.cu[b], tokens = p.cu[b + 1] - row0, rows = tokens * p.rg;
     const int64_t cap = p.width * p.page;
     const int len = (int)min((int64_t)max(p.lens[b], 0), cap);
     // newest position row r may see; every row's is below len
     const int64_t pos0 = (int64_t)p.lens[b] - tokens;
 
-    // the next pair's queries come to L2 meanwhile
-    if (x + n < x1 && warp == 0) {
-      const Place v = locate(prefix, H, x + n, b);
-      const int rows_v = (p.cu[v.b + 1] - p.cu[v.b]) * p.rg;
-      if (lane < rows_v)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            a.q + (int64_t)(p.cu[v.b] + lane / p.rg) * a.qs +
-            (int64_t)(v.h * p.rg + lane % p.rg) * D));
-    }
-    // queries: lane (g, j) holds, of row 8*nt + g, channels 32*G + 8*j .. + 7,
-    // scaled so that the row's largest is in [2^8, 2^9)
+    // queries scaled so that the row's largest is in [2^8, 2^9)
     uint32_t qf[NT][NG][4], qsum[NT];
     float F[NT][2];
     int limit[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = 8 * nt + g;
-      const bool in = r < rows;
-      const uint16_t *src = a.q + (int64_t)(row0 + (in ? r / p.rg : 0)) * a.qs +
-                            (int64_t)(u.h * p.rg + (in ? r % p.rg : 0)) * D + 8 * j;
       float f[NG][8], big = 0.0f;
 #pragma unroll
       for (int G = 0; G < NG; ++G) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 32 * G));
+        const uint4 w = qraw[nt][G];
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -423,7 +442,6 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
             f[G][2 * i] = v.x;
             f[G][2 * i + 1] = v.y;
           }
-          if (!in) f[G][2 * i] = f[G][2 * i + 1] = 0.0f;
           big = fmaxf(big, fmaxf(fabsf(f[G][2 * i]), fabsf(f[G][2 * i + 1])));
         }
       }
@@ -489,47 +507,54 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
         break;
       }
       const uint8_t *at_s = ring + slot * TB;
-      const uint32_t gone = skip >> (TA * slot);
-#pragma unroll 1
-      for (int sub = 0; sub < TA; ++sub, at_s += C::AB) {
-        const int pos = at * kTile + sub * kAtom;
-        if (pos >= len) break;  // (or the one tile of a sequence without tokens)
-        if (gone >> sub & 1) {
-          if (lane == 0) paged_error(p, KVQ_EPAGE);
-          continue;
-        }
-        // token of fragment row r < 8: (r >> 1) + 4 * (r & 1); rows 8.. 8 more
-        const int t0 = (g >> 1) + 4 * (g & 1);
-        uint32_t k0[KW], k1[KW], ks[2][NG], vs[2][NG];
-        lds_words(at_s + t0 * RB + j * (RB / 4), k0);
-        lds_words(at_s + (t0 + 8) * RB + j * (RB / 4), k1);
-        // statistics of a token: NG scales then NG zeros, as pairs
-        const uint8_t *st = at_s + 2 * kAtom * RB;
-        lds_words(st + t0 * SB, ks[0]);
-        lds_words(st + (t0 + 8) * SB, ks[1]);
-        lds_words(st + kAtom * SB + t0 * SB, vs[0]);
-        lds_words(st + kAtom * SB + (t0 + 8) * SB, vs[1]);
-        const bool masked = pos + kAtom - 1 > least;
+      const uint32_t gone = skip >> (TA * slot) & ((1u << TA) - 1);
+      const int pos = at * kTile;
+      // token of fragment row r < 8 of an atom: (r >> 1) + 4 * (r & 1); rows 8..
+      // 8 more
+      const int t0 = (g >> 1) + 4 * (g & 1);
+      // masked: some token is hidden from some row, or is not there at all
+      const bool masked = pos + kTile - 1 > least || gone != 0;
+      if (gone != 0 && pos < len && lane == 0) {
+#pragma unroll
+        for (int u = 0; u < TA; ++u)
+          if ((gone >> u & 1) && pos + u * kAtom < len) paged_error(p, KVQ_EPAGE);
+      }
+      auto absent = [&](int u, int i) {  // token t0 + 8 * i of atom u
+        return pos + u * kAtom + t0 + 8 * i >= len || (gone >> u & 1);
+      };
+      // statistics of a token: NG scales then NG zeros, as pairs; 0 where there
+      // is no token (such slots hold anything)
+      auto load_stats = [&](int u, int which, uint32_t (&st)[2][NG]) {
+        const uint8_t *at = at_s + u * C::AB + 2 * kAtom * RB + which * kAtom * SB + t0 * SB;
+        lds_words(at, st[0]);
+        lds_words(at + 8 * SB, st[1]);
         if (masked) {
-          // slots behind the last token hold anything
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (pos + t0 + 8 * i >= len) {
+            if (absent(u, i)) {
 #pragma unroll
-              for (int n2 = 0; n2 < NG; ++n2) ks[i][n2] = vs[i][n2] = 0u;
+              for (int k = 0; k < NG; ++k) st[i][k] = 0u;
             }
         }
-        // ---- scores
-        float t[NT][4];
+      };
+      // ---- scores, relative to the reference
+      float t[TA][NT][4];
+      bool over = fresh != 0;
+      __half2 smax = __float2half2_rn(0.0f);
+#pragma unroll
+      for (int u = 0; u < TA; ++u) {
+        uint32_t k0[KW], k1[KW], ks[2][NG];
+        lds_words(at_s + u * C::AB + t0 * RB + j * (RB / 4), k0);
+        lds_words(at_s + u * C::AB + (t0 + 8) * RB + j * (RB / 4), k1);
+        load_stats(u, 0, ks);
         {
           const uint32_t z0 = NG == 4 ? (j & 1 ? ks[0][3 % NG] : ks[0][2 % NG]) : ks[0][1];
           const uint32_t z1 = NG == 4 ? (j & 1 ? ks[1][3 % NG] : ks[1][2 % NG]) : ks[1][1];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float zt[4];
-            mma1688(zt, z0, z1, qsum[nt]);
+            mma1688(t[u][nt], z0, z1, qsum[nt]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[nt][i] = zt[i] * (1.0f / kSub);
+            for (int i = 0; i < 4; ++i) t[u][nt][i] *= 1.0f / kSub;
           }
         }
         uint32_t k08[KW], k18[KW];
@@ -554,87 +579,93 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
           }
           const float2 s0 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[0][G / 2]));
           const float2 s1 = __half22float2(*reinterpret_cast<const __half2 *>(&ks[1][G / 2]));
-          const float f0_ = G & 1 ? s0.y : s0.x, f1_ = G & 1 ? s1.y : s1.x;
+          const float fa = G & 1 ? s0.y : s0.x, fb_ = G & 1 ? s1.y : s1.x;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            t[nt][0] = fmaf(f0_, c[nt][0], t[nt][0]);
-            t[nt][1] = fmaf(f0_, c[nt][1], t[nt][1]);
-            t[nt][2] = fmaf(f1_, c[nt][2], t[nt][2]);
-            t[nt][3] = fmaf(f1_, c[nt][3], t[nt][3]);
+            t[u][nt][0] = fmaf(fa, c[nt][0], t[u][nt][0]);
+            t[u][nt][1] = fmaf(fa, c[nt][1], t[u][nt][1]);
+            t[u][nt][2] = fmaf(fb_, c[nt][2], t[u][nt][2]);
+            t[u][nt][3] = fmaf(fb_, c[nt][3], t[u][nt][3]);
           }
         }
-        bool over = fresh != 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // relative to the reference
-            t[nt][i] = fmaf(t[nt][i], F[nt][i & 1], -rf[nt][i & 1]);
-          }
+          for (int i = 0; i < 4; ++i)
+            t[u][nt][i] = fmaf(t[u][nt][i], F[nt][i & 1], -rf[nt][i & 1]);
         if (masked) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (pos + t0 + 8 * (i >> 1) > limit[nt][i & 1]) t[nt][i] = -INFINITY;
+              if (absent(u, i >> 1) || pos + u * kAtom + t0 + 8 * (i >> 1) > limit[nt][i & 1])
+                t[u][nt][i] = -INFINITY;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          over |= fmaxf(fmaxf(t[nt][0], t[nt][1]), fmaxf(t[nt][2], t[nt][3])) > slack;
-        {
-          __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&vs[0][0]),
-                              *reinterpret_cast<const __half2 *>(&vs[1][0]));
-          if (NG == 4)
-            m = __hmax2(m, __hmax2(*reinterpret_cast<const __half2 *>(&vs[0][1]),
-                                   *reinterpret_cast<const __half2 *>(&vs[1][1])));
-          over |= !__hble2(m, *reinterpret_cast<const __half2 *>(&e2));
-          if (__any_sync(0xffffffffu, over)) {
-            // move the reference: to the largest score, and E to the scales
-            float sm = fmaxf(__low2float(m), __high2float(m));
+          over |= fmaxf(fmaxf(t[u][nt][0], t[u][nt][1]), fmaxf(t[u][nt][2], t[u][nt][3])) > slack;
+        // the largest value scale
+        uint32_t vs[2][NG];
+        load_stats(u, 1, vs);
 #pragma unroll
-            for (int s = 16; s; s >>= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, s));
-            const int En = sm > 0.0f ? max(E, ((__float_as_int(sm) >> 23) & 255) - 126) : E;
-            const uint32_t top = h2u(__float2half2_rn(__int_as_float((127 + En) << 23)));
-            e2 = En > 15 ? 0x7bff7bffu : top;
+        for (int k = 0; k < NG / 2; ++k)
+          smax = __hmax2(smax, __hmax2(*reinterpret_cast<const __half2 *>(&vs[0][k]),
+                                       *reinterpret_cast<const __half2 *>(&vs[1][k])));
+      }
+      over |= !__hble2(smax, *reinterpret_cast<const __half2 *>(&e2));
+      if (__any_sync(0xffffffffu, over)) {
+        // move the reference: to the largest score, and E to the scales
+        float sm = fmaxf(__low2float(smax), __high2float(smax));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int s = 16; s; s >>= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, s));
+        const int En = sm > 0.0f ? max(E, ((__float_as_int(sm) >> 23) & 255) - 126) : E;
+        const uint32_t top = h2u(__float2half2_rn(__int_as_float((127 + En) << 23)));
+        e2 = En > 15 ? 0x7bff7bffu : top;
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                float mx = fmaxf(t[nt][s], t[nt][2 + s]);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k = 4; k < 32; k <<= 1)
-                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-                // from the reference to the larger of itself and the scores, and
-                // from the old E to the new; a row without scores stays
-                const bool first = fresh >> (2 * nt + s) & 1;
-                float by = fmaxf(mx + (float)E, 0.0f) + (float)(En - E);
-                if (first) by = mx == -INFINITY ? 0.0f : mx + (float)En;
-                if (mx != -INFINITY) fresh &= ~(1u << (2 * nt + s));
-                const float f = first ? 0.0f : exp2_approx(-by);
-                rf[nt][s] += by;
-                t[nt][s] -= by;
-                t[nt][2 + s] -= by;
-                l[nt][s] *= f;
+          for (int s = 0; s < 2; ++s) {
+            float mx = fmaxf(t[0][nt][s], t[0][nt][2 + s]);
+            if (TA == 2) mx = fmaxf(mx, fmaxf(t[TA - 1][nt][s], t[TA - 1][nt][2 + s]));
 #pragma unroll
-                for (int G = 0; G < NG; ++G) {
-                  za[G][nt][s] *= f;
-                  o[G][0][nt][s] *= f;
-                  o[G][0][nt][2 + s] *= f;
-                  o[G][1][nt][s] *= f;
-                  o[G][1][nt][2 + s] *= f;
-                }
-              }
-            E = En;
-            slack = kSlack - (float)E;
+            for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            // from the reference to the larger of itself and the scores, and
+            // from the old E to the new; a row without scores stays
+            const bool first = fresh >> (2 * nt + s) & 1;
+            float by = fmaxf(mx + (float)E, 0.0f) + (float)(En - E);
+            if (first) by = mx == -INFINITY ? 0.0f : mx + (float)En;
+            if (mx != -INFINITY) fresh &= ~(1u << (2 * nt + s));
+            const float f = first ? 0.0f : exp2_approx(-by);
+            rf[nt][s] += by;
+#pragma unroll
+            for (int u = 0; u < TA; ++u) {
+              t[u][nt][s] -= by;
+              t[u][nt][2 + s] -= by;
+            }
+            l[nt][s] *= f;
+#pragma unroll
+            for (int G = 0; G < NG; ++G) {
+              za[G][nt][s] *= f;
+              o[G][0][nt][s] *= f;
+              o[G][0][nt][2 + s] *= f;
+              o[G][1][nt][s] *= f;
+              o[G][1][nt][2 + s] *= f;
+            }
           }
-        }
+        E = En;
+        slack = kSlack - (float)E;
+      }
+#pragma unroll
+      for (int u = 0; u < TA; ++u) {
         // ---- weights
+        uint32_t vs[2][NG];
+        load_stats(u, 1, vs);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t[nt][i] = exp2_approx(t[nt][i]);
-          l[nt][0] += t[nt][0] + t[nt][2];
-          l[nt][1] += t[nt][1] + t[nt][3];
+          for (int i = 0; i < 4; ++i) t[u][nt][i] = exp2_approx(t[u][nt][i]);
+          l[nt][0] += t[u][nt][0] + t[u][nt][2];
+          l[nt][1] += t[u][nt][1] + t[u][nt][3];
         }
         uint32_t w[NG][NT][2];
 #pragma unroll
@@ -649,14 +680,15 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
           const float ya = G & 1 ? z0.y : z0.x, yb = G & 1 ? z1.y : z1.x;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            w[G][nt][0] = movm(h2u(__floats2half2_rn(t[nt][0] * sa, t[nt][1] * sa)));
-            w[G][nt][1] = movm(h2u(__floats2half2_rn(t[nt][2] * sb, t[nt][3] * sb)));
-            za[G][nt][0] = fmaf(t[nt][0], ya, fmaf(t[nt][2], yb, za[G][nt][0]));
-            za[G][nt][1] = fmaf(t[nt][1], ya, fmaf(t[nt][3], yb, za[G][nt][1]));
+            const float(&q4)[4] = t[u][nt];
+            w[G][nt][0] = movm(h2u(__floats2half2_rn(q4[0] * sa, q4[1] * sa)));
+            w[G][nt][1] = movm(h2u(__floats2half2_rn(q4[2] * sb, q4[3] * sb)));
+            za[G][nt][0] = fmaf(q4[0], ya, fmaf(q4[2], yb, za[G][nt][0]));
+            za[G][nt][1] = fmaf(q4[1], ya, fmaf(q4[3], yb, za[G][nt][1]));
           }
         }
         // ---- values: tokens (j, j + 4) and (j + 8, j + 12), eighth g
-        const uint8_t *vc = at_s + kAtom * RB + g * (RB / 8);
+        const uint8_t *vc = at_s + u * C::AB + kAtom * RB + g * (RB / 8);
         uint32_t v[4][VW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -665,12 +697,12 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
           else
             lds_words(vc + (j + 4 * i) * RB, v[i]);
         }
-        // bits of a half: 16, or 8 for the two-byte eighths of d = 64, 2 bits
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t xa[VW], xb[VW], xa8[VW], xb8[VW];
 #pragma unroll
           for (int i = 0; i < VW; ++i) {
+            // (the two-byte eighths of d = 64, 2 bits: both halves in one)
             const uint32_t sel = RB / 8 == 2 ? 0x5410u : e ? 0x7632u : 0x5410u;
             xa[i] = __byte_perm(v[0][i], v[1][i], sel);
             xb[i] = __byte_perm(v[2][i], v[3][i], sel);
@@ -701,6 +733,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       if (more) issue();
     }
 
+    if (x + n < x1) load_queries(x + n, b);
     // ---- the block's state of this segment: half the warps leave (reference,
     // l, o) in shared memory, the others join theirs to it, and those are then
     // joined slice by slice
@@ -876,11 +909,11 @@ cudaError_t launch_as(RowsArgs &a, int num_sms, cudaStream_t st) {
   const int smem = C::smem(a.p.B);
   int occ = 0;
   auto kern = paged_rows_kernel<D, BITS, NT>;
-  cudaError_t e = kernel_setup(setup, kern, kRowThreads, smem, &occ);
+  cudaError_t e = kernel_setup(setup, kern, C::kRowThreads, smem, &occ);
   if (e != cudaSuccess) return e;
   int blocks = num_sms * occ;
   if (blocks > kPagedRowBlocks) blocks = kPagedRowBlocks;
-  return launch_dependent(kern, (unsigned)blocks, kRowThreads, smem, st, a.early, a);
+  return launch_dependent(kern, (unsigned)blocks, C::kRowThreads, smem, st, a.early, a);
 }
 
 }  // namespace
