@@ -77,17 +77,6 @@ __device__ __forceinline__ void paged_error(const Paged &p, int code) {
   atomicCAS(p.status, 0, code);
 }
 
-// Rows [0, min(cu[B], T)) are real.  Sequence of row t, or -1 for padding
-// (also for a cu_tokens array that does not increase around t).
-__device__ __forceinline__ int seq_of_row(const Paged &p, int64_t t) {
-  int lo = 0, hi = p.B;  // the largest b with cu[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu[mid] <= t) lo = mid; else hi = mid;
-  }
-  return (t >= p.cu[lo] && t < p.cu[lo + 1]) ? lo : -1;
-}
-
 // Position of row t of sequence b (negative: the row precedes its sequence).
 __device__ __forceinline__ int64_t row_position(const Paged &p, int b, int64_t t) {
   return (int64_t)p.lens[b] - p.cu[b + 1] + t;

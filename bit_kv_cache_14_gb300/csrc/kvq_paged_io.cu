@@ -9,23 +9,29 @@ namespace kvq {
 namespace {
 
 constexpr int kIoThreads = 256;
+constexpr int kIoBatch = 4;  // rows of a warp in flight
 
-template <int BF16>
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (BF16) {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+// The sequence of row t, found by the whole warp (32 candidates a round), or -1
+// for padding (also for a cu_tokens array that does not increase around t).
+__device__ __forceinline__ int warp_seq_of_row(const Paged &p, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = p.B;  // the largest b with cu[b] <= t
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, b < hi && p.cu[b] <= t);
+    if (le == 0) return -1;
+    lo += (31 - __clz(le)) * step;
+    hi = min(lo + step, hi);
   }
+  return (t >= p.cu[lo] && t < p.cu[lo + 1]) ? lo : -1;
 }
 
+// The two halves of a word as fp32.
+template <int BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if (BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
 // Two values rounded once to the 16-bit type, x0 in the low half.
 template <int BF16>
 __device__ __forceinline__ uint32_t pack2(float x0, float x1) {
@@ -37,212 +43,299 @@ __device__ __forceinline__ uint32_t pack2(float x0, float x1) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// clamp(rint((x - zero) / scale)), with one reciprocal per group.  The hardware
-// reciprocal is within 2^-23 of 1 / scale and each product or quotient is
-// rounded within 2^-24, so for quotients up to 2^9 the product differs from
-// the IEEE quotient by less than 2^-12 = kTieGuard: rint gives the same
-// integer for both unless the product lies that close to a half-integer,
-// where (and beyond 2^9, which the statistics exclude) the division decides.
+// Packed minimum, maximum (of numbers) and the maximum that keeps NaN.
+template <int BF16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if (BF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <int BF16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if (BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// One 16-bit input as the stored form takes it: saturated, NaN as 0.
+__device__ __forceinline__ float tame(float x) {
+  return x == x ? fminf(fmaxf(x, -kPagedLimit), kPagedLimit) : 0.0f;
+}
+
+// clamp(rint((x - zero) / scale)) by the IEEE division.
 template <int BITS>
-__device__ __forceinline__ uint32_t paged_code(float x, float zero, float scale, float inv) {
-  const float d = __fsub_rn(x, zero);
-  float r = __fmul_rn(d, inv);
-  const float f = __fsub_rn(r, floorf(r));
-  if (!(fabsf(r) < 512.0f) || fabsf(__fsub_rn(f, 0.5f)) < kTieGuard)
-    r = scale == 0.0f ? 0.0f : __fdiv_rn(d, scale);
-  r = fminf(fmaxf(rintf(r), 0.0f), (float)((1 << BITS) - 1));
-  return (uint32_t)r;
+__device__ __forceinline__ float careful_code(float x, float zero, float scale) {
+  const float r = scale == 0.0f ? 0.0f : rintf(__fdiv_rn(__fsub_rn(x, zero), scale));
+  return fminf(fmaxf(r, 0.0f), (float)((1 << BITS) - 1));
 }
 
 // A half warp (d = 128) or quarter warp (d = 64) holds the row of one head,
-// lane l its channels 8*l .. 8*l + 7: group l / 4, quarter j = l % 4 of the
+// lane l its channels 8*l .. 8*l + 7 (w): group l / 4, quarter j = l % 4 of the
 // key layout, eighths 2*j and 2*j + 1 of the value layout.
-template <int D, int BITS>
-__device__ __forceinline__ void quantize_row(const float (&xin)[8], int l, bool value,
-                                             uint8_t *codes, __half *stats) {
+//
+// What bounds it is the instructions per element (about 15 lane operations at
+// the rate HBM delivers), so: minima and maxima on packed pairs; one reciprocal
+// per group; rint by adding 1.5 * 2^23; codes put together as exact fp32 sums
+// code_k * 2^(k*bits).  The hardware reciprocal is within 2^-23 of 1 / scale
+// and each rounding within 2^-24, so the product is within 2^-13 of the IEEE
+// quotient for quotients below 2^8 + 1; the integer is the same for both unless
+// the product lies within kTieGuard = 2^-12 of a half-integer.  Threads that see
+// such a product, a scale under 2^-13 (where its own rounding could pass the
+// code range) or an input to tame go through the division.
+template <int D, int BITS, int BF16>
+__device__ __forceinline__ void quantize_row(uint4 w4, int l, bool value, uint8_t *codes,
+                                             __half *stats) {
   constexpr int NG = D / kPagedGroup;
   constexpr unsigned kAll = 0xffffffffu;
-  float x[8], mn, mx;
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  constexpr uint32_t kSign = 0x80008000u;
+  uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+  // magnitudes as integers: larger than LIMIT, infinite and NaN compare alike
+  constexpr uint32_t kTop = BF16 ? 0x4700u : 0x7800u;  // 32768
+  uint32_t big = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // NaN -> 0; fminf / fmaxf return their other operand for a NaN
-    const float c = xin[i] == xin[i] ? xin[i] : 0.0f;
-    x[i] = fminf(fmaxf(c, -kPagedLimit), kPagedLimit);
-    mn = i ? fminf(mn, x[i]) : x[i];
-    mx = i ? fmaxf(mx, x[i]) : x[i];
-  }
+  for (int i = 0; i < 4; ++i) big = __vmaxu2(big, w[i] & ~kSign);
+  const bool wild = (big & 0xffffu) > kTop || (big >> 16) > kTop;
+  const bool any_wild = __any_sync(kAll, wild);
+  if (any_wild) {
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(kAll, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2<BF16>(w[i]);
+      w[i] = pack2<BF16>(tame(x.x), tame(x.y));
+    }
   }
-  const __half s16 = __float2half_rn(
-      __fdiv_rn(__fsub_rn(mx, mn), (float)((1 << BITS) - 1)));
+  // (-min, max) of the group, packed
+  const uint32_t mx2 = max2<BF16>(max2<BF16>(w[0], w[1]), max2<BF16>(w[2], w[3]));
+  const uint32_t mn2 = min2<BF16>(min2<BF16>(w[0], w[1]), min2<BF16>(w[2], w[3])) ^ kSign;
+  uint32_t mm = max2<BF16>(__byte_perm(mn2, mx2, 0x5410), __byte_perm(mn2, mx2, 0x7632));
+  mm = max2<BF16>(mm, __shfl_xor_sync(kAll, mm, 1));
+  mm = max2<BF16>(mm, __shfl_xor_sync(kAll, mm, 2));
+  const float2 ends = unpack2<BF16>(mm);
+  const float mn = -ends.x, mx = ends.y;
+  const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), (float)((1 << BITS) - 1)));
   const __half z16 = __float2half_rn(canon_zero(mn));
   const float s = __half2float(s16), z = __half2float(z16);
   const float inv = recip_or_zero(s);
-  uint32_t c[8];
+  float c[8], far = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = paged_code<BITS>(x[i], z, s, inv);
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2<BF16>(w[i]);
+    const float r0 = __fmul_rn(__fsub_rn(x.x, z), inv), r1 = __fmul_rn(__fsub_rn(x.y, z), inv);
+    c[2 * i] = __fsub_rn(__fadd_rn(r0, kMagic), kMagic);
+    c[2 * i + 1] = __fsub_rn(__fadd_rn(r1, kMagic), kMagic);
+    far = fmaxf(far, fmaxf(fabsf(__fsub_rn(r0, c[2 * i])), fabsf(__fsub_rn(r1, c[2 * i + 1]))));
+  }
+  if (far > 0.5f - kTieGuard || s < 1.0f / 8192.0f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2<BF16>(w[i]);
+      c[2 * i] = careful_code<BITS>(x.x, z, s);
+      c[2 * i + 1] = careful_code<BITS>(x.y, z, s);
+    }
+  }
 
   const int grp = l >> 2, j = l & 3, e = grp & 1, h = grp >> 1;
   // Key words: pair k (channels 2k, 2k+1) at bit k*BITS of each 16-bit half.
   // Value words: this group's channels at bits i*BITS of half e, so the two
   // lanes of a pair of groups swap one eighth each and hold a full word.
-  uint32_t lo = 0, hi = 0;
+  float q[8];  // low half's four codes, then the high half's
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    lo |= (value ? c[k] : c[2 * k]) << (k * BITS);           // values: eighth 2j
-    hi |= (value ? c[4 + k] : c[2 * k + 1]) << (k * BITS);   // values: eighth 2j + 1
+    q[k] = value ? c[k] : c[2 * k];
+    q[4 + k] = value ? c[4 + k] : c[2 * k + 1];
+  }
+  auto sum2 = [&](int k) { return fmaf(q[k + 1], (float)(1 << BITS), q[k]); };
+  auto whole = [&](float x) { return __float_as_uint(x + kMagic) & 0x1ffffu; };
+  uint32_t lo, hi;
+  if (BITS == 8) {
+    lo = whole(sum2(0)) | whole(sum2(2)) << 16;
+    hi = whole(sum2(4)) | whole(sum2(6)) << 16;
+  } else {
+    lo = whole(fmaf(sum2(2), (float)(1 << (2 * BITS)), sum2(0)));
+    hi = whole(fmaf(sum2(6), (float)(1 << (2 * BITS)), sum2(4)));
   }
   // keys keep (lo, hi) = (even, odd channels); values trade with the lane of
   // the other group of the pair
   const uint32_t got = __shfl_xor_sync(kAll, e ? lo : hi, 4);
-  const uint32_t a = value ? (e ? got : lo) : lo;  // what goes to the low halves
-  const uint32_t b = value ? (e ? hi : got) : hi;  // and to the high halves
+  const uint32_t a = value && e ? got : lo;   // what goes to the low halves
+  const uint32_t b = value && !e ? got : hi;  // and to the high halves
   if (BITS == 8) {
-    const uint2 w = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-    // 8 channels: two words
+    const uint2 word = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     uint8_t *dst = value ? codes + (2 * j + e) * (D / 8) + h * 8 : codes + j * (D / 4) + grp * 8;
-    *reinterpret_cast<uint2 *>(dst) = w;
+    *reinterpret_cast<uint2 *>(dst) = word;
   } else if (BITS == 4) {
     uint8_t *dst = value ? codes + (2 * j + e) * (D / 16) + h * 4 : codes + j * (D / 8) + grp * 4;
     *reinterpret_cast<uint32_t *>(dst) = a | (b << 16);
   } else {
     // 2 bits: a word holds two groups (keys) or two pairs of groups (values)
     const int part = value ? h : e;
-    uint32_t w = (a | (b << 16)) << (8 * part);
-    const uint32_t other = __shfl_xor_sync(kAll, w, value ? 8 : 4);
+    const uint32_t word = (a | (b << 16)) << (8 * part);
+    const uint32_t other = __shfl_xor_sync(kAll, word, value ? 8 : 4);
     if (value && D == 64) {
       // one pair of groups: the eighth is two bytes
       *reinterpret_cast<uint16_t *>(codes + (2 * j + e) * 2) = (uint16_t)(a | (b << 8));
     } else if (part == 0) {
       uint8_t *dst = value ? codes + (2 * j + e) * (D / 32) : codes + j * (D / 16) + h * 4;
-      *reinterpret_cast<uint32_t *>(dst) = w | other;
+      *reinterpret_cast<uint32_t *>(dst) = word | other;
     }
   }
-  if (j == 0) {
-    stats[grp] = s16;
-    stats[NG + grp] = z16;
-  }
+  if (j < 2) stats[grp + NG * j] = j ? z16 : s16;
 }
 
-// One warp per (row, group of heads): a warp instruction covers the key and
-// the value of one head (d = 128) or of two (d = 64).
+// One warp per row and group of heads: a warp instruction covers the key and
+// the value of one head (d = 128) or of two (d = 64), kIoBatch of them in
+// flight.
 template <int D, int BITS, int BF16>
 __global__ void __launch_bounds__(kIoThreads)
-paged_write_kernel(Paged p, const uint16_t *k, int64_t ks, const uint16_t *v, int64_t vs,
-                   int head_groups) {
+paged_write_kernel(const __grid_constant__ Paged p, const uint16_t *k, int64_t ks,
+                   const uint16_t *v, int64_t vs, int groups) {
   constexpr int LR = D / 8;            // lanes of one row
   constexpr int HW = 32 / (2 * LR);    // heads per warp instruction
   constexpr int RB = D * BITS / 8, SB = 4 * D / kPagedGroup;
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * (kIoThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = item / head_groups;
+  int64_t t = item;
+  int h0 = 0;
+  if (groups > 1) t = item / groups, h0 = (int)(item % groups) * kIoBatch * HW;
   if (t >= p.T) return;
-  const int h = (int)(item % head_groups) * HW + (lane / (2 * LR)) % HW;
   const bool value = (lane / LR) & 1;
-  const int l = lane % LR;
-  const int b = seq_of_row(p, t);
+  const int l = lane % LR, hl = h0 + (lane / (2 * LR)) % HW;
+  const int b = warp_seq_of_row(p, t);
   if (b < 0) return;
   const int64_t pos = row_position(p, b, t);
   if (pos < 0) return;
+  const uint16_t *src = (value ? v + t * vs : k + t * ks) + 8 * l;
+  // (lanes past the last head repeat it and store the same bytes as the lanes
+  // that hold it)
+  uint4 w[kIoBatch];
+#pragma unroll
+  for (int i = 0; i < kIoBatch; ++i)
+    if (h0 + i * HW < p.H)
+      w[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)min(hl + i * HW, p.H - 1) * D));
   uint8_t *atom = atom_of(p, b, pos);
   if (!atom) return;
-  // (every exit above is the whole warp's; lanes past the last head repeat it
-  // and store the same bytes as the lanes that hold it)
-  const int hh = h < p.H ? h : p.H - 1;
-  const uint16_t *src = value ? v + t * vs : k + t * ks;
-  const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)hh * D) + l);
-  float x[8];
-  unpack8<BF16>(w, x);
-  atom += hh * p.head_bytes;
+  // (every exit above is the whole warp's)
   const int row = (int)(pos % kAtom);
-  uint8_t *codes = atom + (value ? kAtom * RB : 0) + row * RB;
-  __half *stats = reinterpret_cast<__half *>(atom + 2 * kAtom * RB + (value ? kAtom * SB : 0) +
-                                             row * SB);
-  quantize_row<D, BITS>(x, l, value, codes, stats);
+  const int code_at = (value ? kAtom * RB : 0) + row * RB;
+  const int stat_at = 2 * kAtom * RB + (value ? kAtom * SB : 0) + row * SB;
+#pragma unroll
+  for (int i = 0; i < kIoBatch; ++i) {
+    if (h0 + i * HW >= p.H) break;
+    uint8_t *at = atom + min(hl + i * HW, p.H - 1) * p.head_bytes;
+    quantize_row<D, BITS, BF16>(w[i], l, value, at + code_at,
+                                reinterpret_cast<__half *>(at + stat_at));
+  }
 }
 
-// Codes of 8 (keys: channels 32G + 8j ..; values: 4 channels of a pair of
-// groups) at pair offset p0 of a segment, as bytes of `BITS`-bit values.
-template <int BITS, int W>
-__device__ __forceinline__ uint32_t code_at(const uint32_t *words, int pair, int e) {
-  // W: bits of a half; units of 2W bits
-  const int bit = pair * BITS;
-  const int unit = bit / W, off = bit % W + W * e;
-  if (W == 8) return (words[0] >> (16 * unit + off)) & ((1u << BITS) - 1);
-  return (words[unit] >> off) & ((1u << BITS) - 1);
-}
-
-// Eight threads per token and head: four for the quarters of the key row, four
-// for pairs of eighths of the value row, 32 or 16 channels each.
+// One warp per row and group of heads: eight lanes to a head, four for the
+// quarters of the key row, four for pairs of eighths of the value row, 32 or 16
+// channels each; four heads per warp instruction, kReadBatch of those in
+// flight.
+constexpr int kReadBatch = 2;
 template <int D, int BITS, int BF16>
 __global__ void __launch_bounds__(kIoThreads)
-paged_read_kernel(Paged p, uint16_t *k, uint16_t *v) {
+paged_read_kernel(const __grid_constant__ Paged p, uint16_t *k, uint16_t *v, int groups) {
   constexpr int RB = D * BITS / 8, SB = 4 * D / kPagedGroup, NG = D / kPagedGroup;
-  constexpr int QB = RB / 4;  // bytes of a quarter
-  const int64_t i = (int64_t)blockIdx.x * kIoThreads + threadIdx.x;
-  const int64_t th = i >> 3;
-  const int64_t t = th / p.H;
-  if (t >= p.T) return;
-  const int h = (int)(th % p.H), part = (int)(i & 7), j = part & 3;
+  constexpr int QB = RB / 4, QW = QB / 4;  // bytes, words of a quarter
+  const int lane = threadIdx.x & 31, part = lane & 7, j = part & 3;
   const bool value = part >= 4;
-  const int b = seq_of_row(p, t);
+  const int64_t item = (int64_t)blockIdx.x * (kIoThreads / 32) + (threadIdx.x >> 5);
+  int64_t t = item;
+  int h0 = 0;
+  if (groups > 1) t = item / groups, h0 = (int)(item % groups) * kReadBatch * 4;
+  if (t >= p.T) return;
+  const int b = warp_seq_of_row(p, t);
   if (b < 0) return;
   const int64_t pos = row_position(p, b, t);
   const uint8_t *atom = pos >= 0 ? atom_of(p, b, pos) : nullptr;
-  uint16_t *dst = (value ? v : k) + (t * p.H + h) * D;
-  if (!atom) {
-    for (int g = 0; g < NG; ++g)
-      *reinterpret_cast<uint4 *>(dst + g * 32 + j * 8) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  atom += h * p.head_bytes;
-  const int row = (int)(pos % kAtom);
-  uint32_t w[QB / 4];
-  const uint8_t *src = atom + (value ? kAtom * RB : 0) + row * RB + j * QB;
+  const int row = (int)(pos & (kAtom - 1));
+  const int code_at = (value ? kAtom * RB : 0) + row * RB + j * QB;
+  const int stat_at = 2 * kAtom * RB + (value ? kAtom * SB : 0) + row * SB;
+  uint16_t *out = (value ? v : k) + t * p.H * D + 8 * j;
+  uint32_t w[kReadBatch][QW], st[kReadBatch][NG];
 #pragma unroll
-  for (int n = 0; n < QB / 4; ++n) w[n] = __ldg(reinterpret_cast<const uint32_t *>(src) + n);
-  const __half *st = reinterpret_cast<const __half *>(atom + 2 * kAtom * RB +
-                                                      (value ? kAtom * SB : 0) + row * SB);
+  for (int i = 0; i < kReadBatch; ++i) {
+    const int h = h0 + 4 * i + (lane >> 3);
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const float s = __half2float(st[g]), z = __half2float(st[NG + g]);
-    uint32_t o[4];
+    for (int n = 0; n < NG; ++n) st[i][n] = 0;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      float x[2];
+    for (int n = 0; n < QW; ++n) w[i][n] = 0;
+    if (h < p.H && atom) {
+      const uint8_t *at = atom + h * p.head_bytes;
+      if constexpr (QW % 4 == 0) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t c;
-        if (value) {
-          // channels 8j + 2m + u of group g: eighth 2j + m / 2
-          constexpr int W = (D == 64 && BITS == 2) ? 8 : 16;
-          const int c8 = 2 * m + u;
-          if (W == 8) {
-            const uint32_t half = (w[0] >> (16 * (c8 >> 2))) & 0xffffu;
-            c = (half >> ((c8 & 3) * BITS + 8 * (g & 1))) & ((1u << BITS) - 1);
-          } else {
-            c = code_at<BITS, 16>(w + (c8 >> 2) * (QB / 8), (g >> 1) * 4 + (c8 & 3), g & 1);
-          }
-        } else {
-          c = code_at<BITS, 16>(w, g * 4 + m, u);
+        for (int n = 0; n < QW; n += 4) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at + code_at + 4 * n));
+          w[i][n] = x.x, w[i][n + 1] = x.y, w[i][n + 2] = x.z, w[i][n + 3] = x.w;
         }
-        x[u] = __fadd_rn(__fmul_rn((float)c, s), z);
+      } else if constexpr (QW == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at + code_at));
+        w[i][0] = x.x, w[i][1] = x.y;
+      } else {
+        w[i][0] = __ldg(reinterpret_cast<const uint32_t *>(at + code_at));
       }
-      o[m] = pack2<BF16>(x[0], x[1]);
+      if constexpr (NG == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at + stat_at));
+        st[i][0] = x.x, st[i][1] = x.y, st[i][2 % NG] = x.z, st[i][3 % NG] = x.w;
+      } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at + stat_at));
+        st[i][0] = x.x, st[i][1] = x.y;
+      }
     }
-    *reinterpret_cast<uint4 *>(dst + g * 32 + j * 8) = make_uint4(o[0], o[1], o[2], o[3]);
   }
+  // Codes of channels 8j + m, m = 0 .. 7, of group G: a key's are pairs (2k,
+  // 2k + 1) at bit k*BITS of the two halves, a value's are bits i*BITS of half
+  // G & 1 of its eighth.
+  constexpr uint32_t kOne = (1u << BITS) - 1;
+  constexpr float kBase = 8388608.0f;  // 2^23: a code in the low bits of this is itself
+#pragma unroll
+  for (int i = 0; i < kReadBatch; ++i) {
+    const int h = h0 + 4 * i + (lane >> 3);
+    if (h >= p.H) break;
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      const float2 s2 = __half22float2(*reinterpret_cast<const __half2 *>(&st[i][G / 2]));
+      const float2 z2 = __half22float2(*reinterpret_cast<const __half2 *>(&st[i][NG / 2 + G / 2]));
+      const float s = G & 1 ? s2.y : s2.x, z = G & 1 ? z2.y : z2.x;
+      uint32_t o[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        float x[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c8 = 2 * m + u;
+          const int kbit = (G * 4 + m) * BITS;
+          uint32_t kw = w[i][kbit / 16] >> (kbit % 16 + 16 * u), vw;
+          if (RB / 8 == 2) {
+            vw = w[i][0] >> (16 * (c8 >> 2) + 8 * (G & 1) + (c8 & 3) * BITS);
+          } else {
+            const int vbit = ((G >> 1) * 4 + (c8 & 3)) * BITS;
+            vw = w[i][((c8 >> 2) * (QW / 2) + vbit / 16) % QW] >> (vbit % 16 + 16 * (G & 1));
+          }
+          const uint32_t code = (value ? vw : kw) & kOne;
+          x[u] = fmaf(__uint_as_float(code | 0x4b000000u) - kBase, s, z);
+        }
+        o[m] = pack2<BF16>(x[0], x[1]);
+      }
+      *reinterpret_cast<uint4 *>(out + (int64_t)h * D + G * 32) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// Warps of a call: rows x groups of `per` heads.
+unsigned io_grid(const Paged &p, int per, int *groups) {
+  *groups = (p.H + per - 1) / per;
+  return (unsigned)((p.T * *groups + kIoThreads / 32 - 1) / (kIoThreads / 32));
 }
 
 template <int D, int BITS>
 cudaError_t write_as(const Paged &p, const void *k, int64_t ks, const void *v, int64_t vs,
                      cudaStream_t st) {
-  const int hw = 32 / (2 * D / 8), groups = (p.H + hw - 1) / hw;
-  const int64_t warps = p.T * groups;
-  const unsigned grid = (unsigned)((warps + kIoThreads / 32 - 1) / (kIoThreads / 32));
+  int groups;
+  const unsigned grid = io_grid(p, kIoBatch * (32 / (2 * D / 8)), &groups);
   auto kern = p.bf16 ? paged_write_kernel<D, BITS, 1> : paged_write_kernel<D, BITS, 0>;
   kern<<<grid, kIoThreads, 0, st>>>(p, static_cast<const uint16_t *>(k), ks,
                                     static_cast<const uint16_t *>(v), vs, groups);
@@ -251,10 +344,11 @@ cudaError_t write_as(const Paged &p, const void *k, int64_t ks, const void *v, i
 
 template <int D, int BITS>
 cudaError_t read_as(const Paged &p, void *k, void *v, cudaStream_t st) {
-  const int64_t threads = p.T * p.H * 8;
-  const unsigned grid = (unsigned)((threads + kIoThreads - 1) / kIoThreads);
+  int groups;
+  const unsigned grid = io_grid(p, kReadBatch * 4, &groups);
   auto kern = p.bf16 ? paged_read_kernel<D, BITS, 1> : paged_read_kernel<D, BITS, 0>;
-  kern<<<grid, kIoThreads, 0, st>>>(p, static_cast<uint16_t *>(k), static_cast<uint16_t *>(v));
+  kern<<<grid, kIoThreads, 0, st>>>(p, static_cast<uint16_t *>(k), static_cast<uint16_t *>(v),
+                                    groups);
   return cudaGetLastError();
 }
 
