@@ -488,6 +488,13 @@ def paged_cache_bytes(cfg: PagedConfig):
     return pool.value, page.value
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream's handle (torch.cuda.current_stream builds an object,
+    2 us of a 10 us call)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get else torch.cuda.current_stream(index).cuda_stream
+
+
 class PagedBatch:
     """The sequences of one call (kvq_paged_batch): int32 device tensors
     block_table [n_seqs][width], seq_lens [n_seqs] and cu_tokens [n_seqs + 1].
@@ -513,6 +520,7 @@ class PagedBatch:
         self.n_tokens = int(n_tokens)
         self.max_tokens = int(n_tokens if max_tokens is None else max_tokens)
         self.device = block_table.device
+        self.index = block_table.get_device()
         self.view = _PagedBatch(block_table.data_ptr(), seq_lens.data_ptr(),
                                 cu_tokens.data_ptr(), block_table.shape[1], self.n_tokens, n,
                                 self.max_tokens)
@@ -546,6 +554,13 @@ class PagedKVCache:
         self.ws_bytes = n.value
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self._refs = ctypes.byref(cfg), ctypes.byref(self.view)
+        L = lib()
+        self._write, self._read, self._attend = (L.kvq_paged_write, L.kvq_paged_read,
+                                                 L.kvq_paged_attention)
+        self._ws_ptr = self.ws.data_ptr()
+        self._index = self.device.index if self.device.type == "cuda" else -1
+        self._kv_row = (cfg.n_kv_heads, cfg.head_dim)
+        self._q_row = (cfg.n_q_heads, cfg.head_dim)
         self._scale = 1.0 / math.sqrt(cfg.head_dim)
 
     def _on_device(self, t) -> None:
@@ -555,29 +570,28 @@ class PagedKVCache:
     def _rows(self, t: torch.Tensor, batch: PagedBatch, heads: int) -> int:
         """Checks a packed tensor [n_tokens][heads][head_dim] (rows of any
         stride, each contiguous); returns the stride between rows."""
+        d = self.cfg.head_dim
         if t.dtype != self.dtype:
             raise TypeError("expected a %s tensor, got %s" % (self.dtype, t.dtype))
-        if t.shape != (batch.n_tokens, heads, self.cfg.head_dim):
+        if t.shape != (batch.n_tokens, heads, d):
             raise ValueError("expected shape %s, got %s"
-                             % ((batch.n_tokens, heads, self.cfg.head_dim), tuple(t.shape)))
-        self._on_device(t)
+                             % ((batch.n_tokens, heads, d), tuple(t.shape)))
+        if t.get_device() != self._index:
+            self._on_device(t)
         s0, s1, s2 = t.stride()
-        if t.shape[0] <= 1:
-            s0 = max(s0, heads * self.cfg.head_dim)
-        if s2 != 1 or (heads > 1 and s1 != self.cfg.head_dim):
+        if s2 != 1 or (heads > 1 and s1 != d):
             raise ValueError("each row must be contiguous (got strides %s)" % (t.stride(),))
-        return s0
+        return s0 if batch.n_tokens > 1 else max(s0, heads * d)
 
     def _call(self, fn, batch: PagedBatch, stream, *args) -> None:
-        if batch.device != self.device:
+        if batch.index != self._index:
             raise ValueError("the batch is on %s, the cache on %s" % (batch.device, self.device))
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        if torch.cuda.current_device() == self.device.index:
-            code = fn(*self._refs, batch._ref, *args, stream.cuda_stream)
+        st = _raw_stream(self._index) if stream is None else stream.cuda_stream
+        if torch.cuda.current_device() == self._index:
+            code = fn(*self._refs, batch._ref, *args, st)
         else:
             with torch.cuda.device(self.device):
-                code = fn(*self._refs, batch._ref, *args, stream.cuda_stream)
+                code = fn(*self._refs, batch._ref, *args, st)
         if code != KVQ_OK:
             raise KVQError(code, fn.__name__)
 
@@ -586,21 +600,21 @@ class PagedKVCache:
         tokens) into their pages."""
         H = self.cfg.n_kv_heads
         ks, vs = self._rows(k, batch, H), self._rows(v, batch, H)
-        self._call(lib().kvq_paged_write, batch, stream, k.data_ptr(), ks, v.data_ptr(), vs)
+        self._call(self._write, batch, stream, k.data_ptr(), ks, v.data_ptr(), vs)
 
     def read(self, batch: PagedBatch, out=None, stream=None):
         """Reads the batch's tokens back: (k, v), each contiguous
         [n_tokens][n_kv_heads][head_dim] (``out``: the two tensors to fill)."""
-        H, d = self.cfg.n_kv_heads, self.cfg.head_dim
         if out is None:
-            k, v = (torch.empty((batch.n_tokens, H, d), dtype=self.dtype, device=self.device)
-                    for _ in range(2))
+            k = torch.empty((batch.n_tokens,) + self._kv_row, dtype=self.dtype,
+                            device=self.device)
+            v = torch.empty_like(k)
         else:
             k, v = out
             for t in out:
-                self._rows(t, batch, H)
+                self._rows(t, batch, self.cfg.n_kv_heads)
                 _ptr(t)
-        self._call(lib().kvq_paged_read, batch, stream, k.data_ptr(), v.data_ptr())
+        self._call(self._read, batch, stream, k.data_ptr(), v.data_ptr())
         return k, v
 
     def attend(self, q: torch.Tensor, batch: PagedBatch, out: torch.Tensor | None = None,
@@ -610,13 +624,13 @@ class PagedKVCache:
         those tokens first).  Returns [n_tokens][n_q_heads][head_dim]."""
         qs = self._rows(q, batch, self.cfg.n_q_heads)
         if out is None:
-            out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
+            out = torch.empty((batch.n_tokens,) + self._q_row, dtype=self.dtype,
+                              device=self.device)
         else:
             self._rows(out, batch, self.cfg.n_q_heads)
             _ptr(out)
-        self._call(lib().kvq_paged_attention, batch, stream, q.data_ptr(), qs, out.data_ptr(),
-                   self._scale if scale is None else float(scale), self.ws.data_ptr(),
-                   self.ws_bytes)
+        self._call(self._attend, batch, stream, q.data_ptr(), qs, out.data_ptr(),
+                   self._scale if scale is None else scale, self._ws_ptr, self.ws_bytes)
         return out
 
     def device_status(self, stream=None) -> int:

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from bit_kv_cache_14_gb300 import build_lib, kvq
-from paged_util import Case, pack_row, quantize, random_case
+from paged_util import Case, pack_row, quantize, random_case, values
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
@@ -273,6 +273,143 @@ def test_captured_graph_follows_lengths(most):
         g.replay()
         torch.cuda.synchronize()
         d.check_attention(out)
+    assert cache.device_status() == 0
+
+
+def test_captured_step_writes_attends_and_reads():
+    """A whole serving step in one graph: the new rows of each replay enter the
+    pages, are attended to and read back."""
+    c = Case([100, 37], [1, 1], 8, 2, 64, 2, 16, BF16)
+    cache = c.filled()
+    batch = c.batch()
+    k, v = c.packed("k"), c.packed("v")
+    q = c.queries()
+    cache.write(k, v, batch)
+    cache.attend(q, batch)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        cache.write(k, v, batch)
+        out = cache.attend(q, batch)
+        back = cache.read(batch)
+    for seed in (1, 2):
+        d = Case([100, 37], [1, 1], 8, 2, 64, 2, 16, BF16, seed=seed)
+        d.table = c.table
+        for b in range(2):  # the tokens before stay
+            d.K[b][:-1], d.V[b][:-1] = c.K[b][:-1], c.V[b][:-1]
+        k.copy_(d.packed("k")), v.copy_(d.packed("v")), q.copy_(d.queries())
+        g.replay()
+        torch.cuda.synchronize()
+        d.check_attention(out)
+        assert torch.equal(back[0].cpu(), d.expected_rows("k", d.rows))
+        assert torch.equal(back[1].cpu(), d.expected_rows("v", d.rows))
+
+
+def test_two_graphs_share_a_cache_and_its_scratch():
+    """Replayed one after the other, a decode graph and a chunk graph that both
+    split pairs over blocks use the same scratch."""
+    kv = [3000, 2500]
+    a = Case(kv, [1, 1], 8, 2, 128, 4, 64, F16, seed=3)
+    b = Case(kv, [40, 70], 8, 2, 128, 4, 64, F16, seed=3)
+    cache = a.filled()
+    runs = []
+    for c in (a, b):
+        q, batch = c.queries(), c.batch()
+        cache.attend(q, batch)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = cache.attend(q, batch)
+        runs.append((g, c, out, q, batch))
+    for g, _, _, _, _ in runs * 3:
+        g.replay()
+    torch.cuda.synchronize()
+    for _, c, out, _, _ in runs:
+        c.check_attention(out)
+    assert cache.device_status() == 0
+
+
+@pytest.mark.parametrize("new", (1, 60))
+def test_a_wait_that_runs_out_is_reported(new):
+    """The debug switch makes a wait run out: KVQ_ETIMEOUT in the status word,
+    and the next call, with the scratch cleared, is right again."""
+    c = Case([700, 300], [new, new], 8, 2, 128, 4, 32, F16)
+    cache, batch, q = c.filled(), c.batch(), c.queries()
+    try:
+        kvq.debug_stall_waits(1000)
+        cache.attend(q, batch)
+        torch.cuda.synchronize()
+    finally:
+        kvq.debug_stall_waits(0)
+    assert cache.device_status() == kvq.KVQ_ETIMEOUT
+    c.check_attention(cache.attend(q, batch))
+    assert cache.device_status() == 0
+
+
+@pytest.mark.parametrize("new,launches", [(1, 1), (2, 1), (3, 2), (200, 2)])
+def test_launch_counts(new, launches):
+    """Up to 16 query rows a KV head are the split kernel's alone; a call that may
+    hold more launches both kernels."""
+    c = Case([300], [new], 8, 1, 128, 4, 32, F16)
+    cache = c.filled()
+    out = cache.attend(c.queries(), c.batch())
+    assert kvq.lib().kvq_last_launch_count() == launches
+    c.check_attention(out)
+    cache.read(c.batch())
+    assert kvq.lib().kvq_last_launch_count() == 1
+
+
+@pytest.mark.parametrize("rg,heads", [(20, 1), (128, 1), (24, 2)])
+def test_many_query_heads_per_kv_head(rg, heads):
+    """More query heads per KV head than the split kernel's 16 rows: every
+    sequence goes to the chunk kernel, single tokens too."""
+    c = Case([200, 1, 33], [1, 1, 3], rg * heads, heads, 64, 4, 32, BF16)
+    c.check_attention(c.filled().attend(c.queries(), c.batch()))
+    assert kvq.lib().kvq_last_launch_count() == 1
+
+
+@pytest.mark.parametrize("new", (1, 300))
+def test_many_sequences(new):
+    """More sequences than a warp, and than a block, has lanes."""
+    B = 333
+    c = Case([1 + b % 40 for b in range(B)], [1] * B, 2, 1, 64, 8, 16, F16)
+    if new > 1:  # one long chunk among them
+        c = Case([400] + [1 + b % 40 for b in range(B)], [new] + [1] * B, 2, 1, 64, 8, 16, F16)
+    cache = c.filled()
+    c.check_attention(cache.attend(c.queries(), c.batch()))
+    k, v = cache.read(c.batch())
+    assert torch.equal(k.cpu(), c.expected_rows("k", c.rows))
+
+
+@pytest.mark.parametrize("kv,new,hkv", [(40000, 1, 1), (20000, 40, 1), (9000, 700, 2)])
+def test_long_sequences_are_split_and_joined(kv, new, hkv):
+    """Pairs that many blocks share.  The reference is torch in 64 bits on the
+    GPU, the bound that of the short cases at this length."""
+    c = Case([kv], [0], 4 * hkv, hkv, 128, 4, 64, F16)
+    cache = c.filled()
+    c.new = [new]
+    c.cu = np.array([0, new], np.int32)
+    c.n_tokens = new
+    c.q = c._round(1.2 * c.rng.standard_normal((new, 4 * hkv, 128)).astype(np.float32))
+    out = cache.attend(c.queries(), c.batch()).double()
+    K, V = (torch.from_numpy(values(*quantize(x, 4))).cuda().double() for x in (c.K[0], c.V[0]))
+    q = c.queries().double()
+    u = 2.0 ** -11
+    hidden = (torch.arange(kv, device="cuda")[None]
+              > (kv - new + torch.arange(new, device="cuda"))[:, None])
+    for h in range(4 * hkv):
+        s = (q[:, h] @ K[:, h // 4].T) / 128 ** 0.5
+        A = (q[:, h].abs() @ K[:, h // 4].abs().T) / 128 ** 0.5
+        w = torch.softmax(s.masked_fill(hidden, -float("inf")), -1)
+        m = V[:, h // 4].abs().amax(0) * 3
+        ds = 2 * 2 * u * 3 * A.masked_fill(w < 1e-12, 0).amax(-1, keepdim=True)
+        bound = (w @ (3 * V[:, h // 4].abs())) * (2 * u + torch.expm1(ds) + kv * 2.0 ** -24) \
+            + kv * 2.0 ** -24 * m
+        exp = w @ V[:, h // 4]
+        err = (out[:, h] - exp).abs()
+        assert (err <= bound + u * (exp.abs() + bound) + 1e-7).all()
+        # and on the whole far closer than the worst case
+        assert float(err.norm() / exp.norm()) < 2.0 ** -8
     assert cache.device_status() == 0
 
 

@@ -143,6 +143,7 @@ def test_batch_checks():
 def test_binding_checks_rows():
     cache = kvq.PagedKVCache.__new__(kvq.PagedKVCache)
     cache.cfg, cache.device, cache.dtype = _cfg(), torch.device("cpu"), torch.float16
+    cache._index = -1
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     batch = kvq.PagedBatch(i32(1, 4), i32(1), i32(2), 5)
     row = torch.zeros(5, 2, 128, dtype=torch.float16)
