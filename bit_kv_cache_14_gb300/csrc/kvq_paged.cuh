@@ -9,7 +9,7 @@ namespace kvq {
 
 constexpr int kAtom = 16;         // tokens stored together inside a page
 constexpr int kPagedGroup = 32;   // channels that share a scale and a zero point
-constexpr int kMaxSeqs = 4096;
+constexpr int kMaxSeqs = 2048;  // (running sums over the sequences fit shared memory)
 constexpr float kPagedLimit = 32768.0f;  // stored magnitudes saturate here
 
 // One paged call, resolved on the host and copied by value into every kernel.

@@ -26,9 +26,11 @@
 //   (warps 18, 19 only give up registers)
 //
 // Split: every (sequence, head, 256-row tile) is a list of its visible 128-token
-// steps plus kOver for its start and end; the concatenated list is cut into
-// equal ranges, one per block.  A tile cut by a border leaves partials, joined
-// in block order by the block that finishes last.
+// steps.  Where all tiles in pieces of about kPiece steps give no more pieces
+// than there are blocks, each block takes a piece; a longer list, kOver units
+// added to each tile for its start and end, is cut into equal ranges, one per
+// block.  A tile that several blocks share leaves partials, joined in block
+// order by the block that finishes last.
 #include "kvq_paged.cuh"
 #include "kvq_tc_common.cuh"
 
@@ -50,8 +52,9 @@ constexpr int kAhead = 8;   // steps the list runs ahead of the producers' loads
 constexpr int kPWarps = kMmaWarp - kProducerWarp;
 constexpr int kStep = 128;       // cached tokens per step
 constexpr int kTileRows = 256;   // query rows per block
-constexpr int kOver = 2;         // units of a tile's start and end
-constexpr int kMinUnits = 8;
+constexpr int kOver = 6;         // units of a tile's start and end, which take about as long
+constexpr int kMinUnits = 16;
+constexpr int kPiece = 6;        // steps worth a block of their own
 constexpr int kMaxChunkBlocks = 160;
 constexpr int kChunkWait = 1 << 25;
 constexpr float kChunkSlack = 8.0f;  // log2 units a score may pass the reference by
@@ -85,8 +88,9 @@ struct ChunkCfg {
   static constexpr int kBars = 19 + 2 * kItems + 2 * kAhead;
   static constexpr int off_item = (off_bar + kBars * 8 + 15) / 16 * 16;
   static constexpr int off_misc = off_item + kItems * 64;  // tensor memory base, dead flag, flags
-  static constexpr int off_prefix = off_misc + 64;
-  static constexpr int smem(int seqs) { return off_prefix + (seqs + 1) * 8 + 1024; }
+  static constexpr int smem = off_misc + 64 + 1024;
+  // the running sums of the plan lie where the operands come later
+  static_assert(2 * (kMaxSeqs + 1) * 8 <= 2 * kTile + 4 * kTile, "room for the plan");
 };
 
 // ---- PTX ------------------------------------------------------------------
@@ -265,6 +269,8 @@ __device__ __forceinline__ int steps_of(const ChunkArgs &a, const Seq &s, int t)
   return see < 1 ? 1 : (int)((see + kStep - 1) / kStep);
 }
 
+__device__ __forceinline__ int pieces_of(int steps) { return max(1, (steps + kPiece / 2) / kPiece); }
+
 // One block's share of one tile, as the roles read it from shared memory.
 struct __align__(16) Item {
   int b, h;             // sequence (-1: no more items), KV head
@@ -316,7 +322,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   auto bar_g = [&](int i) { return bars + 8u * (17 + i); };      // the 128 threads of tile i
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::off_misc);
   volatile uint32_t *dead = misc + 1;
-  int64_t *prefix = reinterpret_cast<int64_t *>(smem + C::off_prefix);
+  int64_t *units = reinterpret_cast<int64_t *>(smem);  // running sums over the sequences
+  int64_t *pieces = units + kMaxSeqs + 1;
   int64_t *sh_x = reinterpret_cast<int64_t *>(misc + 4);  // borders of the block's range
   int *sh_at = reinterpret_cast<int *>(misc + 8);         // b, h, t, off of its first unit
 
@@ -344,10 +351,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 16, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     misc[1] = 0;
-    prefix[0] = 0;
+    units[0] = pieces[0] = 0;
   }
 
-  // ---- prefix[b + 1]: units of one head of sequences 0 .. b
+  // ---- units[b + 1], pieces[b + 1]: of one head of sequences 0 .. b
   for (int b = warp; b < p.B; b += kChunkThreads / 32) {
     const Seq s = seq_of(a, b);
     if (lane == 0 && blockIdx.x == 0) {
@@ -355,30 +362,44 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       if (s.rows > 0 && p.lens[b] > p.width * p.page) paged_error(p, KVQ_EPAGE);
     }
     const int tiles = (s.rows + kTileRows - 1) / kTileRows;
-    int64_t sum = 0;
-    for (int t = lane; t < tiles; t += 32) sum += steps_of(a, s, t) + kOver;
+    int64_t sum = 0, psum = 0;
+    for (int t = lane; t < tiles; t += 32) {
+      const int steps = steps_of(a, s, t);
+      sum += steps + kOver;
+      psum += pieces_of(steps);
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) prefix[b + 1] = sum;
+    for (int o = 16; o; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      psum += __shfl_xor_sync(0xffffffffu, psum, o);
+    }
+    if (lane == 0) units[b + 1] = sum, pieces[b + 1] = psum;
   }
   __syncthreads();
-  if (warp == 0) {  // running sums, 32 sequences at a time
-    int64_t before = 0;
+  if (warp < 2) {  // running sums, 32 sequences at a time
+    int64_t *sums = warp ? pieces : units, before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      int64_t v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
+      int64_t v = b0 + lane < p.B ? sums[b0 + lane + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += up;
       }
       v += before;
-      if (b0 + lane < p.B) prefix[b0 + lane + 1] = v;
+      if (b0 + lane < p.B) sums[b0 + lane + 1] = v;
       before = __shfl_sync(0xffffffffu, v, 31);
     }
   }
   __syncthreads();
+  const bool by_piece = p.H * pieces[p.B] <= gridDim.x;
+  const int64_t *prefix = by_piece ? pieces : units;
   const int64_t total = p.H * prefix[p.B];
-  const int64_t U = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kMinUnits);
+  const int64_t U =
+      by_piece ? 1 : max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kMinUnits);
+  auto cost_of = [&](const Seq &s, int t) {
+    const int steps = steps_of(a, s, t);
+    return by_piece ? pieces_of(steps) : steps + kOver;
+  };
   // ---- the block's borders: warp 0 its first unit, warp 1 the next block's.
   // A border inside a tile's first units moves to its start, one at its last
   // step to its end, so every item has steps of its own.
@@ -400,7 +421,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       int64_t y = r - h * per;  // unit inside the head
       const int tiles = (s.rows + kTileRows - 1) / kTileRows;
       for (int t0 = 0;; t0 += 32) {
-        int64_t cost = t0 + lane < tiles ? steps_of(a, s, t0 + lane) + kOver : 0, run = cost;
+        int64_t cost = t0 + lane < tiles ? cost_of(s, t0 + lane) : 0, run = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
@@ -413,7 +434,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           const int64_t end = __shfl_sync(0xffffffffu, run, w);
           cost = __shfl_sync(0xffffffffu, cost, w);
           off = (int)(y - (end - cost));
-          if (off <= kOver + 1) {
+          if (by_piece) {
+          } else if (off <= kOver + 1) {
             x -= off;
             off = 0;
           } else if (cost - off <= 1) {
@@ -608,11 +630,22 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
             } while (s.rows == 0);
             tiles = (s.rows + kTileRows - 1) / kTileRows;
           }
-          const int nsteps = steps_of(a, s, t), cost = nsteps + kOver;
+          const int nsteps = steps_of(a, s, t), cost = cost_of(s, t);
           const int n = (int)min((int64_t)(cost - off), x1 - x);
           const int64_t first = x - off, last = first + cost;
-          j0 = off > kOver ? off - kOver : 0;
-          j1 = off + n - kOver;
+          int c0, c1;  // the blocks that share the tile
+          if (by_piece) {
+            j0 = (int)((int64_t)nsteps * off / cost);
+            j1 = (int)((int64_t)nsteps * (off + 1) / cost);
+            c0 = (int)first, c1 = (int)last - 1;
+          } else {
+            j0 = off > kOver ? off - kOver : 0;
+            j1 = off + n - kOver;
+            // (the borders as they were moved, above)
+            c0 = (int)(first / U), c1 = (int)((last - 1) / U);
+            if ((c0 + 1) * U - first <= kOver + 1) ++c0;
+            if (last - c1 * U <= 1) --c1;
+          }
           if (lane == 0) {
             it->b = b, it->h = h;
             it->j0 = j0, it->j1 = j1;
@@ -620,10 +653,6 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
             it->rows = s.rows, it->len = s.len;
             it->pos0 = s.pos0;
             it->steps = nsteps;
-            // (the borders as they were moved, above)
-            int c0 = (int)(first / U), c1 = (int)((last - 1) / U);
-            if ((c0 + 1) * U - first <= kOver + 1) ++c0;
-            if (last - c1 * U <= 1) --c1;
             it->c0 = c0, it->c1 = c1;
           }
           x += n;
@@ -1210,7 +1239,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
 template <int D, int BITS>
 cudaError_t chunk_as(const ChunkArgs &a, int num_sms, cudaStream_t st) {
   static KernelSetup setup;
-  const int smem = ChunkCfg<D>::smem(a.p.B);
+  constexpr int smem = ChunkCfg<D>::smem;
   auto kern = paged_chunk_kernel<D, BITS>;
   const cudaError_t e = kernel_setup(setup, kern, kChunkThreads, smem, nullptr);
   if (e != cudaSuccess) return e;

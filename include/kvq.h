@@ -456,7 +456,7 @@ typedef struct kvq_paged_cache {
  *   cu_tokens   int32 [n_seqs+1] the call's rows [cu[b], cu[b+1]) belong to
  *     sequence b and are its LAST n_b = cu[b+1] - cu[b] tokens: row cu[b] + i
  *     is position seq_lens[b] - n_b + i.  cu[0] = 0, not decreasing.
- * Host values: n_seqs (1..4096), table_width, n_tokens = rows of the packed
+ * Host values: n_seqs (1..2048), table_width, n_tokens = rows of the packed
  * arrays (rows from cu[n_seqs] on are padding: never read, never written),
  * max_tokens >= every n_b.
  * What the device arrays say is checked there: a row at a negative position

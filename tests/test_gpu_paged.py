@@ -371,7 +371,7 @@ def test_many_query_heads_per_kv_head(rg, heads):
 @pytest.mark.parametrize("new", (1, 300))
 def test_many_sequences(new):
     """More sequences than a warp, and than a block, has lanes."""
-    B = 333
+    B = 2047
     c = Case([1 + b % 40 for b in range(B)], [1] * B, 2, 1, 64, 8, 16, F16)
     if new > 1:  # one long chunk among them
         c = Case([400] + [1 + b % 40 for b in range(B)], [new] + [1] * B, 2, 1, 64, 8, 16, F16)

@@ -93,7 +93,7 @@ def test_calls_refuse_before_touching_the_device():
     for kw in (dict(block_table=None), dict(seq_lens=None), dict(cu_tokens=None), dict(n_seqs=0),
                dict(table_width=0), dict(n_tokens=-1), dict(max_tokens=-1)):
         assert set(_calls(cfg, cache, _batch(**kw))) == {kvq.KVQ_EINVAL}, kw
-    for kw in (dict(n_seqs=4097), dict(table_width=1 << 40), dict(n_tokens=1 << 31)):
+    for kw in (dict(n_seqs=2049), dict(table_width=1 << 40), dict(n_tokens=1 << 31)):
         assert set(_calls(cfg, cache, _batch(**kw))) == {kvq.KVQ_EUNSUPPORTED}, kw
     for kw in (dict(block_table=0x1002), dict(cu_tokens=0x1001)):
         assert set(_calls(cfg, cache, _batch(**kw))) == {kvq.KVQ_EALIGN}, kw
