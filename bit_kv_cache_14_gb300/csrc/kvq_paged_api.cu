@@ -45,6 +45,7 @@ static int resolve_call(const kvq_paged_config *cfg, const kvq_paged_cache *cach
   if (!batch->block_table || !batch->seq_lens || !batch->cu_tokens) return KVQ_EINVAL;
   if (batch->n_seqs < 1 || batch->table_width < 1 || batch->n_tokens < 0 || batch->max_tokens < 0)
     return KVQ_EINVAL;
+  if (batch->n_tokens > 0 && batch->max_tokens < 1) return KVQ_EINVAL;
   if (batch->n_seqs > kMaxSeqs) return KVQ_EUNSUPPORTED;
   // positions and row counts are int32 on the device
   if (batch->table_width > (1LL << 30) / p->page || batch->n_tokens > (1LL << 30) ||
@@ -72,6 +73,14 @@ static int check_rows(const Paged &p, const void *x, int64_t stride, int heads) 
   if (stride < (int64_t)heads * p.d || stride > (1LL << 31)) return KVQ_EINVAL;
   if (!aligned(x, 16) || stride % 8 != 0) return KVQ_EALIGN;
   return KVQ_OK;
+}
+
+// Whether two packed row arrays overlap (16-bit elements).
+static bool overlap(const Paged &p, const void *a, int64_t sa, const void *b, int64_t sb,
+                    int heads) {
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  const uintptr_t row = (uintptr_t)heads * p.d * 2;
+  return a0 < b0 + (uintptr_t)(p.T - 1) * sb * 2 + row && b0 < a0 + (uintptr_t)(p.T - 1) * sa * 2 + row;
 }
 
 static int done(cudaError_t e, int launches) {
@@ -126,6 +135,7 @@ int kvq_paged_read(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
   const int64_t stride = (int64_t)p.H * p.d;
   if ((r = check_rows(p, k_out, stride, p.H)) != KVQ_OK) return r;
   if ((r = check_rows(p, v_out, stride, p.H)) != KVQ_OK) return r;
+  if (overlap(p, k_out, stride, v_out, stride, p.H)) return KVQ_EINVAL;
   return done(launch_paged_read(p, k_out, v_out, static_cast<cudaStream_t>(stream)), 1);
 }
 
@@ -140,9 +150,11 @@ int kvq_paged_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cach
   if (!ws) return KVQ_EINVAL;
   if (!aligned(ws, 16)) return KVQ_EALIGN;
   if (ws_bytes < paged_workspace_bytes()) return KVQ_ECAPACITY;
-  if (p.T == 0 || p.max_tokens == 0) return done(cudaSuccess, 0);
+  if (p.T == 0) return done(cudaSuccess, 0);
   if ((r = check_rows(p, q, q_stride, p.Hq)) != KVQ_OK) return r;
-  if ((r = check_rows(p, out, (int64_t)p.Hq * p.d, p.Hq)) != KVQ_OK) return r;
+  const int64_t stride = (int64_t)p.Hq * p.d;
+  if ((r = check_rows(p, out, stride, p.Hq)) != KVQ_OK) return r;
+  if (overlap(p, q, q_stride, out, stride, p.Hq)) return KVQ_EINVAL;
   int n = 0;
   const cudaError_t e = launch_paged_attention(p, q, q_stride, out, softmax_scale, ws,
                                                static_cast<cudaStream_t>(stream), &n);

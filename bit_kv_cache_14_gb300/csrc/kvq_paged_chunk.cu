@@ -1240,6 +1240,18 @@ template <int D, int BITS>
 cudaError_t chunk_as(const ChunkArgs &a, int num_sms, cudaStream_t st) {
   static KernelSetup setup;
   constexpr int smem = ChunkCfg<D>::smem;
+  // the register split draws on what the block is launched with: a kernel built
+  // with fewer registers a thread would wait for the rest forever
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, paged_chunk_kernel<D, BITS>);
+    if (e != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) * kChunkThreads <
+      256 * kSoftRegs + 256 * kProducerRegs + 128 * kOtherRegs)
+    return cudaErrorInvalidConfiguration;
   auto kern = paged_chunk_kernel<D, BITS>;
   const cudaError_t e = kernel_setup(setup, kern, kChunkThreads, smem, nullptr);
   if (e != cudaSuccess) return e;

@@ -531,7 +531,9 @@ class PagedKVCache:
     """A page pool (torch-allocated unless ``pages`` is given) with the status
     word and the attention scratch, and the paged calls on it.  Calls run on
     ``stream`` (default: the current stream of the cache's device); calls that
-    can run at the same time need caches (or scratch) of their own."""
+    can run at the same time need caches (or scratch) of their own.  As anywhere
+    in torch, tensors handed to a call on another stream than theirs have to
+    stay alive until it is done."""
 
     def __init__(self, cfg: PagedConfig, device="cuda", pages: torch.Tensor | None = None):
         self.cfg = cfg
@@ -615,6 +617,8 @@ class PagedKVCache:
                 self._rows(t, batch, self.cfg.n_kv_heads)
                 _ptr(t)
         self._call(self._read, batch, stream, k.data_ptr(), v.data_ptr())
+        if stream is not None and out is None:
+            k.record_stream(stream), v.record_stream(stream)
         return k, v
 
     def attend(self, q: torch.Tensor, batch: PagedBatch, out: torch.Tensor | None = None,
@@ -623,14 +627,17 @@ class PagedKVCache:
         the batch's newest tokens, over everything their sequences hold (write
         those tokens first).  Returns [n_tokens][n_q_heads][head_dim]."""
         qs = self._rows(q, batch, self.cfg.n_q_heads)
-        if out is None:
-            out = torch.empty((batch.n_tokens,) + self._q_row, dtype=self.dtype,
-                              device=self.device)
-        else:
+        given = out is not None
+        if given:
             self._rows(out, batch, self.cfg.n_q_heads)
             _ptr(out)
+        else:
+            out = torch.empty((batch.n_tokens,) + self._q_row, dtype=self.dtype,
+                              device=self.device)
         self._call(self._attend, batch, stream, q.data_ptr(), qs, out.data_ptr(),
                    self._scale if scale is None else scale, self._ws_ptr, self.ws_bytes)
+        if stream is not None and not given:
+            out.record_stream(stream)
         return out
 
     def device_status(self, stream=None) -> int:

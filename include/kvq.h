@@ -458,13 +458,13 @@ typedef struct kvq_paged_cache {
  *     is position seq_lens[b] - n_b + i.  cu[0] = 0, not decreasing.
  * Host values: n_seqs (1..2048), table_width, n_tokens = rows of the packed
  * arrays (rows from cu[n_seqs] on are padding: never read, never written),
- * max_tokens >= every n_b.
+ * max_tokens >= every n_b (at least 1 where n_tokens > 0).
  * What the device arrays say is checked there: a row at a negative position
  * is skipped (write), reads as zeros (read), attends to nothing (attention);
  * a token whose page entry lies outside [0, n_pages) or behind table_width is
  * skipped, reads as zeros or is not attended to, and KVQ_EPAGE goes to the
- * status word; a sequence with more than max_tokens rows is not attended for
- * and gives KVQ_EINVAL there.
+ * status word; a sequence with more than max_tokens rows, or with rows behind
+ * n_tokens, is not attended for and gives KVQ_EINVAL there.
  */
 typedef struct kvq_paged_batch {
   const int32_t *block_table, *seq_lens, *cu_tokens;
@@ -477,7 +477,8 @@ typedef struct kvq_paged_batch {
 int kvq_paged_cache_bytes(const kvq_paged_config *cfg, size_t *pool, size_t *page);
 
 /* Bytes of scratch kvq_paged_attention needs (any batch).  Zero-fill it once;
- * every call leaves what must be zero at zero again.  Calls that can run at
+ * every call leaves what must be zero at zero again, unless a wait ran out
+ * (KVQ_ETIMEOUT in the status word): zero-fill it then.  Calls that can run at
  * the same time need scratch of their own. */
 int kvq_paged_workspace_bytes(const kvq_paged_config *cfg, size_t *bytes);
 
@@ -496,8 +497,9 @@ int kvq_paged_write(const kvq_paged_config *cfg, kvq_paged_cache *cache,
 
 /*
  * Read the call's tokens back: x_hat rounded once to dtype, k_out and v_out
- * [n_tokens][n_kv_heads][head_dim] contiguous.  cu_tokens = running sums of
- * seq_lens reads whole sequences.  Errors as kvq_paged_write.
+ * [n_tokens][n_kv_heads][head_dim] contiguous, apart from each other.
+ * cu_tokens = running sums of seq_lens reads whole sequences.  Errors as
+ * kvq_paged_write.
  */
 int kvq_paged_read(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
                    const kvq_paged_batch *batch, void *k_out, void *v_out, void *stream);
@@ -508,10 +510,17 @@ int kvq_paged_read(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
  * included: write first).  One row per sequence is a decode step; chunks of
  * any length, and batches that mix both, are one call.
  *   q: device, row t of query head h at q + t*q_stride + h*head_dim
- *   out [n_tokens][n_q_heads][head_dim], contiguous, dtype:
+ *   out [n_tokens][n_q_heads][head_dim], contiguous, dtype, apart from q:
  *     softmax(softmax_scale * q.K^T) V; zeros for a row that sees nothing.
+ *   softmax_scale: any finite number.
  *   ws: device scratch, ws_bytes >= kvq_paged_workspace_bytes.
- * Errors: as kvq_paged_write; KVQ_ECAPACITY (ws too small).
+ * Arithmetic: scores, weights' sums and outputs are held in fp32; the operands
+ * of the two products are rounded to fp16 (the query relative to the largest
+ * of its row, the weights, and for sequences of more than 16 query rows per KV
+ * head, a row being one token and query head, the values x_hat), which costs
+ * about what one fp16 rounding of the output does.
+ * Errors: as kvq_paged_write; KVQ_EINVAL also where q and out overlap;
+ *   KVQ_ECAPACITY (ws too small).
  */
 int kvq_paged_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
                         const kvq_paged_batch *batch, const void *q, int64_t q_stride, void *out,

@@ -91,7 +91,7 @@ def _calls(cfg, cache, batch, rows=0x2000, stride=1024, out=0x3000, scale=0.1, w
 def test_calls_refuse_before_touching_the_device():
     cfg, cache = _cfg(), kvq._PagedCache(0x1000, 0x1000)
     for kw in (dict(block_table=None), dict(seq_lens=None), dict(cu_tokens=None), dict(n_seqs=0),
-               dict(table_width=0), dict(n_tokens=-1), dict(max_tokens=-1)):
+               dict(table_width=0), dict(n_tokens=-1), dict(max_tokens=-1), dict(max_tokens=0)):
         assert set(_calls(cfg, cache, _batch(**kw))) == {kvq.KVQ_EINVAL}, kw
     for kw in (dict(n_seqs=2049), dict(table_width=1 << 40), dict(n_tokens=1 << 31)):
         assert set(_calls(cfg, cache, _batch(**kw))) == {kvq.KVQ_EUNSUPPORTED}, kw
@@ -115,6 +115,9 @@ def test_calls_refuse_before_touching_the_device():
                      (dict(out=0x3004), kvq.KVQ_EALIGN)):
         assert _calls(cfg, cache, ok, **kw)[2] == code, kw
     assert _calls(cfg, cache, ok, out=0x3004)[1] == kvq.KVQ_EALIGN
+    # outputs apart from the queries, and from each other
+    assert _calls(cfg, cache, ok, out=0x2000)[1:] == (kvq.KVQ_EINVAL, kvq.KVQ_EINVAL)
+    assert _calls(cfg, cache, ok, out=0x2000 + 16 * 256 * 2 - 16)[1:] == (kvq.KVQ_EINVAL,) * 2
     # nothing to do: no launch, no pointer needed
     assert set(_calls(cfg, cache, _batch(n_tokens=0), rows=None)) == {kvq.KVQ_OK}
     assert kvq.lib().kvq_last_launch_count() == 0
