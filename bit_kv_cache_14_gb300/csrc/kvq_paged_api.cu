@@ -45,7 +45,6 @@ static int resolve_call(const kvq_paged_config *cfg, const kvq_paged_cache *cach
   if (!batch->block_table || !batch->seq_lens || !batch->cu_tokens) return KVQ_EINVAL;
   if (batch->n_seqs < 1 || batch->table_width < 1 || batch->n_tokens < 0 || batch->max_tokens < 0)
     return KVQ_EINVAL;
-  if (batch->n_tokens > 0 && batch->max_tokens < 1) return KVQ_EINVAL;
   if (batch->n_seqs > kMaxSeqs) return KVQ_EUNSUPPORTED;
   // positions and row counts are int32 on the device
   if (batch->table_width > (1LL << 30) / p->page || batch->n_tokens > (1LL << 30) ||

@@ -16,7 +16,8 @@ size_t paged_workspace_bytes() { return paged_rows_workspace() + paged_chunk_wor
 cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, void *out,
                                    float scale, void *ws, cudaStream_t st, int *launches) {
   const int sms = num_sms_cached();
-  const int64_t most = (int64_t)p.max_tokens * p.rg;
+  // (a call without rows, only padding, still looks whether that is so)
+  const int64_t most = (int64_t)(p.max_tokens > 0 ? p.max_tokens : 1) * p.rg;
   // a mixed call's small sequences are decode steps: the 8-row form of the
   // split kernel, where the heads of one token fit it
   const int few = (most <= 8 || (most > kPagedFewRows && p.rg <= 8)) ? 8 : kPagedFewRows;

@@ -9,7 +9,7 @@ namespace kvq {
 namespace {
 
 constexpr int kIoThreads = 256;
-constexpr int kIoBatch = 4;  // rows of a warp in flight
+constexpr int kIoBatch = 2;  // pairs of loads of a warp in flight
 
 // The sequence of row t, found by the whole warp (32 candidates a round), or -1
 // for padding (also for a cu_tokens array that does not increase around t).
@@ -43,25 +43,37 @@ __device__ __forceinline__ uint32_t pack2(float x0, float x1) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Packed minimum, maximum (of numbers) and the maximum that keeps NaN.
+// Packed minimum and maximum; NaN where either side is.
 template <int BF16>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   uint32_t d;
-  if (BF16) asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  if (BF16) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 template <int BF16>
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   uint32_t d;
-  if (BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  if (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
 // One 16-bit input as the stored form takes it: saturated, NaN as 0.
 __device__ __forceinline__ float tame(float x) {
   return x == x ? fminf(fmaxf(x, -kPagedLimit), kPagedLimit) : 0.0f;
+}
+
+// x / (2^BITS - 1), rounded to nearest even as the IEEE division does: the
+// product with the rounded reciprocal, corrected once by its remainder
+// (Markstein's quotient; compared with the division for every mantissa of x and
+// the three divisors).  For quotients in the normal range; a smaller one may
+// differ in its last bit, far below what the fp16 scale keeps.
+template <int BITS>
+__device__ __forceinline__ float over_top(float x) {
+  constexpr float kTop = (float)((1 << BITS) - 1), kInv = 1.0f / kTop;
+  const float q = __fmul_rn(x, kInv);
+  return fmaf(fmaf(-kTop, q, x), kInv, q);
 }
 
 // clamp(rint((x - zero) / scale)) by the IEEE division.
@@ -75,124 +87,119 @@ __device__ __forceinline__ float careful_code(float x, float zero, float scale) 
 // lane l its channels 8*l .. 8*l + 7 (w): group l / 4, quarter j = l % 4 of the
 // key layout, eighths 2*j and 2*j + 1 of the value layout.
 //
-// What bounds it is the instructions per element (about 15 lane operations at
+// What bounds it is the instructions per element (about 14 lane operations at
 // the rate HBM delivers), so: minima and maxima on packed pairs; one reciprocal
-// per group; rint by adding 1.5 * 2^23; codes put together as exact fp32 sums
-// code_k * 2^(k*bits).  The hardware reciprocal is within 2^-23 of 1 / scale
-// and each rounding within 2^-24, so the product is within 2^-13 of the IEEE
-// quotient for quotients below 2^8 + 1; the integer is the same for both unless
-// the product lies within kTieGuard = 2^-12 of a half-integer.  Threads that see
-// such a product, a scale under 2^-13 (where its own rounding could pass the
-// code range) or an input to tame go through the division.
-template <int D, int BITS, int BF16>
-__device__ __forceinline__ void quantize_row(uint4 w4, int l, bool value, uint8_t *codes,
-                                             __half *stats) {
+// per group; rint by adding 1.5 * 2^23 in the fma that forms the quotient; codes
+// put together as integer sums.  The hardware reciprocal is within 2^-23 of
+// 1 / scale and the IEEE quotient within 2^-24 of the true one, so for quotients
+// below 2^8 + 1 the two are less than 2^-14 apart, and the integer is the same
+// for both unless the quotient lies within kTieGuard = 2^-12 of a half-integer.
+// Threads that see such a quotient, or a scale under 2^-13 (where its own
+// rounding could pass the code range), go through the division; groups with
+// inputs to tame are tamed first.
+template <int D, int BITS, int BF16, bool VALUE>
+__device__ __forceinline__ void quantize_row(uint4 w4, int l, uint8_t *codes, __half *stats) {
   constexpr int NG = D / kPagedGroup;
   constexpr unsigned kAll = 0xffffffffu;
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  constexpr uint32_t kSign = 0x80008000u;
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23 = 0x4b400000
+  constexpr uint32_t kMagicBits = 0x4b400000u, kSign = 0x80008000u;
   uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-  // magnitudes as integers: larger than LIMIT, infinite and NaN compare alike
-  constexpr uint32_t kTop = BF16 ? 0x4700u : 0x7800u;  // 32768
-  uint32_t big = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) big = __vmaxu2(big, w[i] & ~kSign);
-  const bool wild = (big & 0xffffu) > kTop || (big >> 16) > kTop;
-  const bool any_wild = __any_sync(kAll, wild);
-  if (any_wild) {
+  float mn, mx;
+  auto ends = [&]() {  // (-min, max) of the group, packed
+    const uint32_t hi = max2<BF16>(max2<BF16>(w[0], w[1]), max2<BF16>(w[2], w[3]));
+    const uint32_t lo = min2<BF16>(min2<BF16>(w[0], w[1]), min2<BF16>(w[2], w[3])) ^ kSign;
+    uint32_t mm = max2<BF16>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+    mm = max2<BF16>(mm, __shfl_xor_sync(kAll, mm, 1));
+    mm = max2<BF16>(mm, __shfl_xor_sync(kAll, mm, 2));
+    const float2 e = unpack2<BF16>(mm);
+    mn = -e.x, mx = e.y;
+  };
+  ends();
+  if (__any_sync(kAll, !(mx <= kPagedLimit && mn >= -kPagedLimit))) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 x = unpack2<BF16>(w[i]);
       w[i] = pack2<BF16>(tame(x.x), tame(x.y));
     }
+    ends();
   }
-  // (-min, max) of the group, packed
-  const uint32_t mx2 = max2<BF16>(max2<BF16>(w[0], w[1]), max2<BF16>(w[2], w[3]));
-  const uint32_t mn2 = min2<BF16>(min2<BF16>(w[0], w[1]), min2<BF16>(w[2], w[3])) ^ kSign;
-  uint32_t mm = max2<BF16>(__byte_perm(mn2, mx2, 0x5410), __byte_perm(mn2, mx2, 0x7632));
-  mm = max2<BF16>(mm, __shfl_xor_sync(kAll, mm, 1));
-  mm = max2<BF16>(mm, __shfl_xor_sync(kAll, mm, 2));
-  const float2 ends = unpack2<BF16>(mm);
-  const float mn = -ends.x, mx = ends.y;
-  const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), (float)((1 << BITS) - 1)));
+  const __half s16 = __float2half_rn(over_top<BITS>(__fsub_rn(mx, mn)));
   const __half z16 = __float2half_rn(canon_zero(mn));
   const float s = __half2float(s16), z = __half2float(z16);
-  const float inv = recip_or_zero(s);
-  float c[8], far = 0.0f;
+  float inv;  // (a scale of 0 takes the careful way below)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  // keys: even channels then odd ones; values: in order
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = VALUE ? w[i] : __byte_perm(w[2 * (i & 1)], w[2 * (i & 1) + 1], i < 2 ? 0x5410 : 0x7632);
+  uint32_t y[8];  // kMagicBits + code
+  float far = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = unpack2<BF16>(w[i]);
-    const float r0 = __fmul_rn(__fsub_rn(x.x, z), inv), r1 = __fmul_rn(__fsub_rn(x.y, z), inv);
-    c[2 * i] = __fsub_rn(__fadd_rn(r0, kMagic), kMagic);
-    c[2 * i + 1] = __fsub_rn(__fadd_rn(r1, kMagic), kMagic);
-    far = fmaxf(far, fmaxf(fabsf(__fsub_rn(r0, c[2 * i])), fabsf(__fsub_rn(r1, c[2 * i + 1]))));
+    const float2 x = unpack2<BF16>(v[i]);
+    const float d0 = __fsub_rn(x.x, z), d1 = __fsub_rn(x.y, z);
+    const float y0 = fmaf(d0, inv, kMagic), y1 = fmaf(d1, inv, kMagic);
+    far = fmaxf(far, fmaxf(fabsf(fmaf(d0, inv, kMagic - y0)), fabsf(fmaf(d1, inv, kMagic - y1))));
+    y[2 * i] = __float_as_uint(y0);
+    y[2 * i + 1] = __float_as_uint(y1);
   }
   if (far > 0.5f - kTieGuard || s < 1.0f / 8192.0f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack2<BF16>(w[i]);
-      c[2 * i] = careful_code<BITS>(x.x, z, s);
-      c[2 * i + 1] = careful_code<BITS>(x.y, z, s);
+      const float2 x = unpack2<BF16>(v[i]);
+      y[2 * i] = __float_as_uint(careful_code<BITS>(x.x, z, s) + kMagic);
+      y[2 * i + 1] = __float_as_uint(careful_code<BITS>(x.y, z, s) + kMagic);
     }
   }
+  // four codes of BITS bits in a word (the magic numbers taken out again)
+  constexpr uint32_t kFour =
+      kMagicBits * (1u + (1u << BITS) + (1u << 2 * BITS) + (1u << 3 * BITS));
+  auto four = [&](int k) {
+    return y[k] + (y[k + 1] << BITS) + (y[k + 2] << 2 * BITS) + (y[k + 3] << 3 * BITS) - kFour;
+  };
+  const uint32_t lo = four(0), hi = four(4);
 
   const int grp = l >> 2, j = l & 3, e = grp & 1, h = grp >> 1;
   // Key words: pair k (channels 2k, 2k+1) at bit k*BITS of each 16-bit half.
   // Value words: this group's channels at bits i*BITS of half e, so the two
   // lanes of a pair of groups swap one eighth each and hold a full word.
-  float q[8];  // low half's four codes, then the high half's
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    q[k] = value ? c[k] : c[2 * k];
-    q[4 + k] = value ? c[4 + k] : c[2 * k + 1];
+  uint32_t a = lo, b = hi;  // what goes to the low halves and to the high halves
+  if (VALUE) {
+    const uint32_t got = __shfl_xor_sync(kAll, e ? lo : hi, 4);
+    a = e ? got : lo;
+    b = e ? hi : got;
   }
-  auto sum2 = [&](int k) { return fmaf(q[k + 1], (float)(1 << BITS), q[k]); };
-  auto whole = [&](float x) { return __float_as_uint(x + kMagic) & 0x1ffffu; };
-  uint32_t lo, hi;
-  if (BITS == 8) {
-    lo = whole(sum2(0)) | whole(sum2(2)) << 16;
-    hi = whole(sum2(4)) | whole(sum2(6)) << 16;
-  } else {
-    lo = whole(fmaf(sum2(2), (float)(1 << (2 * BITS)), sum2(0)));
-    hi = whole(fmaf(sum2(6), (float)(1 << (2 * BITS)), sum2(4)));
-  }
-  // keys keep (lo, hi) = (even, odd channels); values trade with the lane of
-  // the other group of the pair
-  const uint32_t got = __shfl_xor_sync(kAll, e ? lo : hi, 4);
-  const uint32_t a = value && e ? got : lo;   // what goes to the low halves
-  const uint32_t b = value && !e ? got : hi;  // and to the high halves
   if (BITS == 8) {
     const uint2 word = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-    uint8_t *dst = value ? codes + (2 * j + e) * (D / 8) + h * 8 : codes + j * (D / 4) + grp * 8;
+    uint8_t *dst = VALUE ? codes + (2 * j + e) * (D / 8) + h * 8 : codes + j * (D / 4) + grp * 8;
     *reinterpret_cast<uint2 *>(dst) = word;
   } else if (BITS == 4) {
-    uint8_t *dst = value ? codes + (2 * j + e) * (D / 16) + h * 4 : codes + j * (D / 8) + grp * 4;
+    uint8_t *dst = VALUE ? codes + (2 * j + e) * (D / 16) + h * 4 : codes + j * (D / 8) + grp * 4;
     *reinterpret_cast<uint32_t *>(dst) = a | (b << 16);
+  } else if (VALUE && D == 64) {
+    // one pair of groups: the eighth is two bytes
+    *reinterpret_cast<uint16_t *>(codes + (2 * j + e) * 2) = (uint16_t)(a | (b << 8));
   } else {
     // 2 bits: a word holds two groups (keys) or two pairs of groups (values)
-    const int part = value ? h : e;
+    const int part = VALUE ? h : e;
     const uint32_t word = (a | (b << 16)) << (8 * part);
-    const uint32_t other = __shfl_xor_sync(kAll, word, value ? 8 : 4);
-    if (value && D == 64) {
-      // one pair of groups: the eighth is two bytes
-      *reinterpret_cast<uint16_t *>(codes + (2 * j + e) * 2) = (uint16_t)(a | (b << 8));
-    } else if (part == 0) {
-      uint8_t *dst = value ? codes + (2 * j + e) * (D / 32) : codes + j * (D / 16) + h * 4;
-      *reinterpret_cast<uint32_t *>(dst) = word | other;
-    }
+    const uint32_t other = __shfl_xor_sync(kAll, word, VALUE ? 8 : 4);
+    uint8_t *dst = VALUE ? codes + (2 * j + e) * (D / 32) : codes + j * (D / 16) + h * 4;
+    if (part == 0) *reinterpret_cast<uint32_t *>(dst) = word | other;
   }
   if (j < 2) stats[grp + NG * j] = j ? z16 : s16;
 }
 
-// One warp per row and group of heads: a warp instruction covers the key and
-// the value of one head (d = 128) or of two (d = 64), kIoBatch of them in
-// flight.
+// One warp per row and group of heads: a warp instruction covers the keys, and
+// the next the values, of two heads (d = 128) or of four (d = 64); kIoBatch of
+// those pairs in flight.
 template <int D, int BITS, int BF16>
 __global__ void __launch_bounds__(kIoThreads)
 paged_write_kernel(const __grid_constant__ Paged p, const uint16_t *k, int64_t ks,
                    const uint16_t *v, int64_t vs, int groups) {
-  constexpr int LR = D / 8;            // lanes of one row
-  constexpr int HW = 32 / (2 * LR);    // heads per warp instruction
+  constexpr int LR = D / 8;      // lanes of one row
+  constexpr int HW = 32 / LR;    // heads per warp instruction
   constexpr int RB = D * BITS / 8, SB = 4 * D / kPagedGroup;
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * (kIoThreads / 32) + (threadIdx.x >> 5);
@@ -200,32 +207,36 @@ paged_write_kernel(const __grid_constant__ Paged p, const uint16_t *k, int64_t k
   int h0 = 0;
   if (groups > 1) t = item / groups, h0 = (int)(item % groups) * kIoBatch * HW;
   if (t >= p.T) return;
-  const bool value = (lane / LR) & 1;
-  const int l = lane % LR, hl = h0 + (lane / (2 * LR)) % HW;
+  const int l = lane % LR, hl = h0 + lane / LR;
   const int b = warp_seq_of_row(p, t);
   if (b < 0) return;
   const int64_t pos = row_position(p, b, t);
   if (pos < 0) return;
-  const uint16_t *src = (value ? v + t * vs : k + t * ks) + 8 * l;
+  k += t * ks + 8 * l;
+  v += t * vs + 8 * l;
   // (lanes past the last head repeat it and store the same bytes as the lanes
   // that hold it)
-  uint4 w[kIoBatch];
+  uint4 wk[kIoBatch], wv[kIoBatch];
 #pragma unroll
   for (int i = 0; i < kIoBatch; ++i)
-    if (h0 + i * HW < p.H)
-      w[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)min(hl + i * HW, p.H - 1) * D));
+    if (h0 + i * HW < p.H) {
+      const int h = min(hl + i * HW, p.H - 1);
+      wk[i] = __ldg(reinterpret_cast<const uint4 *>(k + h * D));
+      wv[i] = __ldg(reinterpret_cast<const uint4 *>(v + h * D));
+    }
   uint8_t *atom = atom_of(p, b, pos);
   if (!atom) return;
   // (every exit above is the whole warp's)
-  const int row = (int)(pos % kAtom);
-  const int code_at = (value ? kAtom * RB : 0) + row * RB;
-  const int stat_at = 2 * kAtom * RB + (value ? kAtom * SB : 0) + row * SB;
+  const int row = (int)(pos & (kAtom - 1)), head_bytes = (int)p.head_bytes;
+  atom += row * RB;
+  const int stat_at = 2 * kAtom * RB + row * (SB - RB);
 #pragma unroll
   for (int i = 0; i < kIoBatch; ++i) {
     if (h0 + i * HW >= p.H) break;
-    uint8_t *at = atom + min(hl + i * HW, p.H - 1) * p.head_bytes;
-    quantize_row<D, BITS, BF16>(w[i], l, value, at + code_at,
-                                reinterpret_cast<__half *>(at + stat_at));
+    uint8_t *at = atom + (int64_t)min(hl + i * HW, p.H - 1) * head_bytes;
+    quantize_row<D, BITS, BF16, false>(wk[i], l, at, reinterpret_cast<__half *>(at + stat_at));
+    quantize_row<D, BITS, BF16, true>(wv[i], l, at + kAtom * RB,
+                                      reinterpret_cast<__half *>(at + stat_at + kAtom * SB));
   }
 }
 
@@ -335,7 +346,7 @@ template <int D, int BITS>
 cudaError_t write_as(const Paged &p, const void *k, int64_t ks, const void *v, int64_t vs,
                      cudaStream_t st) {
   int groups;
-  const unsigned grid = io_grid(p, kIoBatch * (32 / (2 * D / 8)), &groups);
+  const unsigned grid = io_grid(p, kIoBatch * (32 / (D / 8)), &groups);
   auto kern = p.bf16 ? paged_write_kernel<D, BITS, 1> : paged_write_kernel<D, BITS, 0>;
   kern<<<grid, kIoThreads, 0, st>>>(p, static_cast<const uint16_t *>(k), ks,
                                     static_cast<const uint16_t *>(v), vs, groups);

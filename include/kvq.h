@@ -458,7 +458,7 @@ typedef struct kvq_paged_cache {
  *     is position seq_lens[b] - n_b + i.  cu[0] = 0, not decreasing.
  * Host values: n_seqs (1..2048), table_width, n_tokens = rows of the packed
  * arrays (rows from cu[n_seqs] on are padding: never read, never written),
- * max_tokens >= every n_b (at least 1 where n_tokens > 0).
+ * max_tokens >= every n_b.
  * What the device arrays say is checked there: a row at a negative position
  * is skipped (write), reads as zeros (read), attends to nothing (attention);
  * a token whose page entry lies outside [0, n_pages) or behind table_width is

@@ -431,10 +431,11 @@ def test_runs_on_the_stream_it_is_given():
     assert torch.equal(v.cpu(), c.expected_rows("v", c.rows))
 
 
-def test_too_many_rows_for_max_tokens_is_reported():
+@pytest.mark.parametrize("most", (0, 2, 19))
+def test_too_many_rows_for_max_tokens_is_reported(most):
     c = Case([100, 50], [20, 1], 4, 2, 128, 4, 32, F16)
     cache = c.filled()
-    batch = c.batch(max_tokens=2)
+    batch = c.batch(max_tokens=most)
     out = torch.full((21, 4, 128), 7.0, dtype=F16, device="cuda")
     cache.attend(c.queries(), batch, out=out)
     assert cache.device_status() == kvq.KVQ_EINVAL

@@ -55,6 +55,21 @@ def test_worked_group():
     assert values(c, s, z)[31] == 15 * np.float32(s[0])
 
 
+@pytest.mark.parametrize("top", (3, 15, 255))
+def test_corrected_quotient_is_the_division(top):
+    """The write kernel's x / (2^b - 1): q = x * r, then q + (x - top * q) * r,
+    each fma rounded once, equals the IEEE quotient for every mantissa (scaling
+    by powers of two changes neither)."""
+    x = (np.arange(1 << 23, dtype=np.uint32) | 0x3F800000).view(np.float32)
+    r = np.float32(1) / np.float32(top)
+    q = x * r
+    # both fmas in 64 bits: the remainder is exact there, the last sum off by
+    # 2^-53 relative, far from any float32 tie it could cross
+    rem = (x.astype(np.float64) - np.float64(top) * q).astype(np.float32)
+    got = (rem.astype(np.float64) * np.float64(r) + q.astype(np.float64)).astype(np.float32)
+    assert np.array_equal(got, x / np.float32(top))
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(head_dim=96), kvq.KVQ_EUNSUPPORTED), (dict(bits=3), kvq.KVQ_EUNSUPPORTED),
     (dict(bits=16), kvq.KVQ_EUNSUPPORTED), (dict(page_size=24), kvq.KVQ_EUNSUPPORTED),
@@ -91,7 +106,7 @@ def _calls(cfg, cache, batch, rows=0x2000, stride=1024, out=0x3000, scale=0.1, w
 def test_calls_refuse_before_touching_the_device():
     cfg, cache = _cfg(), kvq._PagedCache(0x1000, 0x1000)
     for kw in (dict(block_table=None), dict(seq_lens=None), dict(cu_tokens=None), dict(n_seqs=0),
-               dict(table_width=0), dict(n_tokens=-1), dict(max_tokens=-1), dict(max_tokens=0)):
+               dict(table_width=0), dict(n_tokens=-1), dict(max_tokens=-1)):
         assert set(_calls(cfg, cache, _batch(**kw))) == {kvq.KVQ_EINVAL}, kw
     for kw in (dict(n_seqs=2049), dict(table_width=1 << 40), dict(n_tokens=1 << 31)):
         assert set(_calls(cfg, cache, _batch(**kw))) == {kvq.KVQ_EUNSUPPORTED}, kw
