@@ -515,10 +515,11 @@ int kvq_paged_read(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
  *   softmax_scale: any finite number.
  *   ws: device scratch, ws_bytes >= kvq_paged_workspace_bytes.
  * Arithmetic: scores, weights' sums and outputs are held in fp32; the operands
- * of the two products are rounded to fp16 (the query relative to the largest
- * of its row, the weights, and for sequences of more than 16 query rows per KV
- * head, a row being one token and query head, the values x_hat), which costs
- * about what one fp16 rounding of the output does.
+ * of the two products are rounded to fp16: the query (relative to the largest
+ * of its row), the weights, and for sequences of more than 16 query rows per KV
+ * head, a row being one token and query head, the values x_hat.  Measured, the
+ * output is off by 2.5e-4 (few rows) or 4e-4 to 8e-4 (chunks) of its size, where
+ * its own rounding to fp16 is 2e-4 and to bf16 1.7e-3.
  * Errors: as kvq_paged_write; KVQ_EINVAL also where q and out overlap;
  *   KVQ_ECAPACITY (ws too small).
  */
