@@ -44,10 +44,10 @@ cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, vo
                                    float scale, void *ws, cudaStream_t st, int *launches);
 size_t paged_workspace_bytes();
 cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                              int few, bool early, void *ws, int num_sms, cudaStream_t st);
+                              int few, bool beside, void *ws, int num_sms, cudaStream_t st);
 size_t paged_rows_workspace();
 cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                               int few, bool early, void *ws, int num_sms, cudaStream_t st);
+                               int few, void *ws, int num_sms, cudaStream_t st);
 size_t paged_chunk_workspace();
 int num_sms_cached();
 

@@ -23,13 +23,14 @@ cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, vo
   const int few = (most <= 8 || (most > kPagedFewRows && p.rg <= 8)) ? 8 : kPagedFewRows;
   const bool rows = p.rg <= few, chunks = most > few;
   cudaError_t e = cudaSuccess;
-  // Alone, the split kernel may start its blocks while the kernel before the
-  // call ends (it waits before it reads).  Together, the split kernel starts
-  // when everything before it is done, and the other one beside it.
-  if (rows) e = launch_paged_rows(p, q, qs, out, scale, few, !chunks, ws, sms, st);
-  if (e == cudaSuccess && chunks)
-    e = launch_paged_chunk(p, q, qs, out, scale, few, rows,
+  // The split kernel may start its blocks while the kernel before it ends: alone
+  // it waits there before it reads; behind the chunk kernel, which starts when
+  // everything before the call is done, it takes the room that one leaves.
+  if (chunks)
+    e = launch_paged_chunk(p, q, qs, out, scale, few,
                            static_cast<uint8_t *>(ws) + paged_rows_workspace(), sms, st);
+  if (e == cudaSuccess && rows)
+    e = launch_paged_rows(p, q, qs, out, scale, few, chunks, ws, sms, st);
   *launches = (int)rows + (int)chunks;
   return e;
 }

@@ -26,10 +26,10 @@
 //   (warps 18, 19 only give up registers)
 //
 // Split: every (sequence, head, 256-row tile) is a list of its visible 128-token
-// steps.  Where all tiles in pieces of about kPiece steps give no more pieces
-// than there are blocks, each block takes a piece; a longer list, kOver units
-// added to each tile for its start and end, is cut into equal ranges, one per
-// block.  A tile that several blocks share leaves partials, joined in block
+// steps.  Where all tiles in pieces of about 6, 8 or 12 steps (the smallest that
+// does) give no more pieces than there are blocks, each block takes a piece; a
+// longer list, kOver units added to each tile for its start and end, is cut into
+// equal ranges, one per block.  A tile that several blocks share leaves partials, joined in block
 // order by the block that finishes last.
 #include "kvq_paged.cuh"
 #include "kvq_tc_common.cuh"
@@ -53,8 +53,12 @@ constexpr int kPWarps = kMmaWarp - kProducerWarp;
 constexpr int kStep = 128;       // cached tokens per step
 constexpr int kTileRows = 256;   // query rows per block
 constexpr int kOver = 6;         // units of a tile's start and end, which take about as long
-constexpr int kMinUnits = 16;
-constexpr int kPiece = 6;        // steps worth a block of their own
+constexpr int kMinUnits = 16;    // (borders move by up to kOver + 1 units)
+// Steps worth a block of their own: joining the parts of a tile costs about four
+// steps' time (a 512-token chunk in pieces of 4, 6 and 10 steps: all within 1 %,
+// 128 tokens over 4096: 50.5, 47.7, 50.4 us).
+constexpr int kPieceSizes = 3;
+__host__ __device__ constexpr int piece_size(int k) { return k == 0 ? 6 : k == 1 ? 8 : 12; }
 constexpr int kMaxChunkBlocks = 160;
 constexpr int kChunkWait = 1 << 25;
 constexpr float kChunkSlack = 8.0f;  // log2 units a score may pass the reference by
@@ -73,7 +77,6 @@ struct ChunkArgs {
   float *ws_o;       // [2 * blocks][2 tiles][d / 4][128] float4
   int *ws_count;     // [blocks][2 tiles], zero between calls
   int stall_limit;
-  bool early;        // launched behind the split kernel of the same call, see below
 };
 
 template <int D>
@@ -90,7 +93,7 @@ struct ChunkCfg {
   static constexpr int off_misc = off_item + kItems * 64;  // tensor memory base, dead flag, flags
   static constexpr int smem = off_misc + 64 + 1024;
   // the running sums of the plan lie where the operands come later
-  static_assert(2 * (kMaxSeqs + 1) * 8 <= 2 * kTile + 4 * kTile, "room for the plan");
+  static_assert((1 + kPieceSizes) * (kMaxSeqs + 1) * 8 <= 6 * kTile, "room for the plan");
 };
 
 // ---- PTX ------------------------------------------------------------------
@@ -269,7 +272,9 @@ __device__ __forceinline__ int steps_of(const ChunkArgs &a, const Seq &s, int t)
   return see < 1 ? 1 : (int)((see + kStep - 1) / kStep);
 }
 
-__device__ __forceinline__ int pieces_of(int steps) { return max(1, (steps + kPiece / 2) / kPiece); }
+__device__ __forceinline__ int pieces_of(int steps, int size) {
+  return max(1, (steps + size / 2) / size);
+}
 
 // One block's share of one tile, as the roles read it from shared memory.
 struct __align__(16) Item {
@@ -308,6 +313,9 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   // (through a shuffle, so that the compiler knows it to be uniform)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
+  // the split kernel of the same call may run where this one leaves room
+  grid_dep_trigger();
+
   // barriers
   const uint32_t bars = smem_s + C::off_bar;
   auto bar_q = [&](int i) { return bars + 8u * i; };             // queries of tile i are in
@@ -323,7 +331,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::off_misc);
   volatile uint32_t *dead = misc + 1;
   int64_t *units = reinterpret_cast<int64_t *>(smem);  // running sums over the sequences
-  int64_t *pieces = units + kMaxSeqs + 1;
+  // and kPieceSizes times those of the pieces
   int64_t *sh_x = reinterpret_cast<int64_t *>(misc + 4);  // borders of the block's range
   int *sh_at = reinterpret_cast<int *>(misc + 8);         // b, h, t, off of its first unit
 
@@ -351,10 +359,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     bar_init(reinterpret_cast<uint64_t *>(smem + C::off_bar) + 16, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     misc[1] = 0;
-    units[0] = pieces[0] = 0;
+    for (int i = 0; i <= kPieceSizes; ++i) units[i * (kMaxSeqs + 1)] = 0;
   }
 
-  // ---- units[b + 1], pieces[b + 1]: of one head of sequences 0 .. b
+  // ---- units (and pieces) of one head of sequences 0 .. b at [b + 1]
   for (int b = warp; b < p.B; b += kChunkThreads / 32) {
     const Seq s = seq_of(a, b);
     if (lane == 0 && blockIdx.x == 0) {
@@ -362,22 +370,23 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       if (s.rows > 0 && p.lens[b] > p.width * p.page) paged_error(p, KVQ_EPAGE);
     }
     const int tiles = (s.rows + kTileRows - 1) / kTileRows;
-    int64_t sum = 0, psum = 0;
+    int64_t sum[1 + kPieceSizes] = {};
     for (int t = lane; t < tiles; t += 32) {
       const int steps = steps_of(a, s, t);
-      sum += steps + kOver;
-      psum += pieces_of(steps);
+      sum[0] += steps + kOver;
+#pragma unroll
+      for (int i = 0; i < kPieceSizes; ++i) sum[1 + i] += pieces_of(steps, piece_size(i));
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      psum += __shfl_xor_sync(0xffffffffu, psum, o);
+    for (int i = 0; i <= kPieceSizes; ++i) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+      if (lane == 0) units[i * (kMaxSeqs + 1) + b + 1] = sum[i];
     }
-    if (lane == 0) units[b + 1] = sum, pieces[b + 1] = psum;
   }
   __syncthreads();
-  if (warp < 2) {  // running sums, 32 sequences at a time
-    int64_t *sums = warp ? pieces : units, before = 0;
+  if (warp <= kPieceSizes) {  // running sums, 32 sequences at a time
+    int64_t *sums = units + warp * (kMaxSeqs + 1), before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       int64_t v = b0 + lane < p.B ? sums[b0 + lane + 1] : 0;
 #pragma unroll
@@ -391,14 +400,20 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     }
   }
   __syncthreads();
-  const bool by_piece = p.H * pieces[p.B] <= gridDim.x;
-  const int64_t *prefix = by_piece ? pieces : units;
+  int size = 0;  // of the pieces, or 0
+  const int64_t *prefix = units;
+#pragma unroll
+  for (int i = kPieceSizes - 1; i >= 0; --i) {
+    const int64_t *sums = units + (1 + i) * (kMaxSeqs + 1);
+    if (p.H * sums[p.B] <= gridDim.x) size = piece_size(i), prefix = sums;
+  }
+  const bool by_piece = size > 0;
   const int64_t total = p.H * prefix[p.B];
   const int64_t U =
       by_piece ? 1 : max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)kMinUnits);
   auto cost_of = [&](const Seq &s, int t) {
     const int steps = steps_of(a, s, t);
-    return by_piece ? pieces_of(steps) : steps + kOver;
+    return by_piece ? pieces_of(steps, size) : steps + kOver;
   };
   // ---- the block's borders: warp 0 its first unit, warp 1 the next block's.
   // A border inside a tile's first units moves to its start, one at its last
@@ -456,14 +471,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   }
   __syncthreads();
   const int64_t x0 = sh_x[0], x1 = sh_x[1];
-  // Behind the split kernel of the same call this one runs as soon as there is
-  // room: that kernel started after everything before the call was done, and
-  // the two write different rows.  Only the end waits, so that this kernel's
-  // completion stands for both.
-  if (x0 >= x1) {
-    grid_dep_wait();
-    return;
-  }
+  if (x0 >= x1) return;
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -1228,7 +1236,6 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     }
   }
   tc_fence_before();
-  grid_dep_wait();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -1256,7 +1263,7 @@ cudaError_t chunk_as(const ChunkArgs &a, int num_sms, cudaStream_t st) {
   const cudaError_t e = kernel_setup(setup, kern, kChunkThreads, smem, nullptr);
   if (e != cudaSuccess) return e;
   const int blocks = num_sms < kMaxChunkBlocks ? num_sms : kMaxChunkBlocks;
-  return launch_dependent(kern, (unsigned)blocks, kChunkThreads, smem, st, a.early, a);
+  return launch_dependent(kern, (unsigned)blocks, kChunkThreads, smem, st, false, a);
 }
 
 constexpr size_t kCountBytes = 2 * kMaxChunkBlocks * 4;
@@ -1265,7 +1272,7 @@ constexpr size_t kMlBytes = (size_t)2 * kMaxChunkBlocks * kTileRows * 8;
 }  // namespace
 
 cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                               int few, bool early, void *ws, int num_sms, cudaStream_t st) {
+                               int few, void *ws, int num_sms, cudaStream_t st) {
   ChunkArgs a;
   a.p = p;
   a.q = static_cast<const uint16_t *>(q);
@@ -1274,7 +1281,6 @@ cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *
   a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.few = few;
-  a.early = early;
   uint8_t *w = static_cast<uint8_t *>(ws);
   a.ws_count = reinterpret_cast<int *>(w);
   a.ws_ml = reinterpret_cast<float *>(w + kCountBytes);

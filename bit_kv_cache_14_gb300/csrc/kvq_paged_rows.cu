@@ -53,7 +53,11 @@ struct RowsArgs {
   int *ws_count;   // [blocks], zero between calls
   int few;         // sequences with more rows are not this kernel's
   int stall_limit;
-  bool early;      // the blocks may start while the previous kernel ends
+  // Launched beside the chunk kernel of the same call: that kernel started after
+  // everything before the call was done, and the two write different rows, so
+  // this one does not wait for it to begin, only to end, and its completion
+  // stands for both.
+  bool beside;
 };
 
 template <int D, int BITS, int NT>
@@ -198,7 +202,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   if (lane <= S) bar_init(&bars[lane], 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
-  grid_dep_wait();
+  if (!a.beside) grid_dep_wait();
   // ---- the list of work: prefix[b] = tiles of one head of the sequences
   // before b that have between 1 and a.few rows
   {
@@ -252,7 +256,10 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   int first_b, c_first = blockIdx.x, c_last = blockIdx.x;  // by_piece: the blocks of the pair
   if (by_piece) {
     const int c = blockIdx.x;
-    if (c >= H * pieces[p.B]) return;
+    if (c >= H * pieces[p.B]) {
+      if (a.beside) grid_dep_wait();
+      return;
+    }
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -269,7 +276,10 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
   } else {
     x0 = border(prefix, p.B, H, total, U, blockIdx.x);
     x1 = border(prefix, p.B, H, total, U, blockIdx.x + 1);
-    if (x0 >= x1) return;
+    if (x0 >= x1) {
+      if (a.beside) grid_dep_wait();
+      return;
+    }
     first_b = seq_of_unit(prefix, p.B, H, x0);
   }
 
@@ -900,6 +910,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
       bar_wait(&bars[slot], phase, kDrainLimit);
       if (++slot == S) slot = 0, phase ^= 1;
     }
+  if (a.beside) grid_dep_wait();
 }
 
 template <int D, int BITS, int NT>
@@ -913,13 +924,13 @@ cudaError_t launch_as(RowsArgs &a, int num_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   int blocks = num_sms * occ;
   if (blocks > kPagedRowBlocks) blocks = kPagedRowBlocks;
-  return launch_dependent(kern, (unsigned)blocks, C::kRowThreads, smem, st, a.early, a);
+  return launch_dependent(kern, (unsigned)blocks, C::kRowThreads, smem, st, true, a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                              int few, bool early, void *ws, int num_sms, cudaStream_t st) {
+                              int few, bool beside, void *ws, int num_sms, cudaStream_t st) {
   RowsArgs a;
   a.p = p;
   a.q = static_cast<const uint16_t *>(q);
@@ -933,7 +944,7 @@ cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *o
                                      2 * kPagedRowBlocks * kPagedFewRows * 8);
   a.stall_limit = debug_stall_limit();
   a.few = few;
-  a.early = early;
+  a.beside = beside;
   const int64_t most = few;
   // one tile of 8 rows when no sequence has more, two otherwise
   if (p.d == 128) {
