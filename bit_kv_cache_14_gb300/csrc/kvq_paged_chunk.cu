@@ -1197,33 +1197,35 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           __threadfence();
           const float2 *ml = reinterpret_cast<const float2 *>(a.ws_ml);
           float m = kNoRef, sum = 0.0f;
-          for (int c = c0; c <= c1; ++c)
-            m = fmaxf(m, __ldcg(ml + ((2 * c + (c == c0)) * 2 + i) * 128 + r).x);
+#pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
             const float2 y = __ldcg(ml + ((2 * c + (c == c0)) * 2 + i) * 128 + r);
-            sum += y.y * exp2_approx(y.x - m);
+            const float nm = fmaxf(m, y.x);
+            sum = sum * exp2_approx(m - nm) + y.y * exp2_approx(y.x - nm);
+            m = nm;
           }
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
           if (in) {
 #pragma unroll 1
             for (int c32 = 0; c32 < D; c32 += 32) {
+              // (two parts' loads in flight; a part without visible tokens is 0)
               float v[32] = {};
-#pragma unroll 1
+#pragma unroll 2
               for (int c = c0; c <= c1; ++c) {
                 const int at = (2 * c + (c == c0)) * 2 + i;
-                const float2 y = __ldcg(ml + at * 128 + r);
-                // (a part without weight left nothing that counts)
-                const float f = y.y == 0.0f ? 0.0f : exp2_approx(y.x - m);
-                if (f == 0.0f) continue;
                 const float4 *src = reinterpret_cast<const float4 *>(a.ws_o) +
                                     (int64_t)at * (D / 4) * 128 + c32 / 4 * 128 + r;
+                float4 w[8];
+                const float2 y = __ldcg(ml + at * 128 + r);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = __ldcg(src + k * 128);
+                const float f = exp2_approx(y.x - m);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                  const float4 w = __ldcg(src + k * 128);
-                  v[4 * k] += f * w.x;
-                  v[4 * k + 1] += f * w.y;
-                  v[4 * k + 2] += f * w.z;
-                  v[4 * k + 3] += f * w.w;
+                  v[4 * k] += f * w[k].x;
+                  v[4 * k + 1] += f * w[k].y;
+                  v[4 * k + 2] += f * w[k].z;
+                  v[4 * k + 3] += f * w[k].w;
                 }
               }
               put(c32, v, inv);
