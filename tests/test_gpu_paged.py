@@ -381,6 +381,14 @@ def test_many_sequences(new):
     assert torch.equal(k.cpu(), c.expected_rows("k", c.rows))
 
 
+def test_most_sequences_at_the_largest_shared_memory():
+    """2048 sequences on the split kernel's 16-row form, the largest block."""
+    c = Case([1 + b % 20 for b in range(2048)], [1] * 2048, 16, 1, 128, 4, 16, BF16)
+    cache = c.filled()
+    c.check_attention(cache.attend(c.queries(), c.batch()))
+    assert cache.device_status() == 0
+
+
 @pytest.mark.parametrize("kv,new,hkv", [(40000, 1, 1), (20000, 40, 1), (9000, 700, 2)])
 def test_long_sequences_are_split_and_joined(kv, new, hkv):
     """Pairs that many blocks share.  The reference is torch in 64 bits on the
