@@ -583,7 +583,8 @@ class PagedKVCache:
         s0, s1, s2 = t.stride()
         if s2 != 1 or (heads > 1 and s1 != d):
             raise ValueError("each row must be contiguous (got strides %s)" % (t.stride(),))
-        return s0 if batch.n_tokens > 1 else max(s0, heads * d)
+        # a single row's stride is never used and may be anything
+        return s0 if batch.n_tokens > 1 else heads * d
 
     def _call(self, fn, batch: PagedBatch, stream, *args) -> None:
         if batch.index != self._index:

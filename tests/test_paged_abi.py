@@ -176,3 +176,13 @@ def test_binding_checks_rows():
             cache._rows(bad, batch, 2)
     with pytest.raises(ValueError):
         kvq.PagedKVCache(_cfg(), "cpu", pages=torch.zeros(16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("stride", (0, 257, 1 << 33))
+def test_stride_of_a_single_row_does_not_matter(stride):
+    cache = kvq.PagedKVCache(_cfg(), device="cpu")
+    i32 = dict(dtype=torch.int32)
+    batch = kvq.PagedBatch(torch.zeros(1, 4, **i32), torch.ones(1, **i32),
+                           torch.tensor([0, 1], **i32), 1)
+    k = torch.empty_strided((1, 2, 128), (stride, 128, 1), dtype=torch.float16)
+    assert cache._rows(k, batch, 2) == 2 * 128
