@@ -77,6 +77,13 @@ __device__ __forceinline__ void paged_error(const Paged &p, int code) {
   atomicCAS(p.status, 0, code);
 }
 
+// Whether sequence b's rows are none of the call's: out of order (their
+// difference could wrap), outside the packed arrays, or more than allowed.
+__device__ __forceinline__ bool bad_rows(const Paged &p, int b) {
+  const int r0 = p.cu[b], r1 = p.cu[b + 1];
+  return r0 < 0 || r1 < r0 || r1 > p.T || r1 - r0 > p.max_tokens;
+}
+
 // Position of row t of sequence b (negative: the row precedes its sequence).
 __device__ __forceinline__ int64_t row_position(const Paged &p, int b, int64_t t) {
   return (int64_t)p.lens[b] - p.cu[b + 1] + t;

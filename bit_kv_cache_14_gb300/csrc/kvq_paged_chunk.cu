@@ -264,13 +264,12 @@ __device__ __forceinline__ Seq seq_of(const ChunkArgs &a, int b) {
   const Paged &p = a.p;
   Seq s;
   s.row0 = p.cu[b];
-  s.tokens = p.cu[b + 1] - s.row0;
+  s.tokens = (int)((unsigned)p.cu[b + 1] - (unsigned)s.row0);
   const int64_t cap = p.width * p.page;
   s.len = (int)min((int64_t)max(p.lens[b], 0), cap);
   s.pos0 = (int64_t)p.lens[b] - s.tokens;
-  const bool ok = s.tokens <= p.max_tokens && s.row0 >= 0 && p.cu[b + 1] <= p.T;
   const int64_t rows = (int64_t)s.tokens * p.rg;
-  s.rows = ok && rows > a.few ? (int)rows : 0;
+  s.rows = !bad_rows(p, b) && rows > a.few ? (int)rows : 0;
   return s;
 }
 // Visible steps of 256-row tile t.
@@ -374,7 +373,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
   for (int b = warp; b < p.B; b += kChunkThreads / 32) {
     const Seq s = seq_of(a, b);
     if (lane == 0 && blockIdx.x == 0) {
-      if (s.tokens > p.max_tokens || s.row0 < 0 || p.cu[b + 1] > p.T) paged_error(p, KVQ_EINVAL);
+      if (bad_rows(p, b)) paged_error(p, KVQ_EINVAL);
       if (s.rows > 0 && p.lens[b] > p.width * p.page) paged_error(p, KVQ_EPAGE);
     }
     const int tiles = (s.rows + kTileRows - 1) / kTileRows;

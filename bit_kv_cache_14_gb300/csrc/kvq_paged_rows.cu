@@ -222,9 +222,9 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     int64_t sum = 0;
     int psum = 0;
     for (int b = b0; b < b1; ++b) {
-      const int n = p.cu[b + 1] - p.cu[b];
+      const int n = (int)((unsigned)p.cu[b + 1] - (unsigned)p.cu[b]);
       int64_t tiles = 0;
-      if (n > p.max_tokens || p.cu[b] < 0 || p.cu[b + 1] > p.T) {
+      if (bad_rows(p, b)) {
         if (blockIdx.x == 0) paged_error(p, KVQ_EINVAL);
       } else if (n > 0 && (int64_t)n * p.rg <= a.few) {
         const int64_t cap = p.width * p.page, len = p.lens[b];

@@ -463,8 +463,9 @@ typedef struct kvq_paged_cache {
  * is skipped (write), reads as zeros (read), attends to nothing (attention);
  * a token whose page entry lies outside [0, n_pages) or behind table_width is
  * skipped, reads as zeros or is not attended to, and KVQ_EPAGE goes to the
- * status word; a sequence with more than max_tokens rows, or with rows behind
- * n_tokens, is not attended for and gives KVQ_EINVAL there.
+ * status word; a sequence with more than max_tokens rows, with rows behind
+ * n_tokens, or whose cu_tokens decrease, is not attended for and gives
+ * KVQ_EINVAL there.
  */
 typedef struct kvq_paged_batch {
   const int32_t *block_table, *seq_lens, *cu_tokens;

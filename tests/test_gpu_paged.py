@@ -450,6 +450,19 @@ def test_too_many_rows_for_max_tokens_is_reported(most):
     assert (out[:20] == 7).all()
 
 
+@pytest.mark.parametrize("cu", ([0, 20, 19, 21], [0, 20, 2**31 - 1, -2**31], [0, 20, -2**31, -1]))
+@pytest.mark.parametrize("most", (1, 20, 2**31 - 1))
+def test_decreasing_row_offsets_are_reported(cu, most):
+    c = Case([100, 50, 30], [20, 1, 1], 4, 2, 128, 4, 32, F16)
+    cache = c.filled()
+    batch = c.batch(max_tokens=most)
+    batch.cu_tokens.copy_(torch.tensor(cu, dtype=torch.int32))
+    out = torch.full((22, 4, 128), 7.0, dtype=F16, device="cuda")
+    cache.attend(c.queries(), batch, out=out)
+    assert cache.device_status() == kvq.KVQ_EINVAL
+    assert (out[21:] == 7).all()
+
+
 def test_serving_loop():
     """What a server does: two prompts enter in chunks, decode together, a third
     joins, one leaves and its pages serve the next; after every step attention
