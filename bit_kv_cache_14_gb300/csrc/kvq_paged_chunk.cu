@@ -928,26 +928,26 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       tc_fence_before();
       bar_arrive_warp(bar_q(i));
     };
-    // the block's next item with rows for this tile, from item n on
+    auto has_rows = [&](const Item *it) { return it->row_first + i * 128 < it->rows; };
     uint32_t item = 0;
-    auto next_item = [&]() -> const Item * {
-      for (;; ++item) {
-        const Item *it = take_item(item);
-        if (!it || it->row_first + i * 128 < it->rows) return it;
-        step += it->j1 - it->j0;
-        bar_arrive_warp(bar_ie(item));
+    const Item *it = nullptr;  // the item at hand, if its queries are in already
+    for (;;) {
+      if (!it) {
+        // the block's next item with rows for this tile
+        for (;; ++item) {
+          it = take_item(item);
+          if (!it || has_rows(it)) break;
+          step += it->j1 - it->j0;
+          bar_arrive_warp(bar_ie(item));
+        }
+        if (!it) break;
+        uint4 w0[LR / 2], w1[LR / 2];
+        load_queries(it, 0, w0);
+        load_queries(it, 1, w1);
+        store_queries(0, w0);
+        store_queries(1, w1);
+        queries_in();
       }
-    };
-    const Item *it = next_item();
-    if (it) {
-      uint4 w0[LR / 2], w1[LR / 2];
-      load_queries(it, 0, w0);
-      load_queries(it, 1, w1);
-      store_queries(0, w0);
-      store_queries(1, w1);
-      queries_in();
-    }
-    while (it) {
       const int row_first = it->row_first + i * 128, rows = it->rows;
       const int j0 = it->j0, j1 = it->j1;
       const float F = fs[r];  // (rows of this warp: written by this warp)
@@ -1113,9 +1113,13 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       if (!ok) break;
 
       // the next item's queries are on their way while the last sums are added,
-      // and its first scores are computed during this item's output
+      // and its first scores are computed during this item's output.  Only the
+      // next item, though: this one still holds its entry of the ring, which the
+      // list refills once all have let go, so a tile that skipped on from here
+      // past items without rows for it could wait for itself.
       const uint32_t this_item = item++;
-      const Item *next = next_item();
+      const Item *next = take_item(item);
+      if (next && !has_rows(next)) next = nullptr;  // taken up after the release
       {
         uint4 w[LR / 2];
         if (next) load_queries(next, 0, w);
