@@ -35,8 +35,12 @@
 //    what HBM waits for.)
 //  * Softmax: a lazy reference per row, moved only when a score passes it by
 //    more than 2 (log2 units), decided by one vote.  The reference also carries
-//    E, the exponent of the largest value scale seen, so that w <= 2^2 and
-//    keeps fp16's full precision whatever the scale of the values.
+//    E, the exponent of the largest value scale seen, and lies kRoom = 12 below,
+//    so that w <= 2^14: where score and scale are the largest so far w is 2^11 or
+//    more, and a w down to 2^-25 of that is a normal fp16 number; a smaller one
+//    keeps an absolute 2^-36 of it.  (Without the room a warp's 1000 weights of
+//    2^-26.5 beside one of 1 went to zero, and one saturated group of values cost
+//    the others up to 2^-6 of their size.)
 #include "kvq_paged.cuh"
 #include "kvq_tc_common.cuh"
 
@@ -48,6 +52,7 @@ namespace {
 
 constexpr int kRowWaitLimit = 1 << 24;
 constexpr float kNoRef = -1e30f;
+constexpr int kRoom = 12;  // log2 units between the reference and the largest weight
 
 struct RowsArgs {
   Paged p;
@@ -510,7 +515,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
 
     float o[NG][2][NT][4] = {}, za[NG][NT][2] = {}, l[NT][2] = {}, rf[NT][2];
     uint32_t e2 = 0;  // largest value scale covered by the reference, in both halves
-    int E = -24;
+    int E = -24 - kRoom;  // the exponent of that, less the room above the reference
     float slack = kSlack - (float)E;  // how far a score may pass the reference
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -637,9 +642,9 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
         float sm = fmaxf(__low2float(smax), __high2float(smax));
 #pragma unroll
         for (int s = 16; s; s >>= 1) sm = fmaxf(sm, __shfl_xor_sync(0xffffffffu, sm, s));
-        const int En = sm > 0.0f ? max(E, ((__float_as_int(sm) >> 23) & 255) - 126) : E;
-        const uint32_t top = h2u(__float2half2_rn(__int_as_float((127 + En) << 23)));
-        e2 = En > 15 ? 0x7bff7bffu : top;
+        const int En = sm > 0.0f ? max(E, ((__float_as_int(sm) >> 23) & 255) - 126 - kRoom) : E;
+        const uint32_t top = h2u(__float2half2_rn(__int_as_float((127 + En + kRoom) << 23)));
+        e2 = En + kRoom > 15 ? 0x7bff7bffu : top;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -16,9 +16,13 @@ output o = sum_t w_t v_t, the variance of channel c's error is at most
 
 A row's error, its norm over the channels, passes KAPPA = 6 deviations with a
 probability of e^-18 or so (bounded errors, sub-Gaussian).  To this come the
-output's own rounding (half a step of its type, element by element) and, for
-weights below 2^-14 of the row's largest, FLOOR of the largest weight times the
-largest m: fp16's absolute step, below the range that the kernels leave above it.
+output's own rounding (half a step of its type, element by element) and fp16's
+absolute step at the weights: one held below 2^-14 is off by up to 2^-25 instead
+of u relative.  A chunk's largest weight is held at 2^7 or more; of few rows,
+weight times value scale at 2^11 or more where both are the largest.  So a weight
+(or its product with its values' scale) below 2^-21 of the largest adds, for the
+row's largest weight, at most 2^-32 of the group's largest m, or 2^-36 of all
+groups' largest.
 A row of zeros, or one 5 % too large, is outside wherever more than a few tokens
 share the weight.
 """
@@ -29,61 +33,70 @@ from paged_util import GROUP, quantize, values
 
 U = 2.0 ** -11
 KAPPA = 6.0
-FLOOR = 2.0 ** -25
+SMALL, FLOOR, FLOOR_ALL = 2.0 ** -21, 2.0 ** -32, 2.0 ** -36
 
 
 def held(case, which, b, device):
-    """(values, zero points) of sequence b's tokens in 64 bits [t][h][d]."""
+    """(values, zero points, scales) of sequence b's tokens in 64 bits [t][h][d]."""
     codes, s, z = quantize(case.K[b] if which == "k" else case.V[b], case.bits)
-    x = torch.from_numpy(values(codes, s, z)).to(device).double()
-    return x, torch.from_numpy(np.repeat(z.astype(np.float64), GROUP, -1)).to(device)
+    wide = lambda y: torch.from_numpy(np.repeat(y.astype(np.float64), GROUP, -1)).to(device)  # noqa: E731
+    return torch.from_numpy(values(codes, s, z)).to(device).double(), wide(z), wide(s)
 
 
-def check_rows(case, out, scale=None, gone=None, floor=FLOOR):
+def check_rows(case, out, scale=None, gone=None, by_group=False, only=None):
     """Asserts that every real row of `out` is within the bound; returns the
     largest fraction of it that was used.  gone[b]: positions of sequence b that
-    are not there (a page that does not exist)."""
+    are not there (a page that does not exist).  by_group: the norm and the bound
+    of each group of 32 channels by itself.  only: these sequences."""
     rg, d, dev = case.hq // case.hkv, case.d, out.device
+    part = GROUP if by_group else d
+    norm = lambda x: x.unflatten(-1, (-1, part)).norm(dim=-1)  # noqa: E731
     scale = d ** -0.5 if scale is None else scale
     half_step = torch.finfo(case.dtype).eps / 2
     assert torch.isfinite(out[:int(case.cu[-1])].float()).all()
     worst = 0.0
     for b, n in enumerate(case.new):
-        if n == 0:
+        if n == 0 or (only is not None and b not in only):
             continue
         at, kv = int(case.cu[b]), max(case.kv[b], 0)
         got = out[at:at + n].double().unflatten(1, (case.hkv, rg)).transpose(0, 1)  # [H][n][rg][d]
+        if kv == 0:
+            assert (got == 0).all()
+            continue
         q = torch.from_numpy(case.q[at:at + n]).to(dev).double()
         q = q.unflatten(1, (case.hkv, rg)).transpose(0, 1)
-        K, _ = held(case, "k", b, dev)
-        V, Z = held(case, "v", b, dev)
+        K, _, _ = held(case, "k", b, dev)
+        V, Z, C = held(case, "v", b, dev)
         t = torch.arange(kv, device=dev)
         hidden = t[None] > (case.kv[b] - n + torch.arange(n, device=dev))[:, None]
         if gone and gone.get(b):
             hidden[:, list(gone[b])] = True
+        hidden = hidden[:, None]
         for h in range(case.hkv):
             k, v = K[:, h], V[:, h]
             m2 = torch.maximum(v * v, (v - Z[:, h]) ** 2)
-            s = scale * (q[h] @ k.T)                                            # [n][rg][t]
-            w = torch.exp((s - s.masked_fill(hidden[:, None], -np.inf)
-                           .amax(-1, keepdim=True).clamp(min=-1e300)).masked_fill(
-                               hidden[:, None], -np.inf)) if kv else s
+            s = (scale * (q[h] @ k.T)).masked_fill(hidden, -np.inf)             # [n][rg][t]
+            w = torch.exp(s - s.amax(-1, keepdim=True).clamp(min=-1e300))
             total = w.sum(-1, keepdim=True)
             w = w / torch.where(total > 0, total, 1.0)
             o = w @ v
             S = scale ** 2 * (2 * U * U * ((q[h] ** 2) @ (k ** 2).T)
                               + (2.0 ** -21 * (q[h].abs() @ k.abs().T)) ** 2)
-            w2 = w * w
-            a = w2 * S
+            a = w * w * S
             var = (a @ (v * v) - 2 * o * (a @ v) + o * o * a.sum(-1, keepdim=True)).clamp(min=0)
-            var = var + U * U * (w2 @ (m2 + v * v))
-            top = w.amax(-1, keepdim=True) if kv else torch.zeros_like(total)
-            small = ((w < 2.0 ** -14 * top) & ~hidden[:, None]).sum(-1)
-            big = m2.amax().sqrt() if kv else 0.0
-            bound = (KAPPA * var.sum(-1).sqrt() + half_step * o.norm(dim=-1)
-                     + floor * small * top[..., 0] * big * d ** 0.5 + 1e-7)
-            err = (got[h] - o).norm(dim=-1)
-            use = float((err / bound).max())
+            var = var + U * U * ((w * w) @ (m2 + v * v))
+            # the weights that may be below fp16's normal range, group by group
+            top = w.amax(-1, keepdim=True)
+            absolute = []
+            for c in range(0, d, GROUP):
+                size = C[:, h, c] / C[:, h].amax().clamp(min=1e-30)
+                small = ((w * size < SMALL * top) | (w < SMALL * top)) & ~hidden
+                big = FLOOR * m2[:, c:c + GROUP].amax().sqrt() + FLOOR_ALL * m2.amax().sqrt()
+                absolute.append(small.sum(-1) * top[..., 0] * big * GROUP ** 0.5)
+            absolute = torch.stack(absolute, -1).unflatten(-1, (d // part, -1)).norm(dim=-1)
+            bound = (KAPPA * var.unflatten(-1, (-1, part)).sum(-1).sqrt() + half_step * norm(o)
+                     + absolute + 1e-7)
+            use = float((norm(got[h] - o) / bound).max())
             assert use <= 1.0, "sequence %d head %d: %.2f of the bound" % (b, h, use)
             worst = max(worst, use)
     return worst

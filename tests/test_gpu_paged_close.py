@@ -2,6 +2,7 @@
 tests/paged_norm.py): the cases that a wrong value somewhere would fail."""
 import random
 
+import numpy as np
 import pytest
 import torch
 
@@ -69,3 +70,57 @@ def test_ragged_prefill_with_missing_pages(hkv):
     out = cache.attend(c.queries(), c.batch())
     assert cache.device_status() == kvq.KVQ_EPAGE
     check_rows(c, out, gone=gone)
+
+
+# ---- small weights beside large ones ----------------------------------------
+
+FORMATS = [(128, 4, F16), (64, 2, F16), (128, 8, F16), (128, 2, BF16), (64, 4, BF16)]
+
+
+def many(c, new):
+    """The cache of one sequence under 320 block table rows, so that a warp has a
+    long stretch of tokens under one reference; each attends from `new` tokens."""
+    cache, B = c.filled(), 320
+    c.table, c.kv, c.new = np.repeat(c.table, B, 0), c.kv * B, [new] * B
+    c.K, c.V = c.K * B, c.V * B
+    c.cu = (new * np.arange(B + 1)).astype(np.int32)
+    c.n_tokens = new * B
+    c.q = np.tile(c.q, (B, 1, 1))
+    out = cache.attend(c.queries(), c.batch())
+    assert cache.device_status() == 0
+    return out, (0, 1, 77, 160, 318, 319)
+
+
+@pytest.mark.parametrize("d,bits,dtype", FORMATS)
+@pytest.mark.parametrize("new", (1, 4))
+@pytest.mark.parametrize("seen", (True, False))
+def test_one_saturated_group_among_normal_ones(d, bits, dtype, new, seen):
+    """One token has a group of values at the stored form's limit: the other
+    groups keep the precision of their own size and, where no query attends to
+    that token, so do the other tokens of its group."""
+    c = Case([700], [new], 4, 1, d, bits, 32, dtype, seed=bits)
+    c.V[0] = c._round(c.V[0] * np.float32(2.0 ** -6))
+    c.V[0][7, :, :32] = np.resize(np.array([np.inf, -32768, 5000], np.float32), 32)
+    if not seen:  # all queries share a direction, and this key looks away from it
+        base = np.where(c.rng.random(d) < 0.5, -1, 1).astype(np.float32)
+        c.q = c._round(base + np.float32(0.1) * c.q)
+        c.K[0] = c._round(np.float32(0.3) * c.rng.standard_normal(c.K[0].shape).astype(np.float32))
+        c.K[0][7] = -6 * base
+    out, only = many(c, new)
+    check_rows(c, out, by_group=True, only=only)
+
+
+@pytest.mark.parametrize("d,bits,dtype", FORMATS)
+@pytest.mark.parametrize("new", (1, 4))
+def test_a_long_tail_of_small_weights(d, bits, dtype, new):
+    """One token holds nearly all of the weight and has no value of its own; the
+    output is what 6000 others, each 2^-26.5 of it, add up to."""
+    c = Case([6000], [new], 4, 1, d, bits, 64, dtype)
+    base = np.where(c.rng.random(d) < 0.5, -1, 1).astype(np.float32)
+    c.q = np.broadcast_to(base, (new, 4, d)).copy()
+    c.K[0] = c._round(np.float32(0.01) * c.K[0])
+    c.K[0][0] = c._round(base * np.float32(26.5 * np.log(2) / d ** 0.5))
+    c.V[0] = c._round(1 + np.float32(0.3) * c.V[0])
+    c.V[0][0] = 0
+    out, only = many(c, new)
+    check_rows(c, out, only=only)
