@@ -8,10 +8,15 @@
 //   P_i = 2^(S_i F - ref)              one thread per row; fp16, back into tensor memory
 //   O_i (+)= P_i V                     tcgen05.mma, P from tensor memory
 // S, P and O stay in tensor memory (S and P share columns).  The reference of
-// a row is the maximum of earlier steps and moves only when a score passes it by
-// more than 8 (log2 units), so the weights need no pass over the scores for the
-// maximum first, and O is rescaled a few times per row at most, by the row's
-// own thread.
+// a row lies 5 (log2 units) below the maximum of earlier steps and moves only
+// when a score passes that by more than 8, so the weights need no pass over the
+// scores for the maximum first, and O is rescaled a few times per row at most, by
+// the row's own thread.  The 5 are fp16's room above 1: the largest weight is held
+// at 2^5 or more, so weights down to 2^-19 of it are normal fp16 numbers and
+// smaller ones keep an absolute 2^-30 of it (held at 1, weights of 2^-26.5 went to
+// zero, and with them the output of rows that thousands of those make up).  More
+// room costs moves: four times 512 over 8192 in 254, 258, 268 and 276 us at 3, 5,
+// 6 and 7.
 //
 // Bound: 4*128*256*d operations per step on the tensor core against 128*256
 // exponentials and the dequantization of 128 keys and values: eight producer
@@ -69,8 +74,9 @@ constexpr int kPieceSizes = 3;
 __host__ __device__ constexpr int piece_size(int k) { return k == 0 ? 6 : k == 1 ? 8 : 12; }
 constexpr int kMaxChunkBlocks = 160;
 constexpr int kChunkWait = 1 << 25;
-constexpr float kChunkSlack = 8.0f;  // log2 units a score may pass the reference by
-constexpr float kChunkTop = 15.0f;   // ... within a step: weights up to 2^15 fit fp16
+constexpr float kChunkBase = 5.0f;    // log2 of the weight a reference is set to give
+constexpr float kChunkSlack = 13.0f;  // ... above which it moves before the next step
+constexpr float kChunkTop = 15.0f;    // ... within a step: weights up to 2^15 fit fp16
 constexpr float kNoRef = -1e30f;
 
 struct ChunkArgs {
@@ -982,9 +988,9 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           }
         };
         // the reference moves where the last step's scores passed it by more
-        // than the slack
+        // than the slack, back to kChunkBase below them
         if (__any_sync(0xffffffffu, over > kChunkSlack)) {
-          const float by = over > kChunkSlack ? over : 0.0f;
+          const float by = over > kChunkSlack ? over - kChunkBase : 0.0f;
           rescale(exp2_approx(-by));
           ref += by;
         }
@@ -997,47 +1003,53 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
             if (k > seen || (b2 >> (k / 16) & 1)) y[k] = 0xff800000u;
         };
         float sum0 = 0.0f, sum1 = 0.0f;
-        // The usual step: nothing to hide and no weight beyond fp16.  Straight
-        // code without a branch, the weights kept in registers until the
-        // maximum is known; where they turn out too large the scores are still
-        // there for the careful loop below.
-        bool done = false;
-        if (!masked && j > j0) {
-          uint32_t w[64], x[2][16];
-          float m0 = -INFINITY, m1 = -INFINITY;
-          const uint64_t F2 = pair64(F, F), R2 = pair64(-ref, -ref);
-          uint64_t sa = 0, sb = 0;
-          tc_ld16(ts, x[0]);
+        // The usual step: nothing to hide.  Straight code without a branch, the
+        // weights kept in registers until the maximum is known.  Where fp16 could
+        // not hold one, or the row has no reference yet, that moves to
+        // kChunkBase below the maximum and the step is taken once more.
+        if (!masked) {
+          uint32_t w[64];
+          float top;
+#pragma unroll 1
+          for (int again = 0;; ++again) {
+            uint32_t x[2][16];
+            float m0 = -INFINITY, m1 = -INFINITY;
+            const uint64_t F2 = pair64(F, F), R2 = pair64(-ref, -ref);
+            uint64_t sa = 0, sb = 0;
+            tc_ld16(ts, x[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t (&y)[16] = x[c & 1];
-            tc_wait_ld();
-            if (c < 7) tc_ld16(ts + 16 * (c + 1), x[(c + 1) & 1]);
+            for (int c = 0; c < 8; ++c) {
+              uint32_t (&y)[16] = x[c & 1];
+              tc_wait_ld();
+              if (c < 7) tc_ld16(ts + 16 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              m0 = max3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-              m1 = max3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
-              const float2 a0 = unpair64(fma2(pair64u(y[k], y[k + 1]), F2, R2));
-              const float2 a1 = unpair64(fma2(pair64u(y[k + 2], y[k + 3]), F2, R2));
-              const float p0 = exp2_approx(a0.x), p1 = exp2_approx(a0.y);
-              const float p2 = exp2_approx(a1.x), p3 = exp2_approx(a1.y);
-              sa = add2(sa, pair64(p0, p1));
-              sb = add2(sb, pair64(p2, p3));
-              w[8 * c + k / 2] = h2u(__floats2half2_rn(p0, p1));
-              w[8 * c + k / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+              for (int k = 0; k < 16; k += 4) {
+                m0 = max3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+                m1 = max3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
+                const float2 a0 = unpair64(fma2(pair64u(y[k], y[k + 1]), F2, R2));
+                const float2 a1 = unpair64(fma2(pair64u(y[k + 2], y[k + 3]), F2, R2));
+                const float p0 = exp2_approx(a0.x), p1 = exp2_approx(a0.y);
+                const float p2 = exp2_approx(a1.x), p3 = exp2_approx(a1.y);
+                sa = add2(sa, pair64(p0, p1));
+                sb = add2(sb, pair64(p2, p3));
+                w[8 * c + k / 2] = h2u(__floats2half2_rn(p0, p1));
+                w[8 * c + k / 2 + 1] = h2u(__floats2half2_rn(p2, p3));
+              }
             }
-          }
-          const float top = fmaf(fmaxf(m0, m1), F, -ref);
-          done = !__any_sync(0xffffffffu, top > kChunkTop);
-          if (done) {
-            over = fmaxf(top, 0.0f);
+            const float m = fmaxf(m0, m1);
+            top = fmaf(m, F, -ref);
             const float2 s0 = unpair64(sa), s1 = unpair64(sb);
             sum0 = s0.x + s0.y, sum1 = s1.x + s1.y;
-            tc_st32(ts, w);
-            tc_st32(ts + 32, w + 32);
+            if (again || !__any_sync(0xffffffffu, top > kChunkTop)) break;
+            const bool first = ref == kNoRef, jump = top > kChunkTop;
+            const float by = jump && !first ? top - kChunkBase : 0.0f;
+            rescale(exp2_approx(-by));
+            if (jump) ref = first ? fmaf(m, F, -kChunkBase) : ref + by;
           }
-        }
-        if (!done) {
+          over = fmaxf(top, 0.0f);
+          tc_st32(ts, w);
+          tc_st32(ts + 32, w + 32);
+        } else {
         uint32_t x[2][32];
         tc_ld32(ts, x[0]);
         // (rolled: straight-line code for a whole row runs out of the
@@ -1061,10 +1073,10 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
             float top = fmaf(m, F, -ref);
             if (__any_sync(0xffffffffu, top > kChunkTop)) {
               // A weight that fp16 could not hold, or a row's first scores: the
-              // reference moves now, and with it the weights stored before (a
-              // power of two, so they stay exact).
+              // reference moves now, and with it the weights stored before (by a
+              // power of two: exact for those that stay normal).
               const bool first = ref == kNoRef, jump = top > kChunkTop;
-              const float by = jump && !first ? ceilf(top) : 0.0f;
+              const float by = jump && !first ? floorf(top) - kChunkBase : 0.0f;
               const float f = jump && first ? 0.0f : exp2_approx(-by);
               sum0 *= f, sum1 *= f;
               const uint32_t f2 = h2u(__float2half2_rn(f));
@@ -1081,7 +1093,7 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
               }
               rescale(f);
               if (jump) {
-                ref = first ? m * F : ref + by;
+                ref = first ? fmaf(m, F, -kChunkBase) : ref + by;
                 over = 0.0f;
               }
               top = fmaf(m, F, -ref);

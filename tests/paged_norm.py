@@ -18,11 +18,12 @@ A row's error, its norm over the channels, passes KAPPA = 6 deviations with a
 probability of e^-18 or so (bounded errors, sub-Gaussian).  To this come the
 output's own rounding (half a step of its type, element by element) and fp16's
 absolute step at the weights: one held below 2^-14 is off by up to 2^-25 instead
-of u relative.  A chunk's largest weight is held at 2^7 or more; of few rows,
-weight times value scale at 2^11 or more where both are the largest.  So a weight
-(or its product with its values' scale) below 2^-21 of the largest adds, for the
-row's largest weight, at most 2^-32 of the group's largest m, or 2^-36 of all
-groups' largest.
+of u relative.
+  Chunks hold the row's largest weight at 2^5 or more, so a weight below 2^-19 of
+  it adds at most 2^-30 of it times the group's largest m.
+  Few rows hold weight times value scale at 2^11 or more where both are the
+  largest, so a product below 2^-25 of that adds at most 2^-36 of the largest
+  weight times all groups' largest m.
 A row of zeros, or one 5 % too large, is outside wherever more than a few tokens
 share the weight.
 """
@@ -33,7 +34,6 @@ from paged_util import GROUP, quantize, values
 
 U = 2.0 ** -11
 KAPPA = 6.0
-SMALL, FLOOR, FLOOR_ALL = 2.0 ** -21, 2.0 ** -32, 2.0 ** -36
 
 
 def held(case, which, b, device):
@@ -43,11 +43,12 @@ def held(case, which, b, device):
     return torch.from_numpy(values(codes, s, z)).to(device).double(), wide(z), wide(s)
 
 
-def check_rows(case, out, scale=None, gone=None, by_group=False, only=None):
+def check_rows(case, out, scale=None, gone=None, by_group=False, only=None, chunks=True):
     """Asserts that every real row of `out` is within the bound; returns the
     largest fraction of it that was used.  gone[b]: positions of sequence b that
     are not there (a page that does not exist).  by_group: the norm and the bound
-    of each group of 32 channels by itself.  only: these sequences."""
+    of each group of 32 channels by itself.  only: these sequences.
+    chunks: whether some rows may be the chunk kernel's."""
     rg, d, dev = case.hq // case.hkv, case.d, out.device
     part = GROUP if by_group else d
     norm = lambda x: x.unflatten(-1, (-1, part)).norm(dim=-1)  # noqa: E731
@@ -90,9 +91,11 @@ def check_rows(case, out, scale=None, gone=None, by_group=False, only=None):
             absolute = []
             for c in range(0, d, GROUP):
                 size = C[:, h, c] / C[:, h].amax().clamp(min=1e-30)
-                small = ((w * size < SMALL * top) | (w < SMALL * top)) & ~hidden
-                big = FLOOR * m2[:, c:c + GROUP].amax().sqrt() + FLOOR_ALL * m2.amax().sqrt()
-                absolute.append(small.sum(-1) * top[..., 0] * big * GROUP ** 0.5)
+                few_small = ((w * size < 2.0 ** -25 * top) & ~hidden).sum(-1)
+                small = ((w < 2.0 ** -19 * top) & ~hidden).sum(-1) if chunks else 0
+                each = (2.0 ** -36 * few_small * m2.amax().sqrt()
+                        + 2.0 ** -30 * small * m2[:, c:c + GROUP].amax().sqrt())
+                absolute.append(each * top[..., 0] * GROUP ** 0.5)
             absolute = torch.stack(absolute, -1).unflatten(-1, (d // part, -1)).norm(dim=-1)
             bound = (KAPPA * var.unflatten(-1, (-1, part)).sum(-1).sqrt() + half_step * norm(o)
                      + absolute + 1e-7)
