@@ -72,9 +72,11 @@ cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads
 namespace {
 
 // ---- device helpers ------------------------------------------------------
-// The first error of a call stays in the status word until it is read.
+// The first error stays in the status word until it is read, but for a wait that
+// ran out: that one takes the word over, since the scratch has to be cleared.
 __device__ __forceinline__ void paged_error(const Paged &p, int code) {
-  atomicCAS(p.status, 0, code);
+  if (code == KVQ_ETIMEOUT) atomicExch(p.status, code);
+  else atomicCAS(p.status, 0, code);
 }
 
 // Whether sequence b's rows are none of the call's: out of order (their

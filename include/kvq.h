@@ -529,7 +529,8 @@ int kvq_paged_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cach
                         float softmax_scale, void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronizes `stream`, reads and clears the status word; KVQ_OK, or what a
- * kernel recorded there (KVQ_EPAGE, KVQ_EINVAL, KVQ_ETIMEOUT), or KVQ_ECUDA. */
+ * kernel recorded there, or KVQ_ECUDA.  Of several errors it holds the first
+ * (KVQ_EPAGE, KVQ_EINVAL), but KVQ_ETIMEOUT before either. */
 int kvq_paged_status(kvq_paged_cache *cache, void *stream);
 
 /* Number of kernel launches the last successful call of this thread enqueued. */

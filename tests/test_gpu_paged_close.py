@@ -124,3 +124,25 @@ def test_a_long_tail_of_small_weights(d, bits, dtype, new):
     c.V[0][0] = 0
     out, only = many(c, new)
     check_rows(c, out, only=only, chunks=new > 4)
+
+
+# ---- status and scratch -----------------------------------------------------
+
+@pytest.mark.parametrize("new", (1, 60))
+def test_a_timeout_is_not_hidden_by_an_earlier_error(new):
+    """After a wait that ran out the scratch has to be cleared: the status word
+    says so, whatever was recorded before."""
+    c = Case([700, 300], [new, new], 8, 2, 128, 4, 32, F16)
+    cache, batch, q = c.filled(), c.batch(), c.queries()
+    bad = c.batch(new=[700, 300])
+    bad.block_table[1, 2] = -1
+    cache.read(bad)  # records KVQ_EPAGE
+    try:
+        kvq.debug_stall_waits(1000)
+        cache.attend(q, batch)
+        torch.cuda.synchronize()
+    finally:
+        kvq.debug_stall_waits(0)
+    assert cache.device_status() == kvq.KVQ_ETIMEOUT
+    check_rows(c, cache.attend(q, batch))
+    assert cache.device_status() == 0
