@@ -555,6 +555,9 @@ class PagedKVCache:
                "kvq_paged_workspace_bytes")
         self.ws_bytes = n.value
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        if self.device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+            # zero before a call on any stream
+            torch.cuda.current_stream(self.device).synchronize()
         self._refs = ctypes.byref(cfg), ctypes.byref(self.view)
         L = lib()
         self._write, self._read, self._attend = (L.kvq_paged_write, L.kvq_paged_read,

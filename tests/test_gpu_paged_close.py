@@ -146,3 +146,23 @@ def test_a_timeout_is_not_hidden_by_an_earlier_error(new):
     assert cache.device_status() == kvq.KVQ_ETIMEOUT
     check_rows(c, cache.attend(q, batch))
     assert cache.device_status() == 0
+
+
+@pytest.mark.parametrize("new", (1, 60))
+def test_a_new_cache_is_ready_on_every_stream(new):
+    """The scratch of a cache made on a busy stream is zero before a call on
+    another one starts."""
+    c = Case([3000, 2500], [new, new], 8, 2, 128, 4, 64, F16)
+    old, batch, q = c.filled(), c.batch(), c.queries()
+    out = torch.full_like(q, 7.0)
+    side = torch.cuda.Stream()
+    dirty = torch.full((old.ws_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del dirty  # the allocator hands this block out again
+    torch.cuda._sleep(50_000_000)
+    cache = kvq.PagedKVCache(c.config(), pages=old.pages)
+    with torch.cuda.stream(side):
+        cache.attend(q, batch, out=out)
+    torch.cuda.synchronize()
+    check_rows(c, out)
+    assert cache.device_status() == 0
