@@ -518,7 +518,9 @@ class PagedBatch:
             raise ValueError("block_table, seq_lens and cu_tokens are on different devices")
         self.block_table, self.seq_lens, self.cu_tokens = block_table, seq_lens, cu_tokens
         self.n_tokens = int(n_tokens)
-        self.max_tokens = int(n_tokens if max_tokens is None else max_tokens)
+        # (int32 in the call: a larger bound is as good as the largest)
+        most = int(n_tokens if max_tokens is None else max_tokens)
+        self.max_tokens = max(-1, min(most, 2**31 - 1))
         self.device = block_table.device
         self.index = block_table.get_device()
         self.view = _PagedBatch(block_table.data_ptr(), seq_lens.data_ptr(),

@@ -186,3 +186,13 @@ def test_stride_of_a_single_row_does_not_matter(stride):
                            torch.tensor([0, 1], **i32), 1)
     k = torch.empty_strided((1, 2, 128), (stride, 128, 1), dtype=torch.float16)
     assert cache._rows(k, batch, 2) == 2 * 128
+
+
+@pytest.mark.parametrize("most,held", [(2**31 - 1, 2**31 - 1), (2**31, 2**31 - 1),
+                                       (2**32 + 1, 2**31 - 1), (2**40, 2**31 - 1), (-1, -1),
+                                       (-2**32 + 5, -1)])
+def test_bounds_beyond_32_bits_stay_bounds(most, held):
+    """max_tokens is an upper bound: one that the call's 32 bits cannot hold may
+    not come out as a smaller one."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    assert kvq.PagedBatch(i32(1, 4), i32(1), i32(2), 5, most).view.max_tokens == held
