@@ -5,18 +5,20 @@ and different for every token and channel, so the errors of one output row add
 up like independent ones.  With normalised weights w, values v, zero points z,
 output o = sum_t w_t v_t, the variance of channel c's error is at most
 
-    sum_t w_t^2 [ S_t (v_tc - o_c)^2 + u^2 m_tc^2 + u^2 v_tc^2 ]
+    sum_t w_t^2 [ S_t (v_tc - o_c)^2 + u^2 m_tc^2 + u^2 v_tc^2 + a^2 ]
 
-  S_t   variance of the score: u^2 scale^2 sum_c (q_c k_tc)^2 for the key operand,
-        as much again for the query's, and the fp32 sums, (2^-21 |scale| sum_c
-        |q_c k_tc|)^2
+  S_t   variance of the score: scale^2 sum_c q_c^2 (u^2 k_tc^2 + a^2) for the key
+        operand, u^2 scale^2 sum_c (q_c k_tc)^2 for the query's, and the fp32 sums,
+        (2^-21 |scale| sum_c |q_c k_tc|)^2
   m_tc  what the weight operand multiplies: v, or v - z where the zero points are
         summed apart; the larger
   v_tc  the value operand
+  a     half of fp16's smallest step, 2^-25: what rounding a subnormal may cost
 
 A row's error, its norm over the channels, passes KAPPA = 6 deviations with a
 probability of e^-18 or so (bounded errors, sub-Gaussian).  To this come the
-output's own rounding (half a step of its type, element by element) and fp16's
+output's own rounding (half a step of its type, element by element, never below
+half its smallest) and fp16's
 absolute step at the weights: one held below 2^-14 is off by up to 2^-25 instead
 of u relative.
   Chunks hold the row's largest weight at 2^5 or more, so a weight below 2^-19 of
@@ -34,6 +36,7 @@ from paged_util import GROUP, quantize, values
 
 U = 2.0 ** -11
 KAPPA = 6.0
+A = 2.0 ** -25
 
 
 def held(case, which, b, device):
@@ -54,6 +57,7 @@ def check_rows(case, out, scale=None, gone=None, by_group=False, only=None, chun
     norm = lambda x: x.unflatten(-1, (-1, part)).norm(dim=-1)  # noqa: E731
     scale = d ** -0.5 if scale is None else scale
     half_step = torch.finfo(case.dtype).eps / 2
+    tiny = half_step * torch.finfo(case.dtype).tiny + 1e-12
     assert torch.isfinite(out[:int(case.cu[-1])].float()).all()
     worst = 0.0
     for b, n in enumerate(case.new):
@@ -81,11 +85,11 @@ def check_rows(case, out, scale=None, gone=None, by_group=False, only=None, chun
             total = w.sum(-1, keepdim=True)
             w = w / torch.where(total > 0, total, 1.0)
             o = w @ v
-            S = scale ** 2 * (2 * U * U * ((q[h] ** 2) @ (k ** 2).T)
+            S = scale ** 2 * ((q[h] ** 2) @ (2 * U * U * k ** 2 + A * A).T
                               + (2.0 ** -21 * (q[h].abs() @ k.abs().T)) ** 2)
             a = w * w * S
             var = (a @ (v * v) - 2 * o * (a @ v) + o * o * a.sum(-1, keepdim=True)).clamp(min=0)
-            var = var + U * U * ((w * w) @ (m2 + v * v))
+            var = var + U * U * ((w * w) @ (m2 + v * v + (A / U) ** 2))
             # the weights that may be below fp16's normal range, group by group
             top = w.amax(-1, keepdim=True)
             absolute = []
@@ -98,7 +102,7 @@ def check_rows(case, out, scale=None, gone=None, by_group=False, only=None, chun
                 absolute.append(each * top[..., 0] * GROUP ** 0.5)
             absolute = torch.stack(absolute, -1).unflatten(-1, (d // part, -1)).norm(dim=-1)
             bound = (KAPPA * var.unflatten(-1, (-1, part)).sum(-1).sqrt() + half_step * norm(o)
-                     + absolute + 1e-7)
+                     + tiny * part ** 0.5 + absolute)
             use = float((norm(got[h] - o) / bound).max())
             assert use <= 1.0, "sequence %d head %d: %.2f of the bound" % (b, h, use)
             worst = max(worst, use)
