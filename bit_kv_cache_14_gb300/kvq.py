@@ -591,6 +591,16 @@ class PagedKVCache:
         # a single row's stride is never used and may be anything
         return s0 if batch.n_tokens > 1 else heads * d
 
+    def _output_on(self, stream, shape) -> torch.Tensor:
+        """A tensor for a call on another stream than the current one to fill.  It
+        comes from that stream's memory (a block that the current stream has yet to
+        finish with may not be written there) and is kept from reuse until the
+        current stream, which is likely to read it, is done."""
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=self.dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
     def _call(self, fn, batch: PagedBatch, stream, *args) -> None:
         if batch.index != self._index:
             raise ValueError("the batch is on %s, the cache on %s" % (batch.device, self.device))
@@ -614,17 +624,18 @@ class PagedKVCache:
         """Reads the batch's tokens back: (k, v), each contiguous
         [n_tokens][n_kv_heads][head_dim] (``out``: the two tensors to fill)."""
         if out is None:
-            k = torch.empty((batch.n_tokens,) + self._kv_row, dtype=self.dtype,
-                            device=self.device)
-            v = torch.empty_like(k)
+            shape = (batch.n_tokens,) + self._kv_row
+            if stream is None:
+                k = torch.empty(shape, dtype=self.dtype, device=self.device)
+                v = torch.empty_like(k)
+            else:
+                k, v = self._output_on(stream, shape), self._output_on(stream, shape)
         else:
             k, v = out
             for t in out:
                 self._rows(t, batch, self.cfg.n_kv_heads)
                 _ptr(t)
         self._call(self._read, batch, stream, k.data_ptr(), v.data_ptr())
-        if stream is not None and out is None:
-            k.record_stream(stream), v.record_stream(stream)
         return k, v
 
     def attend(self, q: torch.Tensor, batch: PagedBatch, out: torch.Tensor | None = None,
@@ -633,17 +644,16 @@ class PagedKVCache:
         the batch's newest tokens, over everything their sequences hold (write
         those tokens first).  Returns [n_tokens][n_q_heads][head_dim]."""
         qs = self._rows(q, batch, self.cfg.n_q_heads)
-        given = out is not None
-        if given:
+        if out is not None:
             self._rows(out, batch, self.cfg.n_q_heads)
             _ptr(out)
-        else:
+        elif stream is None:
             out = torch.empty((batch.n_tokens,) + self._q_row, dtype=self.dtype,
                               device=self.device)
+        else:
+            out = self._output_on(stream, (batch.n_tokens,) + self._q_row)
         self._call(self._attend, batch, stream, q.data_ptr(), qs, out.data_ptr(),
                    self._scale if scale is None else scale, self._ws_ptr, self.ws_bytes)
-        if stream is not None and not given:
-            out.record_stream(stream)
         return out
 
     def device_status(self, stream=None) -> int:

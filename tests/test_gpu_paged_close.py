@@ -359,6 +359,28 @@ def test_a_call_waits_for_its_stream(new):
     check_rows(c, out)
 
 
+@pytest.mark.parametrize("what", ("read", "attend"))
+def test_an_output_on_another_stream_takes_no_memory_still_in_use(what):
+    """A freed tensor that the current stream has yet to read keeps its contents
+    while a call given another stream makes its own output."""
+    c = Case([1500], [1500], 8, 8, 128, 4, 32, F16)
+    cache, batch, q = c.filled(), c.batch(), c.queries()
+    side = torch.cuda.Stream()
+    old = torch.full_like(q, 3.0)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    copy = old.clone()              # runs after the sleep
+    del old
+    out = cache.attend(q, batch, stream=side) if what == "attend" else \
+        cache.read(batch, stream=side)[0]
+    torch.cuda.synchronize()
+    assert (copy == 3).all()
+    if what == "attend":
+        check_rows(c, out)
+    else:
+        assert torch.equal(out.cpu(), c.expected_rows("k", c.rows))
+
+
 @pytest.mark.parametrize("new", (1, 40))
 def test_pages_beyond_32_bit_offsets(new):
     c = Case([600], [new], 4, 2, 128, 4, 256, F16)
