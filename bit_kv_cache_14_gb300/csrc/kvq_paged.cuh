@@ -11,6 +11,7 @@ constexpr int kAtom = 16;         // tokens stored together inside a page
 constexpr int kPagedGroup = 32;   // channels that share a scale and a zero point
 constexpr int kMaxSeqs = 2048;  // (running sums over the sequences fit shared memory)
 constexpr float kPagedLimit = 32768.0f;  // stored magnitudes saturate here
+constexpr float kMostScale = 3.4028235e38f;  // factors of the scores stay finite: 0 times one is 0
 
 // One paged call, resolved on the host and copied by value into every kernel.
 struct Paged {

@@ -926,7 +926,9 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
                      "r"(o4[2]), "r"(o4[3])
                      : "memory");
         // (never 0: a hidden column's -inf stays -inf)
-        if (ql == 0) fs[rr] = fmaxf(a.scale_log2 * __int_as_float((127 + ex - 8) << 23), 1e-30f);
+        if (ql == 0)
+          fs[rr] = fminf(fmaxf(a.scale_log2 * __int_as_float((127 + ex - 8) << 23), 1e-30f),
+                         kMostScale);
       }
     };
     auto queries_in = [&]() {
@@ -1303,7 +1305,7 @@ cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *
   a.q = static_cast<const uint16_t *>(q);
   a.qs = qs;
   a.out = static_cast<uint16_t *>(out);
-  a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+  a.scale_log2 = fminf(fabsf(scale) * 1.4426950408889634f, kMostScale);
   a.sign = scale < 0.0f ? -1.0f : 1.0f;
   a.few = few;
   uint8_t *w = static_cast<uint8_t *>(ws);

@@ -502,7 +502,8 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
         qsum[nt] = j == 0 ? hi : j == 1 ? lo : 0u;
       }
       // per-row factors move to the lanes that hold the row's scores
-      const float mine = a.scale_log2 * __int_as_float((127 + 24 + ex - 8) << 23);
+      const float mine = fmaxf(
+          fminf(a.scale_log2 * __int_as_float((127 + 24 + ex - 8) << 23), kMostScale), -kMostScale);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int rr = 8 * nt + 2 * j + s;
@@ -950,7 +951,7 @@ cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *o
   a.q = static_cast<const uint16_t *>(q);
   a.qs = qs;
   a.out = static_cast<uint16_t *>(out);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = fmaxf(fminf(scale * 1.4426950408889634f, kMostScale), -kMostScale);
   uint8_t *w = static_cast<uint8_t *>(ws);
   a.ws_count = reinterpret_cast<int *>(w);
   a.ws_ml = reinterpret_cast<float *>(w + kPagedRowBlocks * 4);

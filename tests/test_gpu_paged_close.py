@@ -261,6 +261,31 @@ def test_scores_that_rise_step_by_step(new):
     go(c)
 
 
+@pytest.mark.parametrize("scale", (3e38, -3e38, 1e30))
+@pytest.mark.parametrize("new", (1, 4, 60))
+def test_queries_of_zero_at_any_scale(scale, new):
+    """Every score is 0, whatever it is multiplied by: the mean of the values."""
+    c = Case([200], [new], 8, 2, 128, 4, 32, BF16)
+    c.q[:] = 0
+    go(c, scale)
+
+
+@pytest.mark.parametrize("new", (2, 4, 60))
+@pytest.mark.parametrize("bad", (float("nan"), float("inf")))
+def test_queries_that_are_no_numbers_stay_alone(new, bad):
+    """A row and head with a NaN or an infinity has no output; all others do."""
+    c = Case([500, 300], [new, new], 8, 2, 128, 4, 32, F16)
+    cache, q = c.filled(), c.queries()
+    rows, heads = [0, new - 1, new, 2 * new - 1], [0, 5, 3, 7]
+    good = cache.attend(q, c.batch())
+    q[rows, heads, 17] = bad
+    out = cache.attend(q, c.batch())
+    assert out[rows, heads].isnan().all()
+    out[rows, heads] = good[rows, heads]
+    check_rows(c, out)
+    assert cache.device_status() == 0
+
+
 # ---- pages, replays, streams ------------------------------------------------
 
 @pytest.mark.parametrize("new", (2, 50))
