@@ -8,15 +8,15 @@
 //   P_i = 2^(S_i F - ref)              one thread per row; fp16, back into tensor memory
 //   O_i (+)= P_i V                     tcgen05.mma, P from tensor memory
 // S, P and O stay in tensor memory (S and P share columns).  The reference of
-// a row lies 5 (log2 units) below the maximum of earlier steps and moves only
-// when a score passes that by more than 8, so the weights need no pass over the
+// a row lies 4 (log2 units) below the maximum of earlier steps and moves only
+// when a score passes that by more than 9, so the weights need no pass over the
 // scores for the maximum first, and O is rescaled a few times per row at most, by
-// the row's own thread.  The 5 are fp16's room above 1: the largest weight is held
-// at 2^5 or more, so weights down to 2^-19 of it are normal fp16 numbers and
-// smaller ones keep an absolute 2^-30 of it (held at 1, weights of 2^-26.5 went to
+// the row's own thread.  The 4 are fp16's room above 1: the largest weight is held
+// at 2^4 or more, so weights down to 2^-18 of it are normal fp16 numbers and
+// smaller ones keep an absolute 2^-29 of it (held at 1, weights of 2^-26.5 went to
 // zero, and with them the output of rows that thousands of those make up).  More
-// room costs moves: four times 512 over 8192 in 254, 258, 268 and 276 us at 3, 5,
-// 6 and 7.
+// room costs moves: 4096 tokens over 32768 at 2 bits in 1502, 1549, 1585 and 1611
+// us at 0, 3, 4 and 5; at 4 bits 1410, 1419, 1425 and 1437.
 //
 // Bound: 4*128*256*d operations per step on the tensor core against 128*256
 // exponentials and the dequantization of 128 keys and values: eight producer
@@ -74,7 +74,7 @@ constexpr int kPieceSizes = 3;
 __host__ __device__ constexpr int piece_size(int k) { return k == 0 ? 6 : k == 1 ? 8 : 12; }
 constexpr int kMaxChunkBlocks = 160;
 constexpr int kChunkWait = 1 << 25;
-constexpr float kChunkBase = 5.0f;    // log2 of the weight a reference is set to give
+constexpr float kChunkBase = 4.0f;    // log2 of the weight a reference is set to give
 constexpr float kChunkSlack = 13.0f;  // ... above which it moves before the next step
 constexpr float kChunkTop = 15.0f;    // ... within a step: weights up to 2^15 fit fp16
 constexpr float kNoRef = -1e30f;

@@ -21,8 +21,8 @@ output's own rounding (half a step of its type, element by element, never below
 half its smallest) and fp16's
 absolute step at the weights: one held below 2^-14 is off by up to 2^-25 instead
 of u relative.
-  Chunks hold the row's largest weight at 2^5 or more, so a weight below 2^-19 of
-  it adds at most 2^-30 of it times the group's largest m.
+  Chunks hold the row's largest weight at 2^4 or more, so a weight below 2^-18 of
+  it adds at most 2^-29 of it times the group's largest m.
   Few rows hold weight times value scale at 2^11 or more where both are the
   largest, so a product below 2^-25 of that adds at most 2^-36 of the largest
   weight times all groups' largest m.
@@ -96,9 +96,9 @@ def check_rows(case, out, scale=None, gone=None, by_group=False, only=None, chun
             for c in range(0, d, GROUP):
                 size = C[:, h, c] / C[:, h].amax().clamp(min=1e-30)
                 few_small = ((w * size < 2.0 ** -25 * top) & ~hidden).sum(-1)
-                small = ((w < 2.0 ** -19 * top) & ~hidden).sum(-1) if chunks else 0
+                small = ((w < 2.0 ** -18 * top) & ~hidden).sum(-1) if chunks else 0
                 each = (2.0 ** -36 * few_small * m2.amax().sqrt()
-                        + 2.0 ** -30 * small * m2[:, c:c + GROUP].amax().sqrt())
+                        + 2.0 ** -29 * small * m2[:, c:c + GROUP].amax().sqrt())
                 absolute.append(each * top[..., 0] * GROUP ** 0.5)
             absolute = torch.stack(absolute, -1).unflatten(-1, (d // part, -1)).norm(dim=-1)
             bound = (KAPPA * var.unflatten(-1, (-1, part)).sum(-1).sqrt() + half_step * norm(o)
