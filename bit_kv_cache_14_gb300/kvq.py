@@ -586,9 +586,9 @@ class PagedKVCache:
         if t.get_device() != self._index:
             self._on_device(t)
         s0, s1, s2 = t.stride()
-        if s2 != 1 or (heads > 1 and s1 != d):
+        if batch.n_tokens > 0 and (s2 != 1 or (heads > 1 and s1 != d)):
             raise ValueError("each row must be contiguous (got strides %s)" % (t.stride(),))
-        # a single row's stride is never used and may be anything
+        # a single row's stride is never used and may be anything, and no row has none
         return s0 if batch.n_tokens > 1 else heads * d
 
     def _output_on(self, stream, shape) -> torch.Tensor:

@@ -196,3 +196,14 @@ def test_bounds_beyond_32_bits_stay_bounds(most, held):
     not come out as a smaller one."""
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
     assert kvq.PagedBatch(i32(1, 4), i32(1), i32(2), 5, most).view.max_tokens == held
+
+
+def test_strides_of_no_rows_do_not_matter():
+    cache = kvq.PagedKVCache(_cfg(), device="cpu")
+    i32 = dict(dtype=torch.int32)
+    batch = kvq.PagedBatch(torch.zeros(1, 4, **i32), torch.ones(1, **i32),
+                           torch.zeros(2, **i32), 0)
+    none = torch.from_numpy(np.zeros((0, 2, 128), np.float16)).as_strided((0, 2, 128), (0, 0, 0))
+    assert cache._rows(none, batch, 2) == 2 * 128
+    with pytest.raises(ValueError):
+        cache._rows(none[:, :1], batch, 2)
