@@ -5,8 +5,8 @@
 // Up to 16 rows the cache's bytes bound the time and the split kernel
 // (kvq_paged_rows.cu) reads them once, at 8 or 16 rows an MMA tile; from there
 // on the tcgen05 kernel (kvq_paged_chunk.cu) takes the sequence (32 sequences of
-// 8192 tokens, 4 new ones of 4 heads each, 4 bits: 127 us split, 233 us tcgen05;
-// 8 new ones: 235 us there).  Lengths are on the device, so a call whose
+// 8192 tokens, 4 new ones of 4 heads each, 4 bits: 128 us split, 223 us tcgen05;
+// 8 new ones: 226 us there).  Lengths are on the device, so a call whose
 // max_tokens allows both launches both, and each kernel passes over the other's
 // sequences.
 #include "kvq_paged.cuh"

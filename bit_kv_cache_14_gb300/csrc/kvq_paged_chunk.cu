@@ -24,9 +24,10 @@
 // into fp16 (1024 + code by one LOP3, the code by one HFMA2, code * scale +
 // zero by a second: exact but for one rounding) and store the swizzled operand
 // tiles, which both query tiles use.  Measured on a GB300, 32 query and 8 KV heads
-// of 128, 4 bits: 4096 tokens over 32768, 1454 us = 1418 TFLOP/s, 74 % of the
-// measured matrix rate (1563 us back to back for seconds, at a lower clock); four
-// times 512 over 8192, 259 us = 1027 TFLOP/s; 64 tokens alone, 22 us.
+// of 128, 4 bits: 4096 tokens over 32768, 1424 us = 1448 TFLOP/s, 76 % of the
+// measured matrix rate (1510 us back to back for seconds, at a lower clock; 1583
+// at 2 bits, 1644 at 8, 1253 with heads of 64); four times 512 over 8192, 253 us =
+// 1050 TFLOP/s; 64 tokens alone, 22 us.
 //
 // What made the difference: no role may spill (a spilled MMA thread needed 200
 // clocks an instruction instead of 64), role code has to be small or rolled (five
@@ -42,8 +43,8 @@
 // steps.  Where all tiles in pieces of about 6, 8 or 12 steps (the smallest that
 // does) give no more pieces than there are blocks, each block takes a piece; a
 // longer list, kOver units added to each tile for its start and end, is cut into
-// equal ranges, one per block.  A tile that several blocks share leaves partials, joined in block
-// order by the block that finishes last.
+// equal ranges, one per block.  A tile that several blocks share leaves partials,
+// joined in block order by the block that finishes last.
 #include "kvq_paged.cuh"
 #include "kvq_tc_common.cuh"
 

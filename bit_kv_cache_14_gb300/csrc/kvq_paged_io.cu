@@ -3,8 +3,9 @@
 // Both move bytes: per token and head a write reads 4*d bytes and stores
 // d*b/4 + d/4, a read the reverse; a handful of operations per element, so
 // HBM should bound them.  Measured on a GB300, 32768 tokens of 8 heads of 128 at 4
-// bits (176 MB): write 53 us = 3.3 TB/s, 49 % of the copy rate, bound by its
-// instructions; read 33 us = 5.3 TB/s, 78 %; 48930 tokens at 8 bits, 50 us = 93 %.
+// bits (176 MB): write 53 us = 3.3 TB/s, 49 % of the copy rate, with 3 of 4
+// instructions issued a clock (54 us at 2 bits, 49 at 8); read 33 us = 5.3 TB/s,
+// 78 % (29 us, 81 %, at 2 bits, 34 at 8); 48930 tokens at 8 bits, 50 us = 93 %.
 #include "kvq_paged.cuh"
 
 namespace kvq {
@@ -90,8 +91,8 @@ __device__ __forceinline__ float careful_code(float x, float zero, float scale) 
 // lane l its channels 8*l .. 8*l + 7 (w): group l / 4, quarter j = l % 4 of the
 // key layout, eighths 2*j and 2*j + 1 of the value layout.
 //
-// What bounds it is the instructions per element (about 14 lane operations at
-// the rate HBM delivers), so: minima and maxima on packed pairs; one reciprocal
+// What bounds it is the instructions per element (22 lane operations, where HBM
+// would leave time for about 14), so: minima and maxima on packed pairs; one reciprocal
 // per group; rint by adding 1.5 * 2^23 in the fma that forms the quotient; codes
 // put together as integer sums.  The hardware reciprocal is within 2^-23 of
 // 1 / scale and the IEEE quotient within 2^-24 of the true one, so for quotients

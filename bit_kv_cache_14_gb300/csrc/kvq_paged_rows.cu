@@ -6,9 +6,9 @@
 // head against 4*d operations per row, so HBM, if the instructions per code stay
 // few enough (at 4 bits about 3.4 lane instructions per element keep up).
 // Measured on a GB300: 64 sequences of 5500 to 16384 tokens, 32 query and 8 KV
-// heads of 128, 4 bits: 199 us = 4.49 TB/s, 66 % of the copy rate; 8 bits, 16
-// sequences of 8192: 62 us = 4.9 TB/s; 2 bits, 32 heads of their own, 8 x 4096:
-// 47 us = 2.1 TB/s (instructions, and 11 us of fixed cost).
+// heads of 128, 4 bits: 200 us = 4.47 TB/s, 66 % of the copy rate; 8 bits, 16
+// sequences of 8192: 64 us = 4.7 TB/s; 2 bits, 32 heads of their own, 8 x 4096:
+// 48 us = 2.1 TB/s (twice the instructions a byte, and 11 us of fixed cost).
 //
 //  * Split: the tiles (two 16-token atoms, one at 8 bits) of all (sequence,
 //    head) pairs form one list, cut into equal contiguous ranges, one per block;
@@ -31,8 +31,10 @@
 //    movmatrix turns the score fragment into it.  Zero points: sum p * zero in
 //    fp32.
 //    (Measured without the 17 products per atom: 139 us where the whole takes
-//    199 and the copies alone 137, so they and the issue slots around them are
-//    what HBM waits for.)
+//    199 and the copies alone 137.  No pipe is full meanwhile (2.2 of 4
+//    instructions a clock, ALU 48 %, tensor 19 %): a tile is one chain of scores,
+//    vote, exponentials, turns and products, and three warps a scheduler do not
+//    cover its waits.)
 //  * Softmax: a lazy reference per row, moved only when a score passes it by
 //    more than 2 (log2 units), decided by one vote.  The reference also carries
 //    E, the exponent of the largest value scale seen, and lies kRoom = 12 below,

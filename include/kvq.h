@@ -513,14 +513,27 @@ int kvq_paged_read(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
  *   q: device, row t of query head h at q + t*q_stride + h*head_dim
  *   out [n_tokens][n_q_heads][head_dim], contiguous, dtype, apart from q:
  *     softmax(softmax_scale * q.K^T) V; zeros for a row that sees nothing.
- *   softmax_scale: any finite number.
+ *   softmax_scale: any finite number.  A score (times log2 e) of 2^23 or more in
+ *     magnitude, or a bf16 query beyond 2^90, may make its row NaN: fp32 no longer
+ *     tells such scores apart.  A query with a NaN or an infinity makes its own
+ *     row and head NaN and no other.
  *   ws: device scratch, ws_bytes >= kvq_paged_workspace_bytes.
  * Arithmetic: scores, weights' sums and outputs are held in fp32; the operands
- * of the two products are rounded to fp16: the query (relative to the largest
- * of its row), the weights, and for sequences of more than 16 query rows per KV
- * head, a row being one token and query head, the values x_hat.  Measured, the
- * output is off by 2.5e-4 (few rows) or 4e-4 to 8e-4 (chunks) of its size, where
- * its own rounding to fp16 is 2e-4 and to bf16 1.7e-3.
+ * of the two products are rounded to fp16.  A sequence's rows are its tokens in
+ * the call times r, the query heads of a KV head.  Few rows are at most 8, or at
+ * most 16 where r > 8 or max_tokens * r <= 16 (so the rounding of a sequence with
+ * 9 to 16 rows depends on max_tokens).  With few rows the rounded operands are the
+ * query (relative to the largest of its row) and each weight times its value's
+ * scale, with more the query, the weights and the keys and values x_hat.
+ * fp16's range costs what is small beside something large: of few rows a weight
+ * times scale below 2^-25 of the largest such product is off by up to 2^-36 of
+ * it; of more rows a weight below 2^-18 of the row's largest by up to 2^-29 of
+ * it, and an x_hat below 2^-14 by up to 2^-25.
+ * Measured for normal keys with a few channels 8 times larger, 2, 4 and 8 bits,
+ * both head sizes, fp16 (norm of the error over the norm of the output): few rows
+ * 2.4e-4 to 3.0e-4, more rows 3.8e-4 to 1.2e-3, of which the output's own rounding
+ * is 2.1e-4; single rows of the latter up to 6.6e-3.  For bf16 that rounding alone
+ * is 1.7e-3.
  * Errors: as kvq_paged_write; KVQ_EINVAL also where q and out overlap;
  *   KVQ_ECAPACITY (ws too small).
  */
