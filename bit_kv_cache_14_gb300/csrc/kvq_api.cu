@@ -520,7 +520,7 @@ const char *kvq_strerror(int code) {
     case KVQ_OK: return "ok";
     case KVQ_EINVAL: return "invalid argument";
     case KVQ_EUNSUPPORTED: return "unsupported configuration";
-    case KVQ_ECAPACITY: return "capacity exceeded (max_ctx or workspace)";
+    case KVQ_ECAPACITY: return "capacity exceeded (max_ctx, pages or workspace)";
     case KVQ_EALIGN: return "device buffer not 16-byte aligned";
     case KVQ_ECUDA: return "CUDA error";
     case KVQ_ETIMEOUT: return "device-side wait timed out";

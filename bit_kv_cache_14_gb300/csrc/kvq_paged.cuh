@@ -27,6 +27,7 @@ struct Paged {
   int64_t width;      // block table entries per sequence
   int B;
   int max_tokens;
+  int cross;          // attention: every row sees all of its sequence's tokens
   int64_t T;          // rows of the packed arrays
 };
 
@@ -41,6 +42,8 @@ int resolve_paged(const kvq_paged_config *cfg, Paged *p);
 cudaError_t launch_paged_write(const Paged &p, const void *k, int64_t ks, const void *v,
                                int64_t vs, cudaStream_t st);
 cudaError_t launch_paged_read(const Paged &p, void *k, void *v, cudaStream_t st);
+cudaError_t launch_paged_copy(const Paged &p, const int32_t *copies, int64_t n, int num_sms,
+                              cudaStream_t st);
 cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, void *out,
                                    float scale, void *ws, cudaStream_t st, int *launches);
 size_t paged_workspace_bytes();
@@ -55,10 +58,10 @@ int num_sms_cached();
 // Launch with or without leave to start while the previous kernel on the stream
 // ends (programmatic dependent launch; the kernel waits itself where it has to).
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned threads, int smem,
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, int smem,
                              cudaStream_t st, bool early, A &&...args) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(grid);
+  c.gridDim = grid;
   c.blockDim = dim3(threads);
   c.dynamicSmemBytes = (size_t)smem;
   c.stream = st;
@@ -90,6 +93,12 @@ __device__ __forceinline__ bool bad_rows(const Paged &p, int b) {
 // Position of row t of sequence b (negative: the row precedes its sequence).
 __device__ __forceinline__ int64_t row_position(const Paged &p, int b, int64_t t) {
   return (int64_t)p.lens[b] - p.cu[b + 1] + t;
+}
+
+// Newest position the first of sequence b's `tokens` rows sees; a later row i sees
+// i more, up to the last there is.
+__device__ __forceinline__ int64_t first_seen(const Paged &p, int b, int tokens) {
+  return (int64_t)p.lens[b] - (p.cross ? 1 : tokens);
 }
 
 // Address of the atom that holds position `pos` (>= 0) of sequence b and head

@@ -88,6 +88,29 @@ static int done(cudaError_t e, int launches) {
   return KVQ_OK;
 }
 
+static int attention(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
+                     const kvq_paged_batch *batch, int cross, const void *q, int64_t q_stride,
+                     void *out, float softmax_scale, void *ws, size_t ws_bytes, void *stream) {
+  Paged p;
+  int r = resolve_call(cfg, cache, batch, &p);
+  if (r != KVQ_OK) return r;
+  p.cross = cross;
+  if (!(softmax_scale == softmax_scale) || softmax_scale - softmax_scale != 0.0f)
+    return KVQ_EINVAL;
+  if (!ws) return KVQ_EINVAL;
+  if (!aligned(ws, 16)) return KVQ_EALIGN;
+  if (ws_bytes < paged_workspace_bytes()) return KVQ_ECAPACITY;
+  if (p.T == 0) return done(cudaSuccess, 0);
+  if ((r = check_rows(p, q, q_stride, p.Hq)) != KVQ_OK) return r;
+  const int64_t stride = (int64_t)p.Hq * p.d;
+  if ((r = check_rows(p, out, stride, p.Hq)) != KVQ_OK) return r;
+  if (overlap(p, q, q_stride, out, stride, p.Hq)) return KVQ_EINVAL;
+  int n = 0;
+  const cudaError_t e = launch_paged_attention(p, q, q_stride, out, softmax_scale, ws,
+                                               static_cast<cudaStream_t>(stream), &n);
+  return done(e, n);
+}
+
 }  // namespace kvq
 
 using namespace kvq;
@@ -138,32 +161,45 @@ int kvq_paged_read(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
   return done(launch_paged_read(p, k_out, v_out, static_cast<cudaStream_t>(stream)), 1);
 }
 
+int kvq_paged_copy(const kvq_paged_config *cfg, kvq_paged_cache *cache, const int32_t *copies,
+                   int64_t n_copies, void *stream) {
+  Paged p;
+  const int r = resolve_paged(cfg, &p);
+  if (r != KVQ_OK) return r;
+  if (!cache || !cache->pages || !cache->dev_status || n_copies < 0) return KVQ_EINVAL;
+  if (!aligned(cache->pages, 16) || !aligned(cache->dev_status, 4)) return KVQ_EALIGN;
+  if (n_copies == 0) return done(cudaSuccess, 0);
+  if (!copies) return KVQ_EINVAL;
+  if (!aligned(copies, 8)) return KVQ_EALIGN;
+  if (n_copies > (1LL << 31)) return KVQ_EUNSUPPORTED;
+  p.pages = static_cast<uint8_t *>(cache->pages);
+  p.status = cache->dev_status;
+  return done(launch_paged_copy(p, copies, n_copies, num_sms_cached(),
+                                static_cast<cudaStream_t>(stream)),
+              1);
+}
+
 int kvq_paged_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
                         const kvq_paged_batch *batch, const void *q, int64_t q_stride, void *out,
                         float softmax_scale, void *ws, size_t ws_bytes, void *stream) {
-  Paged p;
-  int r = resolve_call(cfg, cache, batch, &p);
-  if (r != KVQ_OK) return r;
-  if (!(softmax_scale == softmax_scale) || softmax_scale - softmax_scale != 0.0f)
-    return KVQ_EINVAL;
-  if (!ws) return KVQ_EINVAL;
-  if (!aligned(ws, 16)) return KVQ_EALIGN;
-  if (ws_bytes < paged_workspace_bytes()) return KVQ_ECAPACITY;
-  if (p.T == 0) return done(cudaSuccess, 0);
-  if ((r = check_rows(p, q, q_stride, p.Hq)) != KVQ_OK) return r;
-  const int64_t stride = (int64_t)p.Hq * p.d;
-  if ((r = check_rows(p, out, stride, p.Hq)) != KVQ_OK) return r;
-  if (overlap(p, q, q_stride, out, stride, p.Hq)) return KVQ_EINVAL;
-  int n = 0;
-  const cudaError_t e = launch_paged_attention(p, q, q_stride, out, softmax_scale, ws,
-                                               static_cast<cudaStream_t>(stream), &n);
-  return done(e, n);
+  return attention(cfg, cache, batch, 0, q, q_stride, out, softmax_scale, ws, ws_bytes, stream);
+}
+
+int kvq_paged_cross_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
+                              const kvq_paged_batch *batch, const void *q, int64_t q_stride,
+                              void *out, float softmax_scale, void *ws, size_t ws_bytes,
+                              void *stream) {
+  return attention(cfg, cache, batch, 1, q, q_stride, out, softmax_scale, ws, ws_bytes, stream);
 }
 
 int kvq_paged_status(kvq_paged_cache *cache, void *stream) {
-  if (!cache || !cache->dev_status) return KVQ_EINVAL;
+  return cache ? kvq_read_status(cache->dev_status, stream) : KVQ_EINVAL;
+}
+
+int kvq_read_status(int32_t *dev_status, void *stream) {
+  if (!dev_status) return KVQ_EINVAL;
   kvq_cache c = {};
-  c.dev_status = cache->dev_status;
+  c.dev_status = dev_status;
   return kvq_get_device_status(&c, stream);
 }
 

@@ -274,7 +274,7 @@ __device__ __forceinline__ Seq seq_of(const ChunkArgs &a, int b) {
   s.tokens = (int)((unsigned)p.cu[b + 1] - (unsigned)s.row0);
   const int64_t cap = p.width * p.page;
   s.len = (int)min((int64_t)max(p.lens[b], 0), cap);
-  s.pos0 = (int64_t)p.lens[b] - s.tokens;
+  s.pos0 = first_seen(p, b, s.tokens);
   const int64_t rows = (int64_t)s.tokens * p.rg;
   s.rows = !bad_rows(p, b) && rows > a.few ? (int)rows : 0;
   return s;
@@ -296,7 +296,7 @@ struct __align__(16) Item {
   int j0, j1;           // steps [j0, j1) of the tile
   int row0, row_first;  // the sequence's first packed row; the tile's first row in it
   int rows, len;        // rows and visible length of the sequence
-  int64_t pos0;         // position of the sequence's first row
+  int64_t pos0;         // newest position the sequence's first row sees
   int steps;            // of the whole tile
   int c0, c1;           // first and last block with a share
   int pad[3];

@@ -343,6 +343,41 @@ paged_read_kernel(const __grid_constant__ Paged p, uint16_t *k, uint16_t *v) {
   }
 }
 
+// A warp copies 4 KB of a page at a time, its lanes eight 16-byte vectors each, and
+// reads the next piece's page numbers meanwhile.
+constexpr int kCopyVecs = 8, kCopyBytes = 32 * 16 * kCopyVecs;
+__global__ void __launch_bounds__(kIoThreads)
+paged_copy_kernel(const __grid_constant__ Paged p, const int2 *copies, int64_t n) {
+  const int lane = threadIdx.x & 31;
+  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t step = (int64_t)gridDim.x * (kIoThreads / 32);
+  int64_t u = (int64_t)blockIdx.x * (kIoThreads / 32) + (threadIdx.x >> 5);
+  auto pair_of = [&](int64_t piece) {
+    const int64_t k = piece / pieces;
+    return k < n ? __ldg(copies + k) : make_int2(-1, -1);
+  };
+  int2 c = pair_of(u);
+  while (c.x >= 0) {
+    const int64_t at = u % pieces * kCopyBytes + lane * 16;
+    u += step;
+    const int2 next = pair_of(u);
+    if (c.x >= p.n_pages || c.y < 0 || c.y >= p.n_pages) {
+      if (lane == 0) paged_error(p, KVQ_EPAGE);
+    } else if (c.x != c.y) {
+      const uint8_t *src = p.pages + c.x * p.page_bytes + at;
+      uint8_t *dst = p.pages + c.y * p.page_bytes + at;
+      uint4 v[kCopyVecs];
+#pragma unroll
+      for (int i = 0; i < kCopyVecs; ++i)
+        if (at + i * 512 < p.page_bytes) v[i] = *reinterpret_cast<const uint4 *>(src + i * 512);
+#pragma unroll
+      for (int i = 0; i < kCopyVecs; ++i)
+        if (at + i * 512 < p.page_bytes) *reinterpret_cast<uint4 *>(dst + i * 512) = v[i];
+    }
+    c = next;
+  }
+}
+
 // Warps of a call: rows x groups of `per` heads.
 dim3 io_grid(const Paged &p, int per) {
   return dim3((unsigned)((p.T + kIoThreads / 32 - 1) / (kIoThreads / 32)),
@@ -392,6 +427,15 @@ cudaError_t launch_paged_read(const Paged &p, void *k, void *v, cudaStream_t st)
   return p.bits == 2   ? read_as<64, 2>(p, k, v, st)
          : p.bits == 4 ? read_as<64, 4>(p, k, v, st)
                        : read_as<64, 8>(p, k, v, st);
+}
+
+cudaError_t launch_paged_copy(const Paged &p, const int32_t *copies, int64_t n, int num_sms,
+                              cudaStream_t st) {
+  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t blocks = (n * pieces + kIoThreads / 32 - 1) / (kIoThreads / 32);
+  paged_copy_kernel<<<(unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8), kIoThreads, 0, st>>>(
+      p, reinterpret_cast<const int2 *>(copies), n);
+  return cudaGetLastError();
 }
 
 }  // namespace kvq

@@ -445,7 +445,7 @@ paged_rows_kernel(const __grid_constant__ RowsArgs a) {
     const int64_t cap = p.width * p.page;
     const int len = (int)min((int64_t)max(p.lens[b], 0), cap);
     // newest position row r may see; every row's is below len
-    const int64_t pos0 = (int64_t)p.lens[b] - tokens;
+    const int64_t pos0 = first_seen(p, b, tokens);
 
     // queries scaled so that the row's largest is in [2^8, 2^9)
     uint32_t qf[NT][NG][4], qsum[NT];

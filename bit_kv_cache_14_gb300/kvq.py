@@ -41,7 +41,10 @@ EXPORTS = (
     "kvq_decode_attention_noalloc", "kvq_append_decode", "kvq_decode_attention_rope",
     "kvq_decode_kernel_name", "kvq_quantize_prefill_ragged", "kvq_rope_kernel_name",
     "kvq_paged_cache_bytes", "kvq_paged_workspace_bytes", "kvq_paged_write", "kvq_paged_read",
-    "kvq_paged_attention", "kvq_paged_status",
+    "kvq_paged_attention", "kvq_paged_status", "kvq_paged_cross_attention", "kvq_paged_copy",
+    "kvq_read_status", "kvq_pages_state_bytes", "kvq_pages_recount", "kvq_pages_reserve",
+    "kvq_pages_drop", "kvq_pages_select", "kvq_pages_compact", "kvq_verify_workspace_bytes",
+    "kvq_verify_drafts",
 )
 
 
@@ -81,6 +84,19 @@ class _PagedBatch(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("block_table", "seq_lens", "cu_tokens")] + [
         (n, ctypes.c_int64) for n in ("table_width", "n_tokens")] + [
         (n, ctypes.c_int32) for n in ("n_seqs", "max_tokens")]
+
+
+class _PageTable(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "block_table", "seq_lens", "page_refs", "state", "dev_status")] + [
+        (n, ctypes.c_int64) for n in ("n_pages", "table_width")] + [
+        (n, ctypes.c_int32) for n in ("n_seqs", "page_size")]
+
+
+class _DraftBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cu_tokens", "tokens", "dev_status")] + [
+        ("n_tokens", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+            "n_seqs", "vocab", "dtype")]
 
 
 class KVQError(RuntimeError):
@@ -128,7 +144,20 @@ def lib():
             L.kvq_paged_read.argtypes = [PC, PV, PB, P, P, P]
             L.kvq_paged_attention.argtypes = [PC, PV, PB, P, I64, P, ctypes.c_float, P,
                                               ctypes.c_size_t, P]
+            L.kvq_paged_cross_attention.argtypes = L.kvq_paged_attention.argtypes
+            L.kvq_paged_copy.argtypes = [PC, PV, P, I64, P]
             L.kvq_paged_status.argtypes = [PV, P]
+            L.kvq_read_status.argtypes = [P, P]
+            PT, PD = ctypes.POINTER(_PageTable), ctypes.POINTER(_DraftBatch)
+            L.kvq_pages_state_bytes.argtypes = [PT, PS]
+            L.kvq_pages_recount.argtypes = [PT, P]
+            L.kvq_pages_reserve.argtypes = [PT, P, P, P, P]
+            L.kvq_pages_drop.argtypes = [PT, P, P]
+            L.kvq_pages_select.argtypes = [PT, P, P]
+            L.kvq_pages_compact.argtypes = [PT, P, I64, P]
+            L.kvq_verify_workspace_bytes.argtypes = [PD, PS]
+            L.kvq_verify_drafts.argtypes = [PD, P, I64, P, I64, P, P, P, I64, P, P, P, P, P,
+                                            ctypes.c_size_t, P]
             L.kvq_last_launch_count.argtypes = []
             L.kvq_debug_stall_waits.argtypes = [ctypes.c_int64]
             L.kvq_debug_stall_waits.restype = None
@@ -495,6 +524,62 @@ def _raw_stream(index: int) -> int:
     return get(index) if get else torch.cuda.current_stream(index).cuda_stream
 
 
+def _int32(t: torch.Tensor, dims: int, device) -> None:
+    if t.dtype != torch.int32:
+        raise TypeError("expected an int32 tensor, got %s" % t.dtype)
+    if t.dim() != dims or not t.is_contiguous():
+        raise ValueError("expected a contiguous %d-d tensor, got shape %s"
+                         % (dims, tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("expected a tensor on %s, got one on %s" % (device, t.device))
+
+
+def _on(device, index, fn, stream, *args) -> None:
+    """Calls fn(*args, stream) with the device current."""
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        code = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, st)
+    if code != KVQ_OK:
+        raise KVQError(code, fn.__name__)
+
+
+def _output(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor for a call to fill.  On another stream than the current one it
+    comes from that stream's memory (a block that the current stream has yet to
+    finish with may not be written there) and is kept from reuse until the current
+    stream, which is likely to read it, is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _read_status(device, index, status, stream) -> int:
+    with torch.cuda.device(device):
+        st = _raw_stream(index) if stream is None else stream.cuda_stream
+        return lib().kvq_read_status(status.data_ptr(), st)
+
+
+def _cuda_device(device) -> torch.device:
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+def _zeroed(n, dtype, device) -> torch.Tensor:
+    """Zeros that are there before a call on any stream."""
+    t = torch.zeros(n, dtype=dtype, device=device)
+    if device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
+    return t
+
+
 class PagedBatch:
     """The sequences of one call (kvq_paged_batch): int32 device tensors
     block_table [n_seqs][width], seq_lens [n_seqs] and cu_tokens [n_seqs + 1].
@@ -564,6 +649,7 @@ class PagedKVCache:
         L = lib()
         self._write, self._read, self._attend = (L.kvq_paged_write, L.kvq_paged_read,
                                                  L.kvq_paged_attention)
+        self._cross = L.kvq_paged_cross_attention
         self._ws_ptr = self.ws.data_ptr()
         self._index = self.device.index if self.device.type == "cuda" else -1
         self._kv_row = (cfg.n_kv_heads, cfg.head_dim)
@@ -592,14 +678,7 @@ class PagedKVCache:
         return s0 if batch.n_tokens > 1 else heads * d
 
     def _output_on(self, stream, shape) -> torch.Tensor:
-        """A tensor for a call on another stream than the current one to fill.  It
-        comes from that stream's memory (a block that the current stream has yet to
-        finish with may not be written there) and is kept from reuse until the
-        current stream, which is likely to read it, is done."""
-        with torch.cuda.stream(stream):
-            t = torch.empty(shape, dtype=self.dtype, device=self.device)
-        t.record_stream(torch.cuda.current_stream(self.device))
-        return t
+        return _output(shape, self.dtype, self.device, stream)
 
     def _call(self, fn, batch: PagedBatch, stream, *args) -> None:
         if batch.index != self._index:
@@ -643,6 +722,16 @@ class PagedKVCache:
         """Causal attention of q [n_tokens][n_q_heads][head_dim], the rows of
         the batch's newest tokens, over everything their sequences hold (write
         those tokens first).  Returns [n_tokens][n_q_heads][head_dim]."""
+        return self._attention(self._attend, q, batch, out, scale, stream)
+
+    def cross_attend(self, q: torch.Tensor, batch: PagedBatch, out: torch.Tensor | None = None,
+                     scale: float | None = None, stream=None) -> torch.Tensor:
+        """Attention of q [n_tokens][n_q_heads][head_dim] where every row sees
+        all seq_lens tokens of its sequence (an encoder's states), however many
+        rows that has.  Returns [n_tokens][n_q_heads][head_dim]."""
+        return self._attention(self._cross, q, batch, out, scale, stream)
+
+    def _attention(self, fn, q, batch, out, scale, stream) -> torch.Tensor:
         qs = self._rows(q, batch, self.cfg.n_q_heads)
         if out is not None:
             self._rows(out, batch, self.cfg.n_q_heads)
@@ -652,9 +741,19 @@ class PagedKVCache:
                               device=self.device)
         else:
             out = self._output_on(stream, (batch.n_tokens,) + self._q_row)
-        self._call(self._attend, batch, stream, q.data_ptr(), qs, out.data_ptr(),
+        self._call(fn, batch, stream, q.data_ptr(), qs, out.data_ptr(),
                    self._scale if scale is None else scale, self._ws_ptr, self.ws_bytes)
         return out
+
+    def copy_pages(self, copies: torch.Tensor, stream=None) -> None:
+        """Copies pages inside the pool: copies int32 [n][2], pairs (from, to) up
+        to the first whose ``from`` is negative (PageTable.reserve's and
+        PageTable.compact's)."""
+        _int32(copies, 2, self.device)
+        if copies.shape[1] != 2:
+            raise ValueError("expected pairs [n][2], got shape %s" % (tuple(copies.shape),))
+        _on(self.device, self._index, lib().kvq_paged_copy, stream, *self._refs,
+            copies.data_ptr(), copies.shape[0])
 
     def device_status(self, stream=None) -> int:
         """Synchronizes, reads and clears the status word.  After an error the
@@ -667,6 +766,217 @@ class PagedKVCache:
                 self.ws.zero_()
                 torch.cuda.synchronize(self.device)
         return code
+
+
+class PageTable:
+    """Page tables on the device (kvq_page_table): block_table int32
+    [n_seqs][width], seq_lens int32 [n_seqs] and page_refs int32 [n_pages], one set
+    for the page pools of all layers.  An empty pool, or given tables
+    (``block_table`` and ``seq_lens``; they are taken over, not copied).  Calls run
+    on ``stream`` (default: the current stream of the device), one at a time; none
+    waits for the device, and all can be captured."""
+
+    def __init__(self, n_pages: int, page_size: int, n_seqs: int | None = None,
+                 width: int | None = None, device="cuda", block_table=None, seq_lens=None):
+        if (block_table is None) != (seq_lens is None):
+            raise ValueError("block_table and seq_lens are given together")
+        if block_table is not None:
+            self.device = block_table.device
+            _int32(block_table, 2, self.device)
+            _int32(seq_lens, 1, self.device)
+            if seq_lens.shape[0] != block_table.shape[0]:
+                raise ValueError("block_table %s and seq_lens %s do not match"
+                                 % (tuple(block_table.shape), tuple(seq_lens.shape)))
+            if n_seqs not in (None, block_table.shape[0]) or width not in (
+                    None, block_table.shape[1]):
+                raise ValueError("n_seqs and width are the given tables'")
+            n_seqs, width = block_table.shape
+        elif n_seqs is None or width is None:
+            raise ValueError("n_seqs and width, or block_table and seq_lens, are needed")
+        else:
+            self.device = _cuda_device(device)
+        self._index = self.device.index if self.device.type == "cuda" else -1
+        self.n_seqs, self.page_size, self.n_pages = n_seqs, page_size, n_pages
+        self.view = _PageTable(None, None, None, None, None, n_pages, width, n_seqs, page_size)
+        n = ctypes.c_size_t()
+        _check(lib().kvq_pages_state_bytes(ctypes.byref(self.view), ctypes.byref(n)),
+               "kvq_pages_state_bytes")
+        i32 = dict(dtype=torch.int32, device=self.device)
+        if block_table is None:
+            block_table = torch.full((n_seqs, width), -1, **i32)
+            seq_lens = torch.zeros(n_seqs, **i32)
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.page_refs = torch.zeros(n_pages, **i32)
+        self.state = torch.zeros(n.value, dtype=torch.uint8, device=self.device)
+        self.status = _zeroed(1, torch.int32, self.device)
+        for name, t in (("block_table", block_table), ("seq_lens", seq_lens),
+                        ("page_refs", self.page_refs), ("state", self.state),
+                        ("dev_status", self.status)):
+            setattr(self.view, name, t.data_ptr())
+        self._ref = ctypes.byref(self.view)
+        if self.device.type == "cuda":
+            self.recount()
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(self.device).synchronize()
+
+    @property
+    def free_pages(self) -> torch.Tensor:
+        """Number of free pages: int32 [1], on the device."""
+        return self.state[:4].view(torch.int32)
+
+    def batch(self, cu_tokens, n_tokens: int, max_tokens: int | None = None) -> PagedBatch:
+        """These tables and lengths as the sequences of paged calls."""
+        return PagedBatch(self.block_table, self.seq_lens, cu_tokens, n_tokens, max_tokens)
+
+    def _call(self, fn, stream, *args) -> None:
+        _on(self.device, self._index, fn, stream, self._ref, *args)
+
+    def _of_seqs(self, t, n) -> int:
+        _int32(t, 1, self.device)
+        if t.shape[0] != n:
+            raise ValueError("expected %d numbers, got %d" % (n, t.shape[0]))
+        return t.data_ptr()
+
+    def recount(self, stream=None) -> None:
+        """Counts every page's holders again, after block_table or seq_lens were
+        written to."""
+        self._call(lib().kvq_pages_recount, stream)
+
+    def reserve(self, cu_tokens: torch.Tensor, out=None, stream=None):
+        """Pages for cu_tokens' new tokens; seq_lens grows by them.  Returns
+        (copies, cu): int32 [n_seqs][2] for PagedKVCache.copy_pages, to run before
+        the tokens are written, and int32 [n_seqs + 1] for the batch of the calls
+        that follow (cu_tokens, or zeros where pages did not suffice).  ``out``:
+        the two tensors to fill."""
+        cu = self._of_seqs(cu_tokens, self.n_seqs + 1)
+        if out is None:
+            copies = _output((self.n_seqs, 2), torch.int32, self.device, stream)
+            call = _output(self.n_seqs + 1, torch.int32, self.device, stream)
+        else:
+            copies, call = out
+            _int32(copies, 2, self.device)
+            if copies.shape != (self.n_seqs, 2):
+                raise ValueError("expected %d pairs, got shape %s"
+                                 % (self.n_seqs, tuple(copies.shape)))
+            self._of_seqs(call, self.n_seqs + 1)
+        self._call(lib().kvq_pages_reserve, stream, cu, copies.data_ptr(), call.data_ptr())
+        return copies, call
+
+    def drop(self, tokens: torch.Tensor, stream=None) -> None:
+        """Takes back the newest tokens[b] tokens of every sequence (all, and the
+        sequence ends, where that is as many or more) and frees their pages."""
+        self._call(lib().kvq_pages_drop, stream, self._of_seqs(tokens, self.n_seqs))
+
+    def select(self, parents: torch.Tensor, stream=None) -> None:
+        """Sequence b becomes what parents[b] was (b: stays, -1: ends), sharing
+        its pages: forks, beams in a new order."""
+        self._call(lib().kvq_pages_select, stream, self._of_seqs(parents, self.n_seqs))
+
+    def compact(self, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Live pages move to the front of the pool.  Returns the moves for
+        PagedKVCache.copy_pages of every pool, int32 [max(1, n_pages // 2)][2]."""
+        rows = max(1, self.n_pages // 2)
+        if out is None:
+            out = _output((rows, 2), torch.int32, self.device, stream)
+        else:
+            _int32(out, 2, self.device)
+            if out.shape[0] < rows or out.shape[1] != 2:
+                raise ValueError("expected at least %d pairs, got shape %s"
+                                 % (rows, tuple(out.shape)))
+        self._call(lib().kvq_pages_compact, stream, out.data_ptr(), out.shape[0])
+        return out
+
+    def device_status(self, stream=None) -> int:
+        """Synchronizes, reads and clears the status word."""
+        return _read_status(self.device, self._index, self.status, stream)
+
+
+F32 = 2  # logits only
+_LOGIT_DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+
+
+class DraftVerifier:
+    """Decides which drafted tokens stay (kvq_verify_drafts), with scratch for up
+    to n_seqs sequences and n_tokens rows of logits of one type and vocabulary.
+    Calls that can run at the same time need verifiers of their own."""
+
+    def __init__(self, n_seqs: int, n_tokens: int, vocab: int, dtype=torch.bfloat16,
+                 device="cuda"):
+        if dtype not in _LOGIT_DTYPES:
+            raise TypeError("expected float16, bfloat16 or float32 logits, got %s" % dtype)
+        self.device = _cuda_device(device)
+        self._index = self.device.index if self.device.type == "cuda" else -1
+        self.n_seqs, self.n_tokens, self.vocab, self.dtype = n_seqs, n_tokens, vocab, dtype
+        n = ctypes.c_size_t()
+        view = _DraftBatch(None, None, None, n_tokens, n_seqs, vocab, _LOGIT_DTYPES[dtype])
+        _check(lib().kvq_verify_workspace_bytes(ctypes.byref(view), ctypes.byref(n)),
+               "kvq_verify_workspace_bytes")
+        self.ws_bytes = n.value
+        self.ws = torch.zeros(n.value, dtype=torch.uint8, device=self.device)
+        self.status = _zeroed(1, torch.int32, self.device)
+
+    def _rows(self, t: torch.Tensor, rows: int, dtype) -> int:
+        """Checks [rows][vocab] with contiguous rows of any stride; returns it."""
+        if t.dtype != dtype:
+            raise TypeError("expected a %s tensor, got %s" % (dtype, t.dtype))
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != self.vocab:
+            raise ValueError("expected shape %s, got %s" % ((rows, self.vocab), tuple(t.shape)))
+        if t.device != self.device:
+            raise ValueError("expected a tensor on %s, got one on %s" % (self.device, t.device))
+        s0, s1 = t.stride()
+        if rows > 0 and self.vocab > 1 and s1 != 1:
+            raise ValueError("each row must be contiguous (got strides %s)" % (t.stride(),))
+        return s0 if rows > 1 else self.vocab
+
+    def _floats(self, t: torch.Tensor, n: int) -> int:
+        if t.dtype != torch.float32:
+            raise TypeError("expected a float32 tensor, got %s" % t.dtype)
+        if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+            raise ValueError("expected %d contiguous numbers, got shape %s" % (n, tuple(t.shape)))
+        if t.device != self.device:
+            raise ValueError("expected a tensor on %s, got one on %s" % (self.device, t.device))
+        return t.data_ptr()
+
+    def verify(self, logits, tokens, cu_tokens, draft_logits=None, temperature=None,
+               uniform=None, noise=None, stream=None):
+        """Rows [cu_tokens[b], cu_tokens[b+1]) are sequence b's newest token and its
+        drafts: logits [n][vocab] of the token after each, tokens int32 [n];
+        draft_logits [n][vocab] or None (drafts found by lookup); temperature [n_seqs]
+        (None: greedy), uniform [n] in [0, 1) and noise [n_seqs][vocab] of the
+        exponential distribution.  Returns (tokens, accepted, dropped, logprobs):
+        per row the drafts that stay, then the next token, then -1; per sequence the
+        drafts that stay and those that do not (PageTable.drop); per row the
+        token's log probability."""
+        _int32(tokens, 1, self.device)
+        _int32(cu_tokens, 1, self.device)
+        T, B = tokens.shape[0], cu_tokens.shape[0] - 1
+        if B < 1 or B > self.n_seqs or T > self.n_tokens:
+            raise ValueError("%d rows of %d sequences: the verifier is for %d of %d"
+                             % (T, B, self.n_tokens, self.n_seqs))
+        stride = self._rows(logits, T, self.dtype)
+        dptr, dstride = None, 0
+        if draft_logits is not None:
+            dptr, dstride = draft_logits.data_ptr(), self._rows(draft_logits, T, self.dtype)
+        tptr = uptr = nptr = None
+        nstride = 0
+        if temperature is not None:
+            if uniform is None or noise is None:
+                raise ValueError("sampling needs uniform and noise")
+            tptr, uptr = self._floats(temperature, B), self._floats(uniform, T)
+            nptr, nstride = noise.data_ptr(), self._rows(noise, B, torch.float32)
+        out, logprobs = (_output(T, d, self.device, stream) for d in (torch.int32, torch.float32))
+        accepted, dropped = (_output(B, torch.int32, self.device, stream) for _ in range(2))
+        view = _DraftBatch(cu_tokens.data_ptr(), tokens.data_ptr(), self.status.data_ptr(), T, B,
+                           self.vocab, _LOGIT_DTYPES[self.dtype])
+        _on(self.device, self._index, lib().kvq_verify_drafts, stream, ctypes.byref(view),
+            logits.data_ptr(), stride, dptr, dstride, tptr, uptr, nptr, nstride, out.data_ptr(),
+            accepted.data_ptr(), dropped.data_ptr(), logprobs.data_ptr(), self.ws.data_ptr(),
+            self.ws_bytes)
+        return out, accepted, dropped, logprobs
+
+    def device_status(self, stream=None) -> int:
+        """Synchronizes, reads and clears the status word."""
+        return _read_status(self.device, self._index, self.status, stream)
 
 
 def debug_stall_waits(iterations: int) -> None:

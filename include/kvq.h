@@ -84,7 +84,7 @@ extern "C" {
 #define KVQ_OK 0
 #define KVQ_EINVAL (-1)       /* null pointer, negative size, inconsistent config */
 #define KVQ_EUNSUPPORTED (-2) /* valid but not built: head_dim, bits, group sizes */
-#define KVQ_ECAPACITY (-3)    /* the call would exceed max_ctx or the workspace */
+#define KVQ_ECAPACITY (-3)    /* the call would exceed max_ctx, the pages or the workspace */
 #define KVQ_EALIGN (-4)       /* a device buffer is not 16-byte aligned */
 #define KVQ_ECUDA (-5)        /* a CUDA launch or copy failed */
 #define KVQ_ETIMEOUT (-6)     /* a bounded device-side wait gave up (status word) */
@@ -427,6 +427,7 @@ int kvq_rope_kernel_name(const kvq_config *cfg, int64_t n_quant, char *buf, size
  */
 #define KVQ_F16 0
 #define KVQ_BF16 1
+#define KVQ_F32 2 /* logits only */
 
 /*
  *   n_q_heads, n_kv_heads: n_q_heads = r * n_kv_heads, 1 <= r <= 128; query
@@ -541,10 +542,187 @@ int kvq_paged_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cach
                         const kvq_paged_batch *batch, const void *q, int64_t q_stride, void *out,
                         float softmax_scale, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Cross attention of the call's rows over the pages: every row of sequence b sees
+ * all seq_lens[b] tokens (an encoder's states, written once), whatever the number
+ * of its rows, which may be larger: the rows are no tokens of the sequence.  Rows
+ * that read the same states (beams, samples) go in as rows of one sequence and
+ * share its reads.  Arguments, arithmetic, results and errors are otherwise those
+ * of kvq_paged_attention; a sequence without tokens gives its rows zeros.
+ */
+int kvq_paged_cross_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
+                              const kvq_paged_batch *batch, const void *q, int64_t q_stride,
+                              void *out, float softmax_scale, void *ws, size_t ws_bytes,
+                              void *stream);
+
+/*
+ * Copy pages inside the pool.  copies: device int32 [n_copies][2], 8-byte aligned:
+ * pairs (from, to), ended by n_copies or by the first pair whose `from` is
+ * negative.  Pairs run in no order: a page may be copied to several others, but no
+ * `to` is named twice or is another pair's `from`.  A pair that names a page
+ * outside [0, n_pages) is skipped and gives KVQ_EPAGE in the status word.  Whole
+ * pages are copied, slots without tokens too.
+ * Errors: KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EALIGN, KVQ_ECUDA.
+ */
+int kvq_paged_copy(const kvq_paged_config *cfg, kvq_paged_cache *cache, const int32_t *copies,
+                   int64_t n_copies, void *stream);
+
 /* Synchronizes `stream`, reads and clears the status word; KVQ_OK, or what a
  * kernel recorded there, or KVQ_ECUDA.  Of several errors it holds the first
  * (KVQ_EPAGE, KVQ_EINVAL), but KVQ_ETIMEOUT before either. */
 int kvq_paged_status(kvq_paged_cache *cache, void *stream);
+
+/* The same for any status word. */
+int kvq_read_status(int32_t *dev_status, void *stream);
+
+/* ---- Page tables ----------------------------------------------------------
+ *
+ * Who holds which page, kept on the device: pages for a step's new tokens, copies
+ * of shared pages before they are written, tokens taken back, sequences forked,
+ * reordered and ended, the pool made compact.  One set of tables serves the page
+ * pools of all layers: the tables change once a step, and the copies they ask for
+ * (kvq_paged_copy) run in every pool.  Nothing is read back by the host, so a step
+ * with all of these calls can be captured in a CUDA graph.
+ *
+ *   block_table, seq_lens: as in kvq_paged_batch, for n_seqs slots (1..2048).  A
+ *     sequence of n tokens holds ceil(n / page_size) entries; those behind them are
+ *     -1.  A slot without tokens is free.
+ *   page_refs int32 [n_pages]: how many entries of all tables name each page; 0 is
+ *     a free page.
+ *   state: kvq_pages_state_bytes of device memory, 16-byte aligned: the free pages'
+ *     map and scratch of the calls.
+ *   dev_status: an int32 status word, zero-filled once.
+ *   n_pages: 1..2^26.  page_size: 16, 32, 64, 128 or 256.
+ * The buffers are the caller's.  kvq_pages_recount has to run before any other
+ * call, and again after the caller has written to tables or lengths itself.  Calls
+ * on one table never run at the same time.
+ *
+ * What the device arrays say is checked there, and goes to the status word: an
+ * entry that is no page (KVQ_EPAGE, skipped), a negative length or holder counts
+ * that do not agree with the tables (KVQ_EINVAL).
+ * Every call returns KVQ_OK, KVQ_EINVAL (null, sizes), KVQ_EUNSUPPORTED, KVQ_EALIGN
+ * or KVQ_ECUDA, and what is said there.
+ */
+typedef struct kvq_page_table {
+  int32_t *block_table, *seq_lens, *page_refs;
+  void *state;
+  int32_t *dev_status;
+  int64_t n_pages, table_width;
+  int32_t n_seqs, page_size;
+} kvq_page_table;
+
+/* Bytes of `state`; only the sizes of *table are looked at.  Host only. */
+int kvq_pages_state_bytes(const kvq_page_table *table, size_t *bytes);
+
+/* Count the holders of every page from block_table and seq_lens (all zero: an
+ * empty pool), and set entries behind a sequence's last to -1. */
+int kvq_pages_recount(const kvq_page_table *table, void *stream);
+
+/*
+ * Pages for new tokens: sequence b is about to get n_b = cu_tokens[b+1] -
+ * cu_tokens[b] more (0: left alone), seq_lens[b] grows by them, and its table gets
+ * the pages they need, the lowest-numbered free ones first, by sequence and entry.
+ * A partly filled last page that others hold too is copied before it is written:
+ * the sequence gets a page of its own (the first of its new ones).  Of sequences
+ * that get tokens in this call and are all the holders of such a page, the first
+ * keeps it.
+ *   cu_tokens int32 [n_seqs+1], as in kvq_paged_batch.
+ *   copies int32 [n_seqs][2], 8-byte aligned: the copies to make before the tokens
+ *     are written, for kvq_paged_copy; (-1, -1) behind the last.
+ *   cu_call int32 [n_seqs+1], apart from cu_tokens: cu_tokens again, or zeros where
+ *     the call failed; given to kvq_paged_write and kvq_paged_attention as
+ *     cu_tokens, it makes a failed step write and attend to nothing.
+ * All or nothing: where pages (KVQ_ECAPACITY) or table entries (KVQ_ECAPACITY) do
+ * not suffice or the arrays are wrong (KVQ_EINVAL, KVQ_EPAGE), the status word says
+ * so, nothing changes and there are no copies.
+ */
+int kvq_pages_reserve(const kvq_page_table *table, const int32_t *cu_tokens, int32_t *copies,
+                      int32_t *cu_call, void *stream);
+
+/* Take back the newest tokens[b] (device int32 [n_seqs]) tokens of every sequence
+ * (none where <= 0, all where as many or more: the sequence ends), and let go of
+ * the pages that hold nothing else of it. */
+int kvq_pages_drop(const kvq_page_table *table, const int32_t *tokens, void *stream);
+
+/* Sequence b becomes what sequence parents[b] (device int32 [n_seqs]) was before
+ * the call: b itself stays, -1 empties b, others fork or reorder; the pages are
+ * shared, and pages nobody holds any more are free.  A parent outside [-1, n_seqs)
+ * leaves b as it is and gives KVQ_EINVAL in the status word. */
+int kvq_pages_select(const kvq_page_table *table, const int32_t *parents, void *stream);
+
+/* Bring the n live pages to [0, n): the k-th live page from n on moves to the k-th
+ * free page before n, and tables and counts follow.  copies int32 [n_copies][2],
+ * 8-byte aligned, n_copies >= n_pages / 2 (KVQ_ECAPACITY): the moves, for
+ * kvq_paged_copy in every pool; (-1, -1) behind the last. */
+int kvq_pages_compact(const kvq_page_table *table, int32_t *copies, int64_t n_copies,
+                      void *stream);
+
+/* ---- Drafted tokens --------------------------------------------------------
+ *
+ * Speculative decoding's decision.  A step runs the model on rows
+ * [cu_tokens[b], cu_tokens[b+1]) of sequence b: its newest token, then its drafts.
+ * Row t's logits are those of the token after tokens[t], so row t judges
+ * tokens[t+1], and the last row has the token after the last draft.
+ */
+typedef struct kvq_draft_batch {
+  const int32_t *cu_tokens; /* device [n_seqs+1], as in kvq_paged_batch */
+  const int32_t *tokens;    /* device [n_tokens] */
+  int32_t *dev_status;      /* device status word, zero-filled once */
+  int64_t n_tokens;         /* rows of the packed arrays, 0..65535; rows from
+                               cu_tokens[n_seqs] on are padding */
+  int32_t n_seqs, vocab, dtype; /* 1..2048; 1..2^24; KVQ_F16, KVQ_BF16 or KVQ_F32 */
+} kvq_draft_batch;
+
+/* Bytes of scratch kvq_verify_drafts needs for these sizes (the pointers are not
+ * looked at); it does not shrink as sizes grow.  Zero-fill it once; every call
+ * leaves what must be zero at zero again.  Calls that can run at the same time need
+ * scratch of their own.  Host only. */
+int kvq_verify_workspace_bytes(const kvq_draft_batch *batch, size_t *bytes);
+
+/*
+ * Accept or refuse drafts and draw the next token (Leviathan et al. 2023, "Fast
+ * inference from transformers via speculative decoding", algorithm 1).
+ *   logits: device, row t at logits + t*stride (dtype elements, stride >= vocab, any
+ *     alignment of the dtype): x.  draft_logits: y, the draft model's for the same
+ *     rows (a sequence's last row is not read), or NULL: each draft was certain
+ *     (found by lookup).
+ *   temperature: device [n_seqs], T > 0; a sequence where it is not (0, NaN) is
+ *     greedy.  NULL: all are.
+ *   uniform: device [n_tokens], in [0, 1): row t's number judges tokens[t+1].
+ *   noise: device, row b at noise + b*noise_stride: e_i of the exponential
+ *     distribution (-log of a uniform number), one for every token of the vocabulary.
+ *   (uniform and noise may be NULL where temperature is; greedy sequences read
+ *   neither, nor y.)
+ * With p = softmax(x / T), q = softmax(y / T) (1 at the draft for NULL), draft c of
+ * row t stays while every earlier one does and uniform[t] * q_c < p_c.  The next
+ * token is at the first refused row the i of the largest max(p_i - q_i, 0) / e_i
+ * (p_i / e_i if all are 0), at the last row, if all stay, of the largest p_i / e_i;
+ * of equal ones the lowest.  Its distribution is p's, whatever the drafts.  Greedy:
+ * a draft stays while it is the lowest index of x's maximum, and that is the next
+ * token.
+ *   out_tokens [n_tokens]: for each sequence from its first row on, the drafts that
+ *     stayed, then the next token, then -1.
+ *   logprobs fp32 [n_tokens]: ln p of each of those tokens (greedy: at T = 1), 0
+ *     for -1.
+ *   accepted, dropped [n_seqs]: drafts that stayed, and the others: what
+ *     kvq_pages_drop takes back, since the cache holds the rows' tokens.
+ * Masked: a logit of -infinity, NaN or at most -2^126 has probability 0; logits
+ * beyond 2^126 count as 2^126.  A row with nothing else has no next token: -1.
+ * e_i below 2^-126 counts as that, NaN takes i out.  T is held to 2^-25..2^100.
+ * A draft outside [0, vocab) is refused and gives KVQ_EINVAL in the status word;
+ * so do rows of a sequence out of order or behind n_tokens, whose outputs are left
+ * alone but for 0 accepted, 0 dropped.  A sequence without rows gets those too.
+ * Arithmetic: fp32, sums in fp32 in a fixed order; exponents of the drafts' tests
+ * in 64 bits.  p and q are within 1e-6 (relative) of the exact ones, so numbers that
+ * close to a border may fall on its other side.
+ * Errors: KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EALIGN, KVQ_ECAPACITY (ws too small),
+ *   KVQ_ECUDA.
+ */
+int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t stride,
+                      const void *draft_logits, int64_t draft_stride, const float *temperature,
+                      const float *uniform, const float *noise, int64_t noise_stride,
+                      int32_t *out_tokens, int32_t *accepted, int32_t *dropped, float *logprobs,
+                      void *ws, size_t ws_bytes, void *stream);
 
 /* Number of kernel launches the last successful call of this thread enqueued. */
 int kvq_last_launch_count(void);

@@ -1,0 +1,166 @@
+"""Cross attention over the pages: every row sees all tokens of its sequence.  The
+bound is the causal one's (tests/paged_norm.py) of as many sequences of one row."""
+import itertools
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from bit_kv_cache_14_gb300 import build_lib, kvq
+from paged_norm import check_rows
+from paged_util import Case
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build_lib.build()
+    yield
+
+
+class Cross(Case):
+    """A case whose rows are no tokens of the sequences: any number of them."""
+
+    def filled(self, device="cuda"):
+        new, self.new = self.new, [max(k, 0) for k in self.kv]
+        cache = super().filled(device)
+        self.new = new
+        return cache
+
+    def single_rows(self):
+        """The same attention as causal rows, one a sequence."""
+        one = object.__new__(Case)
+        one.__dict__.update(self.__dict__)
+        at = [b for b, n in enumerate(self.new) for _ in range(n)]
+        one.kv, one.new = [self.kv[b] for b in at], [1] * len(at)
+        one.K, one.V = [self.K[b] for b in at], [self.V[b] for b in at]
+        one.cu = np.arange(len(at) + 1)
+        return one
+
+    def check(self, out, **kw):
+        return check_rows(self.single_rows(), out, **kw)
+
+
+FORMATS = list(itertools.product((64, 128), (2, 4, 8), (F16, BF16)))
+
+
+@pytest.mark.parametrize("d,bits,dtype", FORMATS)
+@pytest.mark.parametrize("new", [(1, 1, 1, 1, 1), (4, 3, 2, 1, 4), (16, 0, 9, 12, 5),
+                                 (40, 1, 130, 300, 7)])
+def test_against_64_bits(d, bits, dtype, new):
+    """Empty encoders, one token, pages and tiles that end inside; more rows than
+    tokens; few rows, many, and both in one call."""
+    c = Cross([150, 1, 0, 129, 300], new, 8, 2, d, bits, 32, dtype, seed=d + bits)
+    cache = c.filled()
+    out = cache.cross_attend(c.queries(), c.batch())
+    assert cache.device_status() == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(seed):
+    rng = random.Random(seed)
+    hkv, rg = rng.choice([1, 2, 3]), rng.choice([1, 2, 3, 4, 5, 8, 16, 20])
+    B = rng.randint(1, 6)
+    kv = [rng.choice([0, 1, 15, 16, 17, 33, 127, 128, 129, 300, 700]) for _ in range(B)]
+    new = [rng.choice([0, 1, 1, 2, 5, 33, 90, 400 // rg]) for _ in range(B)]
+    c = Cross(kv, new, hkv * rg, hkv, rng.choice([64, 128]), rng.choice([2, 4, 8]),
+              rng.choice([16, 32, 64, 128, 256]), rng.choice([F16, BF16]), seed=seed,
+              pad=rng.choice([0, 3]))
+    cache = c.filled()
+    out = torch.full((c.n_tokens, c.hq, c.d), 7.0, dtype=c.dtype, device="cuda")
+    cache.cross_attend(c.queries(), c.batch(n_tokens=c.n_tokens), out=out)
+    assert cache.device_status() == 0
+    c.check(out)
+    assert (out[int(c.cu[-1]):] == 7).all()      # padding is left alone
+
+
+@pytest.mark.parametrize("bits", (2, 4, 8))
+@pytest.mark.parametrize("rg", (1, 4))
+def test_one_row_is_the_decode_step(bits, rg):
+    """The newest token sees everything: with one row the causal call's bits."""
+    c = Cross([900, 64, 1, 333], [1] * 4, 2 * rg, 2, 128, bits, 64, BF16)
+    cache = c.filled()
+    assert torch.equal(cache.cross_attend(c.queries(), c.batch()),
+                       cache.attend(c.queries(), c.batch()))
+
+
+def test_beams_share_the_reads_of_an_encoder():
+    """Beams as rows of one sequence, or as sequences over the same pages: both are
+    the operator."""
+    c = Cross([700, 90], [4, 4], 8, 2, 128, 4, 16, F16)
+    cache = c.filled()
+    q = c.queries()
+    together = cache.cross_attend(q, c.batch())
+    t = lambda a: torch.from_numpy(np.repeat(a, 4, 0).astype(np.int32)).cuda()  # noqa: E731
+    apart = kvq.PagedBatch(t(c.table), t(np.array(c.kv)),
+                           torch.arange(9, dtype=torch.int32, device="cuda"), 8, 1)
+    c.check(together)
+    c.check(cache.cross_attend(q, apart))
+
+
+@pytest.mark.parametrize("rows", (3, 70))
+def test_missing_pages_and_lengths(rows):
+    """A page that is not there is not attended to; a length beyond the table ends
+    with it."""
+    c = Cross([200, 200, 64], [rows] * 3, 4, 1, 64, 4, 16, F16)
+    cache = c.filled()
+    c.table[1, 3] = c.n_pages
+    out = cache.cross_attend(c.queries(), c.batch())
+    assert cache.device_status() == kvq.KVQ_EPAGE
+    one = c.single_rows()
+    check_rows(one, out, gone={rows + i: range(48, 64) for i in range(rows)})
+    c.table[1, 3] = 0
+    long = c.batch(kv=[200, 200, 10 ** 6])
+    cache.cross_attend(c.queries(), long)
+    assert cache.device_status() == kvq.KVQ_EPAGE
+    neg = cache.cross_attend(c.queries(), c.batch(kv=[-3, 0, -2 ** 31]))
+    assert (neg == 0).all() and cache.device_status() == 0
+
+
+def test_queries_of_a_wider_tensor_and_any_scale():
+    c = Cross([130, 260], [2, 50], 4, 2, 128, 8, 64, BF16)
+    cache = c.filled()
+    wide = torch.randn(52, 9, 128, device="cuda").to(BF16)
+    wide[:, 3:7] = c.queries()
+    for scale in (0.0, -0.05, 0.3):
+        out = cache.cross_attend(wide[:, 3:7], c.batch(), scale=scale)
+        c.check(out, scale=scale)
+
+
+def test_captured_with_lengths_that_change():
+    c = Cross([300, 40], [2, 30], 4, 1, 64, 4, 16, F16)
+    cache = c.filled()
+    batch, q = c.batch(), c.queries()
+    out = cache.cross_attend(q, batch)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cache.cross_attend(q, batch, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.cross_attend(q, batch, out=out)
+    K, V = c.K, c.V
+    for lens in ([300, 40], [17, 0], [1, 33]):
+        batch.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.kv, c.K, c.V = lens, [K[0][:lens[0]], K[1][:lens[1]]], [V[0][:lens[0]], V[1][:lens[1]]]
+        c.check(out)
+    assert cache.device_status() == 0
+
+
+def test_given_stream():
+    c = Cross([500], [3], 4, 2, 64, 2, 32, F16)
+    cache = c.filled()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = cache.cross_attend(c.queries(), c.batch(), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    c.check(out)
