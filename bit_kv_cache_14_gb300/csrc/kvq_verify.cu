@@ -7,12 +7,12 @@
 // largest p_i / e_i, with the caller's exponential e (the smallest of exponentials
 // of rates p_i is at i with probability p_i).
 //
-// Two launches.  Rows: every (row, part of the vocabulary) leaves its maximum m
-// and s = sum 2^((x - m) c), c = log2(e) / T, so each logit is read once; all rows
-// are taken, since which draft is the first refused is known only afterwards.
-// Draw: the blocks of a sequence each join its rows' parts (a few hundred bytes),
-// decide, and race their share of the one row that is drawn from; shares are joined
-// by a maximum over (score, lowest index), which has no order.
+// Two launches.  Rows: a warp reads 4 KB of a row and leaves its maximum m and s = sum
+// 2^((x - m) c), c = log2(e) / T, so each logit is read once; all rows are taken, since
+// which draft is the first refused is known only afterwards.  Draw: the blocks of a
+// sequence each join its rows' parts (a KB a row), decide, and race their share of the
+// one row that is drawn from; shares are joined by a maximum over (score, lowest
+// index), which has no order.
 #include <algorithm>
 
 #include "kvq_paged.cuh"
@@ -23,12 +23,9 @@ namespace {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int64_t kMaxRows = 65535;      // (rows are a grid dimension)
+constexpr int64_t kMaxRows = 65535;
 constexpr int64_t kMaxVocab = 1 << 24;
-// Logits are held to +-2^126, so that differences of two are finite; a logit down
-// there is masked (probability 0), and NaN is taken as masked.
-constexpr float kMasked = -8.507059e37f;
-constexpr double kLog2e = 1.4426950408889634;
+constexpr float kMasked = -INFINITY;  // logits of probability 0; NaN is taken as one
 
 struct VerifyArgs {
   const int32_t *cu, *tokens;
@@ -38,7 +35,7 @@ struct VerifyArgs {
   int32_t *out, *accepted, *dropped;
   float *logprobs;
   int32_t *status;
-  unsigned long long *keys;  // [B][2], zero between calls
+  unsigned long long *keys;  // [B], zero between calls
   int *tickets;              // [B], zero between calls
   float4 *parts;             // [2][T][parts]: maximum, sum, lowest index of the maximum
   int64_t T;
@@ -67,16 +64,28 @@ __device__ __forceinline__ int sequence_of(const VerifyArgs &a, int64_t t) {
   return t >= r0 && t < r1 && !bad_range(a, r0, r1) ? lo : -1;
 }
 
-// The temperature of sequence b; 0: greedy (also for what is no temperature).
+// The temperature of sequence b; 0: greedy (also for NaN).
 __device__ __forceinline__ float temperature_of(const VerifyArgs &a, int b) {
   const float t = a.temperature ? a.temperature[b] : 0.0f;
-  return t > 0.0f ? t : 0.0f;
+  return t > 0.0f ? fminf(fmaxf(t, 0x1p-100f), 0x1p100f) : 0.0f;
 }
-// log2(e) / T in 64 bits, held where its product with any difference of logits and
-// that product's low part stay numbers.  Greedy rows: T = 1.
-__device__ __forceinline__ double factor_of(float temperature) {
-  const double c = temperature > 0.0f ? kLog2e / (double)temperature : kLog2e;
-  return fmin(fmax(c, 0x1p-100), 0x1p25);
+// log2(e) / T in two parts (greedy rows: T = 1): a difference of logits is exact or
+// nearly so, and its product keeps what one rounded factor would lose for every
+// element alike.  Both are positive, so minus infinity times them stays that.
+struct Factor {
+  float hi, lo;
+};
+__device__ __forceinline__ Factor factor_of(float temperature) {
+  constexpr float kHi = 1.4426950408889634f;
+  constexpr float kLo = (float)(1.4426950408889634 - (double)kHi);
+  static_assert(kLo > 0.0f, "the first part is rounded down");
+  const float t = temperature > 0.0f ? temperature : 1.0f, hi = __fdiv_rz(kHi, t);
+  return {hi, (fmaf(-hi, t, kHi) + kLo) / t};
+}
+// 2^((x - m) c)
+__device__ __forceinline__ float weight(float x, float m, Factor c) {
+  const float d = x - m;
+  return exp2_approx(fmaf(d, c.hi, d * c.lo));
 }
 
 // Types: 0 fp16, 1 bf16, 2 fp32.
@@ -84,8 +93,27 @@ template <int TYPE>
 struct Logit {
   static constexpr int kSize = TYPE == 2 ? 4 : 2;
   static constexpr int kVec = 16 / kSize;  // of a 16-byte vector
+  static constexpr float kMost = TYPE == 0 ? 65504.0f : TYPE == 1 ? 3.3895314e38f : 3.4028235e38f;
 };
-__device__ __forceinline__ float tame(float x) { return fminf(fmaxf(x, kMasked), -kMasked); }
+// A logit as the operator takes it: NaN masked, plus infinity the largest number.
+template <int TYPE>
+__device__ __forceinline__ float tame(float x) {
+  return fminf(fmaxf(x, kMasked), Logit<TYPE>::kMost);
+}
+// ... and a word of them.
+template <int TYPE>
+__device__ __forceinline__ uint32_t tame_word(uint32_t w) {
+  if (TYPE == 0) {
+    asm("max.f16x2 %0, %0, %1;" : "+r"(w) : "r"(0xfc00fc00u));
+    asm("min.f16x2 %0, %0, %1;" : "+r"(w) : "r"(0x7bff7bffu));
+  } else if (TYPE == 1) {
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xff80ff80u));
+    asm("min.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x7f7f7f7fu));
+  } else {
+    w = __float_as_uint(tame<2>(__uint_as_float(w)));
+  }
+  return w;
+}
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 template <int TYPE>
@@ -97,7 +125,7 @@ __device__ __forceinline__ float load_logit(const void *row, int64_t i) {
     const uint32_t h = __ldg(static_cast<const uint16_t *>(row) + i);
     x = TYPE == 1 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
   }
-  return tame(x);
+  return tame<TYPE>(x);
 }
 // Elements of a 16-byte vector.
 template <int TYPE>
@@ -123,98 +151,181 @@ __device__ __forceinline__ int lead_of(const void *row) {
   return (int)((uintptr_t)row & 15) / Logit<TYPE>::kSize;
 }
 
-// 2^((x - m) c), c in two parts: a difference is exact or nearly so, and its
-// product keeps what one rounded factor would lose for every element alike.
-__device__ __forceinline__ float weight(float x, float m, float ch, float cl) {
-  const float d = x - m;
-  return exp2_approx(fmaf(d, ch, d * cl));
+// Two fp32 numbers in a 64-bit register, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair64(uint64_t v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The larger elements of two words.
+template <int TYPE>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  if (TYPE == 0) asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  else if (TYPE == 1) asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  else a = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  return a;
+}
+// The word's two elements (fp32: the word twice).
+template <int TYPE>
+__device__ __forceinline__ float2 both(uint32_t w) {
+  if (TYPE == 0) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  if (TYPE == 1) return make_float2(bf16_lo(w), bf16_hi(w));
+  return make_float2(__uint_as_float(w), __uint_as_float(w));
 }
 
 // ---- rows -------------------------------------------------------------------
-// Block (part, row, model): NV vectors a thread, vector i of thread t the part's
-// vector i * threads + t.
+// A warp a unit: (model, row, part), NV vectors a lane, vector i of lane l the part's
+// vector 32 * i + l.  What bounds it is HBM, if the instructions a logit stay few:
+// packed pairs for taming and the maximum, pairs of fp32 for differences, products and
+// sums, one exponential a logit.  Vectors that the row's ends cut are left out there;
+// their up to seven logits are taken one by one.
 template <int TYPE, int NV>
 __global__ void __launch_bounds__(kVerifyThreads)
 verify_rows_kernel(const __grid_constant__ VerifyArgs a) {
   using L = Logit<TYPE>;
   constexpr int N = L::kVec;
-  __shared__ float sm[kVerifyWarps], ss[kVerifyWarps];
-  __shared__ int first;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int part = blockIdx.x, model = blockIdx.z;
-  const int64_t t = blockIdx.y;
+  const int lane = threadIdx.x & 31;
   grid_dep_trigger();
   grid_dep_wait();
+  const int64_t unit = (int64_t)blockIdx.x * kVerifyWarps + (threadIdx.x >> 5);
+  const int part = (int)(unit % a.n_parts);
+  const int64_t at = unit / a.n_parts, t = at < a.T ? at : at - a.T;
+  const int model = at >= a.T;
+  if (at >= (a.draft ? 2 : 1) * a.T) return;
+  int b = -1;
+  if (model) {  // (looked up first: the last rows' are not read)
+    b = sequence_of(a, t);
+    if (b < 0 || t + 1 == a.cu[b + 1]) return;
+  }
   const char *row = static_cast<const char *>(model ? a.draft : a.logits) +
                     t * (model ? a.dstride : a.stride) * L::kSize;
   const int lead = lead_of<TYPE>(row);
   // vector v holds elements v * N - lead .. + N - 1
-  float x[NV][N];
-  const int64_t v0 = (int64_t)part * NV * kVerifyThreads + tid;
+  const int64_t v0 = (int64_t)part * NV * 32 + lane;
   const uint4 *vec = reinterpret_cast<const uint4 *>(row - lead * L::kSize);
+  uint32_t w[NV][4];
+  uint32_t have = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e0 = (v0 + i * kVerifyThreads) * N - lead;
+    const int64_t e0 = (v0 + i * 32) * N - lead;
+    uint4 v = make_uint4(0, 0, 0, 0);
     if (e0 >= 0 && e0 + N <= a.V) {
-      unpack<TYPE>(__ldg(vec + v0 + i * kVerifyThreads), x[i]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        x[i][k] = e0 + k >= 0 && e0 + k < a.V ? load_logit<TYPE>(row, e0 + k) : kMasked;
+      v = __ldg(vec + v0 + i * 32);
+      have |= 1u << i;
     }
+    w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
   }
-  const int b = sequence_of(a, t);
+  if (!model) b = sequence_of(a, t);
   if (b < 0) return;
   const float temperature = temperature_of(a, b);
-  if (model && (temperature == 0.0f || t + 1 == a.cu[b + 1])) return;  // not looked at
-  float m = kMasked;
+  if (model && temperature == 0.0f) return;  // not looked at
+  const Factor c = factor_of(temperature);
+
+  constexpr uint32_t kNone = TYPE == 0 ? 0xfc00fc00u : TYPE == 1 ? 0xff80ff80u : 0xff800000u;
+  uint32_t most = kNone;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
+    if (have >> i & 1) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      x[i][k] = tame(x[i][k]);
-      m = fmaxf(m, x[i][k]);
+      for (int k = 0; k < 4; ++k) {
+        w[i][k] = tame_word<TYPE>(w[i][k]);
+        most = larger<TYPE>(most, w[i][k]);
+      }
     }
-  const double c = factor_of(temperature);
-  const float ch = (float)c, cl = (float)(c - (double)ch);
-  float s = 0.0f;
-  const float mine = m;
-  if (m > kMasked) {
+  const float2 ends = both<TYPE>(most);
+  float m = fmaxf(ends.x, ends.y), s = 0.0f;
+  {
+    const float ref = m > kMasked ? m : 0.0f;
+    const uint64_t nm = pair64(-ref, -ref), chi = pair64(c.hi, c.hi), clo = pair64(c.lo, c.lo);
+    uint64_t s2 = 0;
+    auto add = [&](uint64_t x) {
+      const uint64_t d = add2(x, nm);
+      const float2 e = unpair64(fma2(d, chi, mul2(d, clo)));
+      s2 = add2(s2, pair64(exp2_approx(e.x), exp2_approx(e.y)));
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i)
+      if (have >> i & 1) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) s += weight(x[i][k], m, ch, cl);
+        for (int k = 0; k < 4; ++k) {
+          if (TYPE == 2) {
+            if (k & 1) add(pair64(__uint_as_float(w[i][k - 1]), __uint_as_float(w[i][k])));
+          } else {
+            const float2 x = both<TYPE>(w[i][k]);
+            add(pair64(x.x, x.y));
+          }
+        }
+      }
+    const float2 e = unpair64(s2);
+    s = e.x + e.y;
+  }
+  // the row's ends: what the last vector holds of it, where that is cut, and (by
+  // another lane) what vector 0 does, where that begins before the row
+  const int last = (a.V - 1 + lead) / N;
+  const bool cut = (a.V + lead) % N != 0;
+  int e0 = 0, e1 = 0;
+  if (cut && part == last / (NV * 32) && lane == last % 32)
+    e0 = max(last * N - lead, 0), e1 = a.V;
+  else if (lead > 0 && part == 0 && lane == (last + 1) % 32 && !(cut && last == 0))
+    e1 = min(N - lead, a.V);
+  for (int e = e0; e < e1; ++e) {
+    const float x = load_logit<TYPE>(row, e);
+    if (x > m) {
+      s = s * weight(m, x, c) + 1.0f;
+      m = x;
+    } else if (x > kMasked) {
+      s += weight(x, m, c);
+    }
   }
   float top = m;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) sm[warp] = top;
-  if (tid == 0) first = 0x7fffffff;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kVerifyWarps; ++w) top = fmaxf(top, sm[w]);
-  s = mine > kMasked ? s * weight(mine, top, ch, cl) : 0.0f;
+  s = m > kMasked ? s * weight(m, top, c) : 0.0f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) ss[warp] = s;
-  // the lowest index of the maximum, for greedy rows
-  if (temperature == 0.0f && mine == top && top > kMasked) {
-    int at = 0x7fffffff;
+  int first = 0x7fffffff;
+  if (temperature == 0.0f) {  // the lowest index of the maximum
+    if (m == top && top > kMasked) {
+      for (int e = e1 - 1; e >= e0; --e)
+        if (load_logit<TYPE>(row, e) == top) first = e;
 #pragma unroll
-    for (int i = NV - 1; i >= 0; --i)
+      for (int i = NV - 1; i >= 0; --i)
+        if (have >> i & 1) {
 #pragma unroll
-      for (int k = N - 1; k >= 0; --k)
-        if (x[i][k] == top) at = (int)((v0 + i * kVerifyThreads) * N - lead + k);
-    atomicMin(&first, at);
+          for (int k = 3; k >= 0; --k) {
+            const float2 x = both<TYPE>(w[i][k]);
+            const int e = (int)((v0 + i * 32) * N - lead) + k * (4 / L::kSize);
+            if (TYPE != 2 && x.y == top) first = min(first, e + 1);
+            if (x.x == top) first = min(first, e);
+          }
+        }
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
   }
-  __syncthreads();
-  if (tid == 0) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kVerifyWarps; ++w) sum += ss[w];
+  if (lane == 0)
     a.parts[((int64_t)model * a.T + t) * a.n_parts + part] =
-        make_float4(top, sum, __int_as_float(first), 0.0f);
-  }
+        make_float4(top, s, __int_as_float(first), 0.0f);
 }
 
 // ---- draw -------------------------------------------------------------------
@@ -224,68 +335,88 @@ struct Row {
   float m, s;
   int at;
 };
-__device__ __forceinline__ Row join_row(const VerifyArgs &a, int model, int64_t t, double c) {
+__device__ __forceinline__ Row join_row(const VerifyArgs &a, int model, int64_t t, Factor c) {
   const int lane = threadIdx.x & 31;
   const float4 *p = a.parts + ((int64_t)model * a.T + t) * a.n_parts;
-  const float ch = (float)c, cl = (float)(c - (double)ch);
   Row r = {kMasked, 0.0f, 0x7fffffff};
-  for (int i = lane; i < a.n_parts; i += 32) r.m = fmaxf(r.m, __ldcg(p + i).x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
-  if (r.m == kMasked) return r;
+#pragma unroll 2
   for (int i = lane; i < a.n_parts; i += 32) {
     const float4 v = __ldcg(p + i);
-    if (v.x > kMasked) r.s += v.y * weight(v.x, r.m, ch, cl);
-    if (v.x == r.m) r.at = min(r.at, __float_as_int(v.z));
+    if (v.x > r.m) {
+      r.s = r.s * weight(r.m, v.x, c) + v.y;
+      r.m = v.x;
+      r.at = __float_as_int(v.z);
+    } else if (v.x > kMasked) {
+      r.s += v.y * weight(v.x, r.m, c);
+    }
   }
+  float m = r.m;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
-    r.at = min(r.at, __shfl_xor_sync(0xffffffffu, r.at, o));
-  }
-  return r;
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = r.m > kMasked ? r.s * weight(r.m, m, c) : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int at = __reduce_min_sync(0xffffffffu, r.m == m ? r.at : 0x7fffffff);
+  return {m, s, at};
 }
 
 // Natural logarithm of a token's probability: logit x in a row of maximum m, sum s.
-__device__ __forceinline__ float log_probability(float x, const Row &r, double c) {
-  return (float)(((double)(x - r.m) * c) * 0.6931471805599453) - logf(r.s);
+__device__ __forceinline__ float log_probability(float x, const Row &r, float temperature) {
+  return (x - r.m) / (temperature > 0.0f ? temperature : 1.0f) - logf(r.s);
 }
 
-// u q(c) < p(c): 2^(tp - tq) s_q / s_p against u, the exponent in 64 bits.
+// u q(c) < p(c), as u s_p < 2^(tp - tq) s_q with the exponent in two parts.
 __device__ __forceinline__ bool stays(float u, float x, const Row &p, float y, const Row &q,
-                                      bool model, double c) {
+                                      bool model, Factor c) {
   if (!(x > kMasked)) return false;  // p(c) = 0
-  double t = (double)(x - p.m) * c;
-  float sq = 1.0f;
-  if (model) {
-    if (!(y > kMasked)) return true;  // q(c) = 0 < p(c)
-    t -= (double)(y - q.m) * c;
-    sq = q.s;
-  }
-  t = fmin(fmax(t, -1000.0), 1000.0);
-  const double k = rint(t);
-  const float f = exp2f((float)(t - k));
-  return (double)u * (double)p.s < ldexp((double)(f * sq), (int)k);
+  if (model && !(y > kMasked)) return true;  // q(c) = 0 < p(c)
+  if (u == 0.0f) return true;
+  const float dp = x - p.m, dq = model ? y - q.m : 0.0f;
+  const float hp = dp * c.hi, hq = dq * c.hi;
+  const float lp = fmaf(dp, c.hi, -hp) + dp * c.lo, lq = fmaf(dq, c.hi, -hq) + dq * c.lo;
+  // hp - hq and what its rounding loses
+  const float h = hp - hq, back = h - hp, lost = (hp - (h - back)) + (-hq - back);
+  // a clamped exponent decides: the sums lie in [1, 2^24]
+  const float k = rintf(fminf(fmaxf(h, -400.0f), 400.0f));
+  const float f = exp2f(fabsf(h) < 400.0f ? (h - k) + (lost + (lp - lq)) : 0.0f);
+  // both sides times 2^100, so that small numbers stay normal ones
+  return u * 0x1p100f * p.s < ldexpf(f * (model ? q.s : 1.0f), (int)k + 100);
 }
 
-__device__ __forceinline__ unsigned long long key_of(float score, int64_t i) {
-  return score > 0.0f ? (unsigned long long)__float_as_uint(score) << 32 | (0xffffffffu - (uint32_t)i)
-                      : 0ull;
-}
-__device__ __forceinline__ unsigned long long max64(unsigned long long a, unsigned long long b) {
-  return a > b ? a : b;
+// The best of a thread's candidates so far: i only grows, so of equal scores the
+// lowest index stays.
+struct Best {
+  float score;
+  uint32_t at;
+  __device__ __forceinline__ void take(float x, uint32_t i) {
+    if (x > score) score = x, at = i;
+  }
+  __device__ __forceinline__ unsigned long long key() const {
+    return score > 0.0f ? (unsigned long long)__float_as_uint(score) << 32 | (0xffffffffu - at)
+                        : 0ull;
+  }
+};
+// 1 / e of the race: e below 2^-126 counts as that, NaN stays.
+__device__ __forceinline__ float rate(float e) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00800000;\n rcp.approx.ftz.f32 %0, %0;" : "=&f"(r) : "f"(e));
+  return r;
 }
 
 // Block (share, sequence).
+constexpr int kSaved = 64;  // rows whose joined parts a block keeps
 template <int TYPE>
 __global__ void __launch_bounds__(kVerifyThreads)
 verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   using L = Logit<TYPE>;
-  __shared__ int stop, last;
-  __shared__ Row row_p, row_q;  // of the row that is drawn from
-  __shared__ unsigned long long best[2][kVerifyWarps];
+  constexpr int N = L::kVec;
+  __shared__ int stop, last, next;
+  __shared__ Row saved[2][kSaved], row_p, row_q;
+  __shared__ unsigned long long best[kVerifyWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y, share = blockIdx.x;
+  if (tid == 0) stop = 0x7fffffff;
+  __syncthreads();
   grid_dep_trigger();
   grid_dep_wait();
   const int r0 = a.cu[b], r1 = a.cu[b + 1], n = r1 - r0;
@@ -299,132 +430,157 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   }
   const float temperature = temperature_of(a, b);
   const bool greedy = temperature == 0.0f, model = a.draft != nullptr && !greedy;
-  const double c = factor_of(temperature);
+  const Factor c = factor_of(temperature);
+  // the share's tokens
+  const int per = ((a.V + a.splits - 1) / a.splits + 7) & ~7;
+  const int i0 = min(share * per, a.V), i1 = min(i0 + per, a.V);
+  const float *er = a.noise + b * a.nstride;
+  if (!greedy)  // its noise comes into L2 meanwhile
+    for (int i = i0 + tid * 32; i < i1; i += kVerifyThreads * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(er + i));
   auto row_of = [&](int which, int64_t t) {
     return static_cast<const char *>(which ? a.draft : a.logits) +
            t * (which ? a.dstride : a.stride) * L::kSize;
   };
-  if (tid == 0) stop = n - 1;
-  __syncthreads();
-  // ---- the drafts that stay; the block of share 0 writes their outputs below
-  for (int i = warp; i < n - 1; i += kVerifyWarps) {
+  // ---- the drafts that stay
+  for (int i = warp; i < n; i += kVerifyWarps) {
     const int64_t t = r0 + i;
-    const int token = a.tokens[t + 1];
+    const bool drafted = i < n - 1;
+    const int token = drafted ? a.tokens[t + 1] : -1;
+    const bool valid = token >= 0 && token < a.V;
+    const bool test = valid && !greedy;
+    const float x = test ? load_logit<TYPE>(row_of(0, t), token) : 0.0f;
+    const float y = test && model ? load_logit<TYPE>(row_of(1, t), token) : 0.0f;
+    const float u = test ? a.uniform[t] : 0.0f;
     const Row p = join_row(a, 0, t, c);
-    bool ok = token >= 0 && token < a.V;
-    if (!ok && share == 0 && lane == 0) verify_error(a, KVQ_EINVAL);
-    if (ok && greedy) {
-      ok = p.at == token;
-    } else if (ok) {
-      Row q = {0.0f, 1.0f, 0};
-      float y = 0.0f;
-      if (model) {
-        q = join_row(a, 1, t, c);
-        y = load_logit<TYPE>(row_of(1, t), token);
-      }
-      ok = stays(a.uniform[t], load_logit<TYPE>(row_of(0, t), token), p, y, q, model, c);
+    Row q = {kMasked, 0.0f, 0};
+    if (drafted && model) q = join_row(a, 1, t, c);
+    if (lane == 0) {
+      if (i < kSaved) saved[0][i] = p, saved[1][i] = q;
+      if (drafted && !valid && share == 0) verify_error(a, KVQ_EINVAL);
+      const bool ok = valid && (greedy ? p.at == token : stays(u, x, p, y, q, model, c));
+      if (!ok) atomicMin(&stop, i);  // (the last row is the end anyway)
     }
-    if (!ok && lane == 0) atomicMin(&stop, i);
   }
   __syncthreads();
   const int kept = stop;
   const int64_t t = r0 + kept;
   const bool refused = kept < n - 1;
-  if (warp == 0) {
-    const Row p = join_row(a, 0, t, c);
-    if (lane == 0) row_p = p;
-  } else if (warp == 1 && refused && model) {
-    const Row q = join_row(a, 1, t, c);
-    if (lane == 0) row_q = q;
+  if (kept >= kSaved && warp < 2) {
+    const Row r = warp == 0 || (refused && model) ? join_row(a, warp, t, c)
+                                                  : Row{kMasked, 0.0f, 0};
+    if (lane == 0) *(warp == 0 ? &row_p : &row_q) = r;
   }
-  __syncthreads();
-  const Row p = row_p;
-  if (greedy) {
-    if (share != 0) return;
-  } else {
-    // ---- the race over this share of the vocabulary
-    const bool rest = refused && model;
-    const int gone = refused && !model ? a.tokens[t + 1] : -1;  // all of q
-    const float ch = (float)c, cl = (float)(c - (double)ch);
-    const Row q = rest ? row_q : Row{0.0f, 1.0f, 0};
-    // (a draft row without a finite logit takes nothing off)
+  if (kept >= kSaved) __syncthreads();
+  const Row p = kept < kSaved ? saved[0][kept] : row_p;
+  if (greedy && share != 0) return;
+  // ---- the race over tokens [from, to) of the row
+  auto race = [&](int from, int to, bool rest) {
+    Best win = {0.0f, 0};
+    const Row q = kept < kSaved ? saved[1][kept] : row_q;
+    const int gone = refused && !model && rest ? a.tokens[t + 1] : -1;  // all of q
+    rest = rest && refused && model;
+    // (a draft row without a logit takes nothing off)
     const float ip = 1.0f / p.s, iq = rest && q.s > 0.0f ? 1.0f / q.s : 0.0f;
     const char *xr = row_of(0, t), *yr = rest ? row_of(1, t) : xr;
-    const float *er = a.noise + b * a.nstride;
-    unsigned long long k0 = 0, k1 = 0;  // by what is left of p; by p
-    auto race = [&](int64_t i, float x, float y, float e) {
+    auto one = [&](int i, float x, float y, float e) {
       // (products rounded by themselves: equal p and q leave exactly nothing)
-      const float wp = __fmul_rn(weight(x, p.m, ch, cl), ip);
-      const float r = 1.0f / fmaxf(e, 1.1754944e-38f);
-      float w = wp;
-      if (rest) w = __fsub_rn(wp, __fmul_rn(weight(y, q.m, ch, cl), iq));
+      float w = __fmul_rn(weight(x, p.m, c), ip);
+      if (rest) w = __fsub_rn(w, __fmul_rn(weight(y, q.m, c), iq));
       if (i == gone) w = 0.0f;
-      if (e == e) k0 = max64(k0, key_of(w * r, i)), k1 = max64(k1, key_of(wp * r, i));
+      win.take(w * rate(e), (uint32_t)i);
     };
-    if (p.m > kMasked) {
-      const int64_t per = (a.V + a.splits - 1) / a.splits;
-      const int64_t i0 = share * per, i1 = min(i0 + per, (int64_t)a.V);
-      for (int64_t i = i0 + tid; i < i1; i += kVerifyThreads)
-        race(i, load_logit<TYPE>(xr, i), rest ? load_logit<TYPE>(yr, i) : 0.0f, __ldg(er + i));
+    auto single = [&](int i) {
+      one(i, load_logit<TYPE>(xr, i), rest ? load_logit<TYPE>(yr, i) : 0.0f, __ldg(er + i));
+    };
+    // 16-byte vectors where the rows and the noise agree on where those begin
+    const int lead = lead_of<TYPE>(xr), skip = (N - lead) % N;
+    if (lead_of<TYPE>(yr) == lead && (((uintptr_t)(er + from + skip)) & 15) == 0) {
+      // (from is a multiple of eight)
+      const int v0 = min(from + skip, to), v1 = v0 + (to - v0) / N * N;
+      if (tid < v0 - from) single(from + tid);
+      for (int i = v0 + tid * N; i < v1; i += kVerifyThreads * N) {
+        float x[N], y[N], e[N];
+        unpack<TYPE>(__ldg(reinterpret_cast<const uint4 *>(xr + (int64_t)i * L::kSize)), x);
+        if (rest) unpack<TYPE>(__ldg(reinterpret_cast<const uint4 *>(yr + (int64_t)i * L::kSize)), y);
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+          const float4 f = __ldg(reinterpret_cast<const float4 *>(er + i + k));
+          e[k] = f.x, e[k + 1] = f.y, e[k + 2] = f.z, e[k + 3] = f.w;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) one(i + k, tame<TYPE>(x[k]), rest ? tame<TYPE>(y[k]) : 0.0f, e[k]);
+      }
+      if (tid < to - v1) single(v1 + tid);
+    } else {
+#pragma unroll 4
+      for (int i = from + tid; i < to; i += kVerifyThreads) single(i);
     }
+    unsigned long long key = win.key();
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      k0 = max64(k0, __shfl_xor_sync(0xffffffffu, k0, o));
-      k1 = max64(k1, __shfl_xor_sync(0xffffffffu, k1, o));
+      const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
+      key = other > key ? other : key;
     }
-    if (lane == 0) best[0][warp] = k0, best[1][warp] = k1;
+    if (lane == 0) best[warp] = key;
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0)
 #pragma unroll
-      for (int w = 1; w < kVerifyWarps; ++w) k0 = max64(k0, best[0][w]), k1 = max64(k1, best[1][w]);
-      if (k0) atomicMax(&a.keys[2 * b], k0);
-      if (k1) atomicMax(&a.keys[2 * b + 1], k1);
+      for (int w = 1; w < kVerifyWarps; ++w) key = best[w] > key ? best[w] : key;
+    return key;  // of thread 0: the block's
+  };
+  int token = greedy && p.m > kMasked ? p.at : -1;
+  if (!greedy) {
+    unsigned long long key = p.m > kMasked ? race(i0, i1, true) : 0;
+    if (tid == 0) {
+      if (key) atomicMax(&a.keys[b], key);
       __threadfence();
       last = atomicAdd(&a.tickets[b], 1) == a.splits - 1;
     }
     __syncthreads();
     if (!last) return;
-  }
-  // ---- outputs
-  __shared__ int next;
-  if (tid == 0) {
-    int token = greedy && p.m > kMasked ? p.at : -1;
-    if (!greedy) {
+    __shared__ unsigned long long won;
+    if (tid == 0) {
       __threadfence();
-      const unsigned long long k0 = atomicExch(&a.keys[2 * b], 0ull);
-      const unsigned long long k1 = atomicExch(&a.keys[2 * b + 1], 0ull);
-      const unsigned long long k = k0 ? k0 : k1;
-      if (k) token = (int)(0xffffffffu - (uint32_t)k);
+      won = atomicExch(&a.keys[b], 0ull);
       a.tickets[b] = 0;
     }
+    __syncthreads();
+    key = won;
+    // nothing was left of p (or only where the noise is NaN or infinite): p itself
+    if (key == 0 && refused && p.m > kMasked) key = race(0, a.V, false);
+    if (key) token = (int)(0xffffffffu - (uint32_t)key);
+  }
+  // ---- outputs
+  if (tid == 0) {
     next = token;
     a.accepted[b] = kept;
     a.dropped[b] = n - 1 - kept;
   }
   __syncthreads();
   for (int i = warp; i < n; i += kVerifyWarps) {
-    const int token = i < kept ? a.tokens[r0 + i + 1] : i == kept ? next : -1;
+    const int out = i < kept ? a.tokens[r0 + i + 1] : i == kept ? next : -1;
     float lp = 0.0f;
-    if (token >= 0) {
-      const Row r = i == kept ? p : join_row(a, 0, r0 + i, c);
-      lp = log_probability(load_logit<TYPE>(row_of(0, r0 + i), token), r, c);
+    if (out >= 0) {
+      const Row r = i == kept ? p : i < kSaved ? saved[0][i] : join_row(a, 0, r0 + i, c);
+      lp = log_probability(load_logit<TYPE>(row_of(0, r0 + i), out), r, temperature);
     }
     if (lane == 0) {
-      a.out[r0 + i] = token;
+      a.out[r0 + i] = out;
       a.logprobs[r0 + i] = lp;
     }
   }
 }
 
-// Vectors a thread of the rows' kernel.
-constexpr int kVectors = 4;
+// Vectors a lane of the rows' kernel.
+constexpr int kVectors = 8;
 int parts_of(int64_t vocab, int type) {
-  const int64_t per = (int64_t)kVectors * kVerifyThreads * (type == 2 ? 4 : 8);
+  const int64_t per = (int64_t)kVectors * 32 * (type == 2 ? 4 : 8);
   return (int)((vocab + (type == 2 ? 3 : 7) + per - 1) / per);
 }
 
 // What must stay zero lies in front, whatever the call's sizes.
-constexpr size_t kTicketsAt = (size_t)kMaxSeqs * 16, kPartsAt = kTicketsAt + (size_t)kMaxSeqs * 4;
+constexpr size_t kTicketsAt = (size_t)kMaxSeqs * 8, kPartsAt = kTicketsAt + (size_t)kMaxSeqs * 4;
 size_t verify_bytes(int64_t T, int64_t V, int type) {
   return kPartsAt + (size_t)2 * T * parts_of(V, type) * sizeof(float4);
 }
@@ -433,7 +589,8 @@ template <int TYPE>
 cudaError_t verify_as(const VerifyArgs &a, cudaStream_t st, int *launches) {
   *launches = 0;
   if (a.T > 0) {
-    const dim3 grid((unsigned)a.n_parts, (unsigned)a.T, a.draft ? 2 : 1);
+    const int64_t units = (a.draft ? 2 : 1) * a.T * a.n_parts;
+    const unsigned grid = (unsigned)((units + kVerifyWarps - 1) / kVerifyWarps);
     const cudaError_t e = launch_dependent(verify_rows_kernel<TYPE, kVectors>, grid,
                                            kVerifyThreads, 0, st, true, a);
     if (e != cudaSuccess) return e;
@@ -520,9 +677,10 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
   a.keys = reinterpret_cast<unsigned long long *>(w);
   a.tickets = reinterpret_cast<int *>(w + kTicketsAt);
   a.parts = reinterpret_cast<float4 *>(w + kPartsAt);
-  // shares of 2048 tokens, fewer where the sequences alone fill the GPU
-  int64_t splits = (V + 2047) / 2048;
-  const int64_t most = std::max<int64_t>(1, (int64_t)num_sms_cached() * 16 / a.B);
+  // shares of 2048 tokens (a vector a thread), or larger ones, since every block of a
+  // sequence decides about its drafts by itself
+  const int64_t splits = (V + 2047) / 2048;
+  const int64_t most = std::max<int64_t>(1, (int64_t)num_sms_cached() * 4 / a.B);
   a.splits = temperature ? (int)std::min(splits, most) : 1;
   int n = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

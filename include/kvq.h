@@ -706,9 +706,9 @@ int kvq_verify_workspace_bytes(const kvq_draft_batch *batch, size_t *bytes);
  *     for -1.
  *   accepted, dropped [n_seqs]: drafts that stayed, and the others: what
  *     kvq_pages_drop takes back, since the cache holds the rows' tokens.
- * Masked: a logit of -infinity, NaN or at most -2^126 has probability 0; logits
- * beyond 2^126 count as 2^126.  A row with nothing else has no next token: -1.
- * e_i below 2^-126 counts as that, NaN takes i out.  T is held to 2^-25..2^100.
+ * Masked: a logit of -infinity or NaN has probability 0; +infinity counts as the
+ * type's largest number.  A row of masked logits has no next token: -1.
+ * e_i below 2^-126 counts as that, NaN takes i out.  T is held to 2^-100..2^100.
  * A draft outside [0, vocab) is refused and gives KVQ_EINVAL in the status word;
  * so do rows of a sequence out of order or behind n_tokens, whose outputs are left
  * alone but for 0 accepted, 0 dropped.  A sequence without rows gets those too.

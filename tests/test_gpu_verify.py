@@ -55,7 +55,7 @@ def run_and_check(a, **kw):
     got = call(v, **a)
     assert v.device_status() == 0
     check(got, expected(**a), a["cu"].tolist(), a["tokens"].cpu().numpy(), **kw)
-    assert not v.ws[:2048 * 20].any()      # what has to be zero is zero again
+    assert not v.ws[:2048 * 12].any()      # what has to be zero is zero again
     return v, got
 
 

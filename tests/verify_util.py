@@ -19,7 +19,7 @@ FLOOR = 2.0 ** -126
 def softmax(x, T):
     """Probabilities and their logarithms, masked logits at 0; None: nothing left."""
     x = np.where(np.isnan(x), -np.inf, x)
-    x = np.where(x <= -2.0 ** 126, -np.inf, np.minimum(x, 2.0 ** 126))
+    x = np.minimum(x, 3e38)
     if not (x > -np.inf).any():
         return None
     t = (x - x.max()) / T
