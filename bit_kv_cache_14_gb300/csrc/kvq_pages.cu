@@ -102,9 +102,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sums, int64_t 
 
 // ---- reserve ------------------------------------------------------------------
 // One block: a sequence (or two) a thread counts the pages it needs, running sums
-// number them, and the warps walk the free map a bit a lane and hand the r-th free
-// page to the sequence whose numbers hold r.
-__global__ void __launch_bounds__(kReserveThreads)
+// number them, and the warps walk the free map a bit a lane (neighbouring words in
+// different warps) and hand the r-th free page to the sequence whose numbers hold r.
+__global__ void __launch_bounds__(kReserveThreads, 1)
 pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *copies,
                      int32_t *cu_call) {
   constexpr int kPer = kMaxSeqs / kReserveThreads;
@@ -113,7 +113,9 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
   __shared__ int entry[kMaxSeqs];       // its table entry
   __shared__ int from[kMaxSeqs];        // the page it copies, or -1
   __shared__ int pair[kMaxSeqs];        // ... and that copy's place in the list
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ uint32_t map_bits[kReserveThreads];  // a stretch of the map, and the number
+  __shared__ int map_before[kReserveThreads];     // of each word's first free page
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_trigger();
   grid_dep_wait();
   const int per = t.B > kReserveThreads ? kPer : 1;
@@ -231,14 +233,13 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
     if (!__syncthreads_or(bits != 0)) continue;
     const int64_t count = __popc(bits);
     int64_t found = 0;
-    const int before = (int)(done + block_scan<kReserveWarps>(count, sums, found) - count);
-    // a word at a time, a lane a bit
-    unsigned busy = __ballot_sync(kAll, bits != 0 && before < n);
-    while (busy) {
-      const int l = __ffs(busy) - 1;
-      busy &= busy - 1;
-      const uint32_t word = __shfl_sync(kAll, bits, l);
-      const int r = __shfl_sync(kAll, before, l) + __popc(word & ((1u << lane) - 1));
+    map_bits[tid] = bits;
+    map_before[tid] = (int)(done + block_scan<kReserveWarps>(count, sums, found) - count);
+    __syncthreads();
+    // a warp takes every 32nd word, a lane a bit of it
+    for (int j = warp; j < kReserveThreads && map_before[j] < n; j += kReserveWarps) {
+      const uint32_t word = map_bits[j];
+      const int r = map_before[j] + __popc(word & ((1u << lane) - 1));
       const bool take = (word >> lane & 1) && r < n;
       if (take) {
         int lo = 0, hi = t.B;  // the last b with first[b] <= r that needs a page
@@ -246,13 +247,13 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
           const int mid = (lo + hi) >> 1;
           if (first[mid] <= r) lo = mid; else hi = mid;
         }
-        const int page = (w0 + (tid & ~31) + l) * 32 + lane;
+        const int page = (w0 + j) * 32 + lane;
         t.table[lo * t.width + entry[lo] + (r - first[lo])] = page;
         t.refs[page] = 1;
         if (from[lo] >= 0 && r == first[lo]) copies[pair[lo]] = make_int2(from[lo], page);
       }
       const unsigned gone = __ballot_sync(kAll, take);
-      if (lane == l) t.map[w] = bits & ~gone;
+      if (lane == 0 && gone) t.map[w0 + j] = word & ~gone;
     }
     done += found;
     hint = w0;
@@ -391,12 +392,12 @@ pages_map_kernel(const __grid_constant__ Table t) {
   grid_dep_wait();
   const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
   const unsigned bits = __ballot_sync(kAll, i < t.n_pages && t.refs[i] == 0);
-  if ((threadIdx.x & 31) == 0 && i < (int64_t)t.words * 32) {
-    t.map[i >> 5] = bits;
-    if (bits) {
-      atomicAdd(&t.head->free, __popc(bits));
-      atomicMin(&t.head->hint, (int)(i >> 5));
-    }
+  if ((threadIdx.x & 31) == 0 && i < (int64_t)t.words * 32) t.map[i >> 5] = bits;
+  // one addition a block: of single ones the head's word is the bound
+  const int n = __syncthreads_count(i < t.n_pages && (bits >> (threadIdx.x & 31) & 1));
+  if (threadIdx.x == 0 && n) {
+    atomicAdd(&t.head->free, n);
+    atomicMin(&t.head->hint, (int)(i >> 5));
   }
 }
 

@@ -16,7 +16,7 @@
 #include <algorithm>
 
 #include "kvq_paged.cuh"
-#include "kvq_tc_common.cuh"
+#include "kvq_umma.cuh"
 
 namespace kvq {
 namespace {
@@ -39,7 +39,8 @@ struct VerifyArgs {
   int *tickets;              // [B], zero between calls
   float4 *parts;             // [2][T][parts]: maximum, sum, lowest index of the maximum
   int64_t T;
-  int B, V, n_parts, splits;
+  int B, V, splits;
+  int row_pieces, pieces, n_parts;  // pieces of a row, of a part; parts of a row
 };
 
 __device__ __forceinline__ void verify_error(const VerifyArgs &a, int code) {
@@ -151,33 +152,6 @@ __device__ __forceinline__ int lead_of(const void *row) {
   return (int)((uintptr_t)row & 15) / Logit<TYPE>::kSize;
 }
 
-// Two fp32 numbers in a 64-bit register, and arithmetic on both at once.
-__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpair64(uint64_t v) {
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 // The larger elements of two words.
 template <int TYPE>
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
@@ -195,69 +169,79 @@ __device__ __forceinline__ float2 both(uint32_t w) {
 }
 
 // ---- rows -------------------------------------------------------------------
-// A warp a unit: (model, row, part), NV vectors a lane, vector i of lane l the part's
-// vector 32 * i + l.  What bounds it is HBM, if the instructions a logit stay few:
-// packed pairs for taming and the maximum, pairs of fp32 for differences, products and
-// sums, one exponential a logit.  Vectors that the row's ends cut are left out there;
-// their up to seven logits are taken one by one.
-template <int TYPE, int NV>
-__global__ void __launch_bounds__(kVerifyThreads)
+// A warp a unit: `pieces` pieces of a row of one model, a piece being kVectors 16-byte
+// vectors a lane, vector i of lane l its vector 32 * i + l.  What bounds it is HBM, if
+// the instructions a logit stay few: packed pairs for taming and the maximum, pairs of
+// fp32 for differences, products and sums, one exponential a logit.  Vectors that the
+// row's ends cut are left out there; their up to seven logits are taken one by one.
+constexpr int kVectors = 8;
+template <int TYPE>
+__global__ void __launch_bounds__(kVerifyThreads, 4)
 verify_rows_kernel(const __grid_constant__ VerifyArgs a) {
   using L = Logit<TYPE>;
-  constexpr int N = L::kVec;
+  constexpr int N = L::kVec, kPiece = kVectors * 32;  // vectors
   const int lane = threadIdx.x & 31;
-  grid_dep_trigger();
+  // (in this order: where the draw's blocks start, everything before the call is done)
   grid_dep_wait();
-  const int64_t unit = (int64_t)blockIdx.x * kVerifyWarps + (threadIdx.x >> 5);
-  const int part = (int)(unit % a.n_parts);
-  const int64_t at = unit / a.n_parts, t = at < a.T ? at : at - a.T;
-  const int model = at >= a.T;
-  if (at >= (a.draft ? 2 : 1) * a.T) return;
-  int b = -1;
-  if (model) {  // (looked up first: the last rows' are not read)
-    b = sequence_of(a, t);
-    if (b < 0 || t + 1 == a.cu[b + 1]) return;
-  }
+  grid_dep_trigger();
+  const uint32_t unit = blockIdx.x * kVerifyWarps + (threadIdx.x >> 5);
+  const uint32_t line = unit / (uint32_t)a.n_parts;
+  const int part = (int)(unit - line * (uint32_t)a.n_parts);
+  const bool model = line >= a.T;
+  const int64_t t = model ? line - a.T : line;
+  if (line >= (a.draft ? 2 : 1) * a.T) return;
+  const int b = sequence_of(a, t);
+  if (b < 0) return;
+  const float temperature = temperature_of(a, b);
+  // a draft row is looked at where there is a draft to sample against
+  if (model && (temperature == 0.0f || t + 1 == a.cu[b + 1])) return;
+  const Factor c = factor_of(temperature);
+  const uint64_t chi = pair64(c.hi, c.hi), clo = pair64(c.lo, c.lo);
   const char *row = static_cast<const char *>(model ? a.draft : a.logits) +
                     t * (model ? a.dstride : a.stride) * L::kSize;
   const int lead = lead_of<TYPE>(row);
   // vector v holds elements v * N - lead .. + N - 1
-  const int64_t v0 = (int64_t)part * NV * 32 + lane;
   const uint4 *vec = reinterpret_cast<const uint4 *>(row - lead * L::kSize);
-  uint32_t w[NV][4];
-  uint32_t have = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t e0 = (v0 + i * 32) * N - lead;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (e0 >= 0 && e0 + N <= a.V) {
-      v = __ldg(vec + v0 + i * 32);
-      have |= 1u << i;
-    }
-    w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
-  }
-  if (!model) b = sequence_of(a, t);
-  if (b < 0) return;
-  const float temperature = temperature_of(a, b);
-  if (model && temperature == 0.0f) return;  // not looked at
-  const Factor c = factor_of(temperature);
-
   constexpr uint32_t kNone = TYPE == 0 ? 0xfc00fc00u : TYPE == 1 ? 0xff80ff80u : 0xff800000u;
-  uint32_t most = kNone;
+
+  float m = kMasked, s = 0.0f;
+  int first = 0x7fffffff;  // greedy rows: the lane's lowest index of its maximum
+  auto take = [&](int v0, auto whole) {
+    uint32_t w[kVectors][4];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (have >> i & 1) {
+    for (int i = 0; i < kVectors; ++i) {
+      const int e0 = (v0 + i * 32) * N - lead;
+      if (decltype(whole)::value || (e0 >= 0 && e0 + N <= a.V)) {
+        const uint4 v = __ldg(vec + v0 + i * 32);
+        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+      } else {
+        w[i][0] = w[i][1] = w[i][2] = w[i][3] = kNone;
+      }
+    }
+    uint32_t most = kNone;
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         w[i][k] = tame_word<TYPE>(w[i][k]);
         most = larger<TYPE>(most, w[i][k]);
       }
+    const float2 ends = both<TYPE>(most);
+    const float top = fmaxf(m, fmaxf(ends.x, ends.y));
+    if (temperature == 0.0f && top > m) {
+      first = 0x7fffffff;
+#pragma unroll
+      for (int i = kVectors - 1; i >= 0; --i)
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const float2 x = both<TYPE>(w[i][k]);
+          const int e = (v0 + i * 32) * N - lead + k * (4 / L::kSize);
+          if (TYPE != 2 && x.y == top) first = e + 1;
+          if (x.x == top) first = e;
+        }
     }
-  const float2 ends = both<TYPE>(most);
-  float m = fmaxf(ends.x, ends.y), s = 0.0f;
-  {
-    const float ref = m > kMasked ? m : 0.0f;
-    const uint64_t nm = pair64(-ref, -ref), chi = pair64(c.hi, c.hi), clo = pair64(c.lo, c.lo);
+    const float ref = top > kMasked ? top : 0.0f;
+    const uint64_t nm = pair64(-ref, -ref);
     uint64_t s2 = 0;
     auto add = [&](uint64_t x) {
       const uint64_t d = add2(x, nm);
@@ -265,27 +249,34 @@ verify_rows_kernel(const __grid_constant__ VerifyArgs a) {
       s2 = add2(s2, pair64(exp2_approx(e.x), exp2_approx(e.y)));
     };
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (have >> i & 1) {
+    for (int i = 0; i < kVectors; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (TYPE == 2) {
-            if (k & 1) add(pair64(__uint_as_float(w[i][k - 1]), __uint_as_float(w[i][k])));
-          } else {
-            const float2 x = both<TYPE>(w[i][k]);
-            add(pair64(x.x, x.y));
-          }
+      for (int k = 0; k < 4; ++k) {
+        if (TYPE == 2) {
+          if (k & 1) add(pair64(__uint_as_float(w[i][k - 1]), __uint_as_float(w[i][k])));
+        } else {
+          const float2 x = both<TYPE>(w[i][k]);
+          add(pair64(x.x, x.y));
         }
       }
     const float2 e = unpair64(s2);
-    s = e.x + e.y;
+    s = (m > kMasked ? s * weight(m, top, c) : 0.0f) + (e.x + e.y);
+    m = top;
+  };
+  const int p1 = min((part + 1) * a.pieces, a.row_pieces);
+  for (int piece = part * a.pieces; piece < p1; ++piece) {
+    const int v0 = piece * kPiece;
+    if (v0 * N >= lead && (v0 + kPiece) * N - lead <= a.V)
+      take(v0 + lane, std::true_type());
+    else
+      take(v0 + lane, std::false_type());
   }
   // the row's ends: what the last vector holds of it, where that is cut, and (by
   // another lane) what vector 0 does, where that begins before the row
   const int last = (a.V - 1 + lead) / N;
   const bool cut = (a.V + lead) % N != 0;
   int e0 = 0, e1 = 0;
-  if (cut && part == last / (NV * 32) && lane == last % 32)
+  if (cut && part == last / kPiece / a.pieces && lane == last % 32)
     e0 = max(last * N - lead, 0), e1 = a.V;
   else if (lead > 0 && part == 0 && lane == (last + 1) % 32 && !(cut && last == 0))
     e1 = min(N - lead, a.V);
@@ -294,8 +285,10 @@ verify_rows_kernel(const __grid_constant__ VerifyArgs a) {
     if (x > m) {
       s = s * weight(m, x, c) + 1.0f;
       m = x;
+      first = e;
     } else if (x > kMasked) {
       s += weight(x, m, c);
+      if (x == m) first = min(first, e);
     }
   }
   float top = m;
@@ -304,25 +297,7 @@ verify_rows_kernel(const __grid_constant__ VerifyArgs a) {
   s = m > kMasked ? s * weight(m, top, c) : 0.0f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  int first = 0x7fffffff;
-  if (temperature == 0.0f) {  // the lowest index of the maximum
-    if (m == top && top > kMasked) {
-      for (int e = e1 - 1; e >= e0; --e)
-        if (load_logit<TYPE>(row, e) == top) first = e;
-#pragma unroll
-      for (int i = NV - 1; i >= 0; --i)
-        if (have >> i & 1) {
-#pragma unroll
-          for (int k = 3; k >= 0; --k) {
-            const float2 x = both<TYPE>(w[i][k]);
-            const int e = (int)((v0 + i * 32) * N - lead) + k * (4 / L::kSize);
-            if (TYPE != 2 && x.y == top) first = min(first, e + 1);
-            if (x.x == top) first = min(first, e);
-          }
-        }
-    }
-    first = __reduce_min_sync(0xffffffffu, first);
-  }
+  first = __reduce_min_sync(0xffffffffu, m == top ? first : 0x7fffffff);
   if (lane == 0)
     a.parts[((int64_t)model * a.T + t) * a.n_parts + part] =
         make_float4(top, s, __int_as_float(first), 0.0f);
@@ -383,19 +358,6 @@ __device__ __forceinline__ bool stays(float u, float x, const Row &p, float y, c
   return u * 0x1p100f * p.s < ldexpf(f * (model ? q.s : 1.0f), (int)k + 100);
 }
 
-// The best of a thread's candidates so far: i only grows, so of equal scores the
-// lowest index stays.
-struct Best {
-  float score;
-  uint32_t at;
-  __device__ __forceinline__ void take(float x, uint32_t i) {
-    if (x > score) score = x, at = i;
-  }
-  __device__ __forceinline__ unsigned long long key() const {
-    return score > 0.0f ? (unsigned long long)__float_as_uint(score) << 32 | (0xffffffffu - at)
-                        : 0ull;
-  }
-};
 // 1 / e of the race: e below 2^-126 counts as that, NaN stays.
 __device__ __forceinline__ float rate(float e) {
   float r;
@@ -418,9 +380,11 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   if (tid == 0) stop = 0x7fffffff;
   __syncthreads();
   grid_dep_trigger();
-  grid_dep_wait();
+  // Until the wait only the call's inputs are looked at (the rows' kernel passes its
+  // own wait before this one starts), and nothing is written.
   const int r0 = a.cu[b], r1 = a.cu[b + 1], n = r1 - r0;
   if (bad_range(a, r0, r1) || n == 0) {
+    grid_dep_wait();
     if (share == 0 && tid == 0) {
       if (n != 0 || bad_range(a, r0, r1)) verify_error(a, KVQ_EINVAL);
       a.accepted[b] = 0;
@@ -442,7 +406,8 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
     return static_cast<const char *>(which ? a.draft : a.logits) +
            t * (which ? a.dstride : a.stride) * L::kSize;
   };
-  // ---- the drafts that stay
+  // ---- the drafts that stay, a warp a draft
+  bool waited = false;
   for (int i = warp; i < n; i += kVerifyWarps) {
     const int64_t t = r0 + i;
     const bool drafted = i < n - 1;
@@ -452,6 +417,8 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
     const float x = test ? load_logit<TYPE>(row_of(0, t), token) : 0.0f;
     const float y = test && model ? load_logit<TYPE>(row_of(1, t), token) : 0.0f;
     const float u = test ? a.uniform[t] : 0.0f;
+    if (!waited) grid_dep_wait();
+    waited = true;
     const Row p = join_row(a, 0, t, c);
     Row q = {kMasked, 0.0f, 0};
     if (drafted && model) q = join_row(a, 1, t, c);
@@ -462,6 +429,7 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
       if (!ok) atomicMin(&stop, i);  // (the last row is the end anyway)
     }
   }
+  if (!waited) grid_dep_wait();
   __syncthreads();
   const int kept = stop;
   const int64_t t = r0 + kept;
@@ -474,24 +442,22 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   if (kept >= kSaved) __syncthreads();
   const Row p = kept < kSaved ? saved[0][kept] : row_p;
   if (greedy && share != 0) return;
-  // ---- the race over tokens [from, to) of the row
+  // ---- the race over tokens [from, to) of the row.  Scores are taken times the sum
+  // of p, so what is left of p is w_x - w_y s_p / s_q (equal rows leave exactly
+  // nothing).  A thread's i only grows: of equal scores its lowest index stays.
   auto race = [&](int from, int to, bool rest) {
-    Best win = {0.0f, 0};
     const Row q = kept < kSaved ? saved[1][kept] : row_q;
     const int gone = refused && !model && rest ? a.tokens[t + 1] : -1;  // all of q
-    rest = rest && refused && model;
-    // (a draft row without a logit takes nothing off)
-    const float ip = 1.0f / p.s, iq = rest && q.s > 0.0f ? 1.0f / q.s : 0.0f;
+    rest = rest && refused && model && q.s > 0.0f;  // (a masked draft row takes nothing off)
+    const float ratio = rest ? p.s / q.s : 0.0f;
     const char *xr = row_of(0, t), *yr = rest ? row_of(1, t) : xr;
-    auto one = [&](int i, float x, float y, float e) {
-      // (products rounded by themselves: equal p and q leave exactly nothing)
-      float w = __fmul_rn(weight(x, p.m, c), ip);
-      if (rest) w = __fsub_rn(w, __fmul_rn(weight(y, q.m, c), iq));
-      if (i == gone) w = 0.0f;
-      win.take(w * rate(e), (uint32_t)i);
-    };
+    float score = 0.0f;
+    uint32_t at = 0;
     auto single = [&](int i) {
-      one(i, load_logit<TYPE>(xr, i), rest ? load_logit<TYPE>(yr, i) : 0.0f, __ldg(er + i));
+      float w = weight(load_logit<TYPE>(xr, i), p.m, c);
+      if (rest) w = fmaf(-weight(load_logit<TYPE>(yr, i), q.m, c), ratio, w);
+      const float r = w * rate(__ldg(er + i));
+      if (r > score && i != gone) score = r, at = (uint32_t)i;
     };
     // 16-byte vectors where the rows and the noise agree on where those begin
     const int lead = lead_of<TYPE>(xr), skip = (N - lead) % N;
@@ -499,24 +465,61 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
       // (from is a multiple of eight)
       const int v0 = min(from + skip, to), v1 = v0 + (to - v0) / N * N;
       if (tid < v0 - from) single(from + tid);
+      const uint64_t chi = pair64(c.hi, c.hi), clo = pair64(c.lo, c.lo);
+      const uint64_t np = pair64(-p.m, -p.m), nq = pair64(-q.m, -q.m);
+      auto pairs = [&](uint4 v, uint64_t nm, float (&out)[N]) {  // weights of a vector
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+          float2 x;
+          if (TYPE == 2)
+            x = make_float2(__uint_as_float(tame_word<TYPE>(w[k % 4])),
+                            __uint_as_float(tame_word<TYPE>(w[(k + 1) % 4])));
+          else
+            x = both<TYPE>(tame_word<TYPE>(w[k / 2]));
+          const uint64_t d = add2(pair64(x.x, x.y), nm);
+          const float2 e = unpair64(fma2(d, chi, mul2(d, clo)));
+          out[k] = exp2_approx(e.x);
+          out[k + 1] = exp2_approx(e.y);
+        }
+      };
+#pragma unroll 2
       for (int i = v0 + tid * N; i < v1; i += kVerifyThreads * N) {
-        float x[N], y[N], e[N];
-        unpack<TYPE>(__ldg(reinterpret_cast<const uint4 *>(xr + (int64_t)i * L::kSize)), x);
-        if (rest) unpack<TYPE>(__ldg(reinterpret_cast<const uint4 *>(yr + (int64_t)i * L::kSize)), y);
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(xr + (int64_t)i * L::kSize));
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (rest) y = __ldg(reinterpret_cast<const uint4 *>(yr + (int64_t)i * L::kSize));
+        float w[N], e[N];
 #pragma unroll
         for (int k = 0; k < N; k += 4) {
           const float4 f = __ldg(reinterpret_cast<const float4 *>(er + i + k));
           e[k] = f.x, e[k + 1] = f.y, e[k + 2] = f.z, e[k + 3] = f.w;
         }
+        pairs(x, np, w);
+        if (rest) {
+          float wy[N];
+          pairs(y, nq, wy);
 #pragma unroll
-        for (int k = 0; k < N; ++k) one(i + k, tame<TYPE>(x[k]), rest ? tame<TYPE>(y[k]) : 0.0f, e[k]);
+          for (int k = 0; k < N; ++k) w[k] = fmaf(-wy[k], ratio, w[k]);
+        }
+        float top = score;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          w[k] *= rate(e[k]);
+          top = fmaxf(top, w[k]);  // (NaN is dropped)
+        }
+        if (top > score) {  // rare after the first few
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+            if (w[k] > score && i + k != gone) score = w[k], at = (uint32_t)(i + k);
+        }
       }
       if (tid < to - v1) single(v1 + tid);
     } else {
 #pragma unroll 4
       for (int i = from + tid; i < to; i += kVerifyThreads) single(i);
     }
-    unsigned long long key = win.key();
+    unsigned long long key =
+        score > 0.0f ? (unsigned long long)__float_as_uint(score) << 32 | (0xffffffffu - at) : 0ull;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
@@ -572,33 +575,33 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   }
 }
 
-// Vectors a lane of the rows' kernel.
-constexpr int kVectors = 8;
-int parts_of(int64_t vocab, int type) {
+// Pieces of a row that begins `lead` elements into a 16-byte vector.
+int pieces_of(int64_t vocab, int type, int lead) {
   const int64_t per = (int64_t)kVectors * 32 * (type == 2 ? 4 : 8);
-  return (int)((vocab + (type == 2 ? 3 : 7) + per - 1) / per);
+  return (int)((vocab + lead + per - 1) / per);
 }
+int most_pieces(int64_t vocab, int type) { return pieces_of(vocab, type, type == 2 ? 3 : 7); }
 
 // What must stay zero lies in front, whatever the call's sizes.
 constexpr size_t kTicketsAt = (size_t)kMaxSeqs * 8, kPartsAt = kTicketsAt + (size_t)kMaxSeqs * 4;
 size_t verify_bytes(int64_t T, int64_t V, int type) {
-  return kPartsAt + (size_t)2 * T * parts_of(V, type) * sizeof(float4);
+  return kPartsAt + (size_t)2 * T * most_pieces(V, type) * sizeof(float4);
 }
 
 template <int TYPE>
 cudaError_t verify_as(const VerifyArgs &a, cudaStream_t st, int *launches) {
   *launches = 0;
   if (a.T > 0) {
-    const int64_t units = (a.draft ? 2 : 1) * a.T * a.n_parts;
+    const int64_t units = (a.draft ? 2 : 1) * a.T * a.n_parts;  // (below 2^32)
     const unsigned grid = (unsigned)((units + kVerifyWarps - 1) / kVerifyWarps);
-    const cudaError_t e = launch_dependent(verify_rows_kernel<TYPE, kVectors>, grid,
+    const cudaError_t e = launch_dependent(verify_rows_kernel<TYPE>, grid,
                                            kVerifyThreads, 0, st, true, a);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
   ++*launches;
   const dim3 grid((unsigned)a.splits, (unsigned)a.B);
-  return launch_dependent(verify_draw_kernel<TYPE>, grid, kVerifyThreads, 0, st, true, a);
+  return launch_dependent(verify_draw_kernel<TYPE>, grid, kVerifyThreads, 0, st, a.T > 0, a);
 }
 
 int check_drafts(const kvq_draft_batch *d) {
@@ -672,7 +675,16 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
   a.T = T;
   a.B = batch->n_seqs;
   a.V = (int)V;
-  a.n_parts = parts_of(V, batch->dtype);
+  // rows that all begin on a 16-byte vector have no lead
+  const int size = batch->dtype == KVQ_F32 ? 4 : 2;
+  const bool even = ((uintptr_t)logits & 15) == 0 && stride * size % 16 == 0 &&
+                    (!a.draft || (((uintptr_t)draft_logits & 15) == 0 && draft_stride * size % 16 == 0));
+  a.row_pieces = even ? pieces_of(V, batch->dtype, 0) : most_pieces(V, batch->dtype);
+  // about one unit for each of the 32 warps an SM holds, since a unit's start and end
+  // take as long as a piece; a piece where there are fewer
+  const int64_t all = (a.draft ? 2 : 1) * T * a.row_pieces, warps = (int64_t)num_sms_cached() * 32;
+  a.pieces = (int)std::min<int64_t>(std::max<int64_t>(all / warps, 1), 16);
+  a.n_parts = (a.row_pieces + a.pieces - 1) / a.pieces;
   uint8_t *w = static_cast<uint8_t *>(ws);
   a.keys = reinterpret_cast<unsigned long long *>(w);
   a.tickets = reinterpret_cast<int *>(w + kTicketsAt);

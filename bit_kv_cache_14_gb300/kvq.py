@@ -524,14 +524,32 @@ def _raw_stream(index: int) -> int:
     return get(index) if get else torch.cuda.current_stream(index).cuda_stream
 
 
-def _int32(t: torch.Tensor, dims: int, device) -> None:
-    if t.dtype != torch.int32:
-        raise TypeError("expected an int32 tensor, got %s" % t.dtype)
-    if t.dim() != dims or not t.is_contiguous():
-        raise ValueError("expected a contiguous %d-d tensor, got shape %s"
-                         % (dims, tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("expected a tensor on %s, got one on %s" % (device, t.device))
+def _refuse(t, dtype, shape, device) -> None:
+    """Says what is wrong with a tensor that was to be contiguous, of this type and
+    shape (None: any), on this device."""
+    if t.dtype != dtype:
+        raise TypeError("expected a %s tensor, got %s" % (dtype, t.dtype))
+    if t.dim() != len(shape) or any(m not in (None, n) for m, n in zip(shape, t.shape)):
+        raise ValueError("expected shape %s, got %s" % (shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor (got strides %s)" % (t.stride(),))
+    raise ValueError("expected a tensor on %s, got one on %s" % (device, t.device))
+
+
+def _numbers(t, dtype, n: int, device, index: int) -> int:
+    """Checks n numbers in a row (few attributes are looked at: each is 0.2 us of a
+    10 us call); returns their address."""
+    if (t.dtype is not dtype or t.dim() != 1 or t.numel() != n or t.get_device() != index
+            or not t.is_contiguous()):
+        _refuse(t, dtype, (n,), device)
+    return t.data_ptr()
+
+
+def _pairs(t, rows, device, index: int) -> int:
+    if (t.dtype is not torch.int32 or t.dim() != 2 or t.shape[1] != 2 or t.get_device() != index
+            or rows not in (None, t.shape[0]) or not t.is_contiguous()):
+        _refuse(t, torch.int32, (rows, 2), device)
+    return t.data_ptr()
 
 
 def _on(device, index, fn, stream, *args) -> None:
@@ -649,7 +667,7 @@ class PagedKVCache:
         L = lib()
         self._write, self._read, self._attend = (L.kvq_paged_write, L.kvq_paged_read,
                                                  L.kvq_paged_attention)
-        self._cross = L.kvq_paged_cross_attention
+        self._cross, self._copy = L.kvq_paged_cross_attention, L.kvq_paged_copy
         self._ws_ptr = self.ws.data_ptr()
         self._index = self.device.index if self.device.type == "cuda" else -1
         self._kv_row = (cfg.n_kv_heads, cfg.head_dim)
@@ -749,11 +767,8 @@ class PagedKVCache:
         """Copies pages inside the pool: copies int32 [n][2], pairs (from, to) up
         to the first whose ``from`` is negative (PageTable.reserve's and
         PageTable.compact's)."""
-        _int32(copies, 2, self.device)
-        if copies.shape[1] != 2:
-            raise ValueError("expected pairs [n][2], got shape %s" % (tuple(copies.shape),))
-        _on(self.device, self._index, lib().kvq_paged_copy, stream, *self._refs,
-            copies.data_ptr(), copies.shape[0])
+        at = _pairs(copies, None, self.device, self._index)
+        _on(self.device, self._index, self._copy, stream, *self._refs, at, copies.shape[0])
 
     def device_status(self, stream=None) -> int:
         """Synchronizes, reads and clears the status word.  After an error the
@@ -782,11 +797,11 @@ class PageTable:
             raise ValueError("block_table and seq_lens are given together")
         if block_table is not None:
             self.device = block_table.device
-            _int32(block_table, 2, self.device)
-            _int32(seq_lens, 1, self.device)
-            if seq_lens.shape[0] != block_table.shape[0]:
-                raise ValueError("block_table %s and seq_lens %s do not match"
-                                 % (tuple(block_table.shape), tuple(seq_lens.shape)))
+            if (block_table.dtype != torch.int32 or block_table.dim() != 2
+                    or not block_table.is_contiguous()):
+                _refuse(block_table, torch.int32, (None, None), self.device)
+            _numbers(seq_lens, torch.int32, block_table.shape[0], self.device,
+                     block_table.get_device())
             if n_seqs not in (None, block_table.shape[0]) or width not in (
                     None, block_table.shape[1]):
                 raise ValueError("n_seqs and width are the given tables'")
@@ -814,6 +829,10 @@ class PageTable:
                         ("dev_status", self.status)):
             setattr(self.view, name, t.data_ptr())
         self._ref = ctypes.byref(self.view)
+        L = lib()
+        self._reserve, self._drop, self._select, self._compact, self._recount = (
+            L.kvq_pages_reserve, L.kvq_pages_drop, L.kvq_pages_select, L.kvq_pages_compact,
+            L.kvq_pages_recount)
         if self.device.type == "cuda":
             self.recount()
             if not torch.cuda.is_current_stream_capturing():
@@ -832,15 +851,12 @@ class PageTable:
         _on(self.device, self._index, fn, stream, self._ref, *args)
 
     def _of_seqs(self, t, n) -> int:
-        _int32(t, 1, self.device)
-        if t.shape[0] != n:
-            raise ValueError("expected %d numbers, got %d" % (n, t.shape[0]))
-        return t.data_ptr()
+        return _numbers(t, torch.int32, n, self.device, self._index)
 
     def recount(self, stream=None) -> None:
         """Counts every page's holders again, after block_table or seq_lens were
         written to."""
-        self._call(lib().kvq_pages_recount, stream)
+        self._call(self._recount, stream)
 
     def reserve(self, cu_tokens: torch.Tensor, out=None, stream=None):
         """Pages for cu_tokens' new tokens; seq_lens grows by them.  Returns
@@ -854,23 +870,20 @@ class PageTable:
             call = _output(self.n_seqs + 1, torch.int32, self.device, stream)
         else:
             copies, call = out
-            _int32(copies, 2, self.device)
-            if copies.shape != (self.n_seqs, 2):
-                raise ValueError("expected %d pairs, got shape %s"
-                                 % (self.n_seqs, tuple(copies.shape)))
+            _pairs(copies, self.n_seqs, self.device, self._index)
             self._of_seqs(call, self.n_seqs + 1)
-        self._call(lib().kvq_pages_reserve, stream, cu, copies.data_ptr(), call.data_ptr())
+        self._call(self._reserve, stream, cu, copies.data_ptr(), call.data_ptr())
         return copies, call
 
     def drop(self, tokens: torch.Tensor, stream=None) -> None:
         """Takes back the newest tokens[b] tokens of every sequence (all, and the
         sequence ends, where that is as many or more) and frees their pages."""
-        self._call(lib().kvq_pages_drop, stream, self._of_seqs(tokens, self.n_seqs))
+        self._call(self._drop, stream, self._of_seqs(tokens, self.n_seqs))
 
     def select(self, parents: torch.Tensor, stream=None) -> None:
         """Sequence b becomes what parents[b] was (b: stays, -1: ends), sharing
         its pages: forks, beams in a new order."""
-        self._call(lib().kvq_pages_select, stream, self._of_seqs(parents, self.n_seqs))
+        self._call(self._select, stream, self._of_seqs(parents, self.n_seqs))
 
     def compact(self, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Live pages move to the front of the pool.  Returns the moves for
@@ -879,11 +892,10 @@ class PageTable:
         if out is None:
             out = _output((rows, 2), torch.int32, self.device, stream)
         else:
-            _int32(out, 2, self.device)
-            if out.shape[0] < rows or out.shape[1] != 2:
-                raise ValueError("expected at least %d pairs, got shape %s"
-                                 % (rows, tuple(out.shape)))
-        self._call(lib().kvq_pages_compact, stream, out.data_ptr(), out.shape[0])
+            _pairs(out, None, self.device, self._index)
+            if out.shape[0] < rows:
+                raise ValueError("expected at least %d pairs, got %d" % (rows, out.shape[0]))
+        self._call(self._compact, stream, out.data_ptr(), out.shape[0])
         return out
 
     def device_status(self, stream=None) -> int:
@@ -914,28 +926,20 @@ class DraftVerifier:
         self.ws_bytes = n.value
         self.ws = torch.zeros(n.value, dtype=torch.uint8, device=self.device)
         self.status = _zeroed(1, torch.int32, self.device)
+        self._verify, self._ws_ptr = lib().kvq_verify_drafts, self.ws.data_ptr()
+        self._status_ptr, self._code = self.status.data_ptr(), _LOGIT_DTYPES[dtype]
 
     def _rows(self, t: torch.Tensor, rows: int, dtype) -> int:
         """Checks [rows][vocab] with contiguous rows of any stride; returns it."""
-        if t.dtype != dtype:
-            raise TypeError("expected a %s tensor, got %s" % (dtype, t.dtype))
-        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != self.vocab:
-            raise ValueError("expected shape %s, got %s" % ((rows, self.vocab), tuple(t.shape)))
-        if t.device != self.device:
-            raise ValueError("expected a tensor on %s, got one on %s" % (self.device, t.device))
+        V = self.vocab
+        if t.dtype is not dtype or t.dim() != 2 or t.get_device() != self._index:
+            _refuse(t, dtype, (rows, V), self.device)
+        if t.size(0) != rows or t.size(1) != V:
+            _refuse(t, dtype, (rows, V), self.device)
         s0, s1 = t.stride()
-        if rows > 0 and self.vocab > 1 and s1 != 1:
+        if s1 != 1 and rows > 0 and V > 1:
             raise ValueError("each row must be contiguous (got strides %s)" % (t.stride(),))
-        return s0 if rows > 1 else self.vocab
-
-    def _floats(self, t: torch.Tensor, n: int) -> int:
-        if t.dtype != torch.float32:
-            raise TypeError("expected a float32 tensor, got %s" % t.dtype)
-        if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-            raise ValueError("expected %d contiguous numbers, got shape %s" % (n, tuple(t.shape)))
-        if t.device != self.device:
-            raise ValueError("expected a tensor on %s, got one on %s" % (self.device, t.device))
-        return t.data_ptr()
+        return s0 if rows > 1 else V
 
     def verify(self, logits, tokens, cu_tokens, draft_logits=None, temperature=None,
                uniform=None, noise=None, stream=None):
@@ -947,12 +951,13 @@ class DraftVerifier:
         per row the drafts that stay, then the next token, then -1; per sequence the
         drafts that stay and those that do not (PageTable.drop); per row the
         token's log probability."""
-        _int32(tokens, 1, self.device)
-        _int32(cu_tokens, 1, self.device)
-        T, B = tokens.shape[0], cu_tokens.shape[0] - 1
+        device, index, i32, f32 = self.device, self._index, torch.int32, torch.float32
+        T, B = tokens.numel(), cu_tokens.numel() - 1
         if B < 1 or B > self.n_seqs or T > self.n_tokens:
             raise ValueError("%d rows of %d sequences: the verifier is for %d of %d"
                              % (T, B, self.n_tokens, self.n_seqs))
+        tokens_at = _numbers(tokens, i32, T, device, index)
+        cu = _numbers(cu_tokens, i32, B + 1, device, index)
         stride = self._rows(logits, T, self.dtype)
         dptr, dstride = None, 0
         if draft_logits is not None:
@@ -962,16 +967,21 @@ class DraftVerifier:
         if temperature is not None:
             if uniform is None or noise is None:
                 raise ValueError("sampling needs uniform and noise")
-            tptr, uptr = self._floats(temperature, B), self._floats(uniform, T)
-            nptr, nstride = noise.data_ptr(), self._rows(noise, B, torch.float32)
-        out, logprobs = (_output(T, d, self.device, stream) for d in (torch.int32, torch.float32))
-        accepted, dropped = (_output(B, torch.int32, self.device, stream) for _ in range(2))
-        view = _DraftBatch(cu_tokens.data_ptr(), tokens.data_ptr(), self.status.data_ptr(), T, B,
-                           self.vocab, _LOGIT_DTYPES[self.dtype])
-        _on(self.device, self._index, lib().kvq_verify_drafts, stream, ctypes.byref(view),
-            logits.data_ptr(), stride, dptr, dstride, tptr, uptr, nptr, nstride, out.data_ptr(),
-            accepted.data_ptr(), dropped.data_ptr(), logprobs.data_ptr(), self.ws.data_ptr(),
-            self.ws_bytes)
+            tptr = _numbers(temperature, f32, B, device, index)
+            uptr = _numbers(uniform, f32, T, device, index)
+            nptr, nstride = noise.data_ptr(), self._rows(noise, B, f32)
+        if stream is None:
+            out = torch.empty(T, dtype=i32, device=device)
+            accepted = torch.empty(B, dtype=i32, device=device)
+            dropped = torch.empty(B, dtype=i32, device=device)
+            logprobs = torch.empty(T, dtype=f32, device=device)
+        else:
+            out, accepted, dropped = (_output(n, i32, device, stream) for n in (T, B, B))
+            logprobs = _output(T, f32, device, stream)
+        view = _DraftBatch(cu, tokens_at, self._status_ptr, T, B, self.vocab, self._code)
+        _on(device, index, self._verify, stream, ctypes.byref(view), logits.data_ptr(), stride,
+            dptr, dstride, tptr, uptr, nptr, nstride, out.data_ptr(), accepted.data_ptr(),
+            dropped.data_ptr(), logprobs.data_ptr(), self._ws_ptr, self.ws_bytes)
         return out, accepted, dropped, logprobs
 
     def device_status(self, stream=None) -> int:

@@ -164,3 +164,136 @@ def test_given_stream():
     out = cache.cross_attend(c.queries(), c.batch(), stream=side)
     torch.cuda.current_stream().wait_stream(side)
     c.check(out)
+
+
+# ---- 9 to 32 rows per KV head (operands turned) --------------------------------
+
+@pytest.mark.parametrize("bits,dtype", list(itertools.product((2, 4, 8), (F16, BF16))))
+@pytest.mark.parametrize("rg,new", [(1, [9, 1, 16, 3]), (4, [8, 2, 1, 5]), (1, [31, 32, 0, 17]),
+                                    (16, [1, 1, 2, 1]), (5, [6, 6, 6, 6])])
+def test_rows_of_beams(bits, dtype, rg, new):
+    c = Cross([1000, 127, 0, 385], new, 2 * rg, 2, 128, bits, 64, dtype, seed=rg)
+    cache = c.filled()
+    out = cache.cross_attend(c.queries(), c.batch())
+    assert cache.device_status() == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("bits", (2, 4, 8))
+@pytest.mark.parametrize("kv,rows", [([9000], 12), ([30000], 32), ([128] * 200, 10),
+                                     ([1] * 40 + [4000], 16), ([129, 5000, 0, 1] * 9, 20),
+                                     ([500] * 19, 24)])
+def test_beams_shared_by_blocks(bits, kv, rows):
+    """One long encoder over all blocks, several pairs a block, both."""
+    c = Cross(kv, [rows] * len(kv), 3, 3, 128, bits, 16, F16, seed=len(kv))
+    cache = c.filled()
+    q = c.queries()
+    out = cache.cross_attend(q, c.batch())
+    assert cache.device_status() == 0
+    c.check(out)
+    for _ in range(3):       # joined in an order of its own: the same bits
+        assert torch.equal(out, cache.cross_attend(q, c.batch()))
+
+
+def test_many_sequences_of_beams():
+    c = Cross([(37 * i) % 300 for i in range(700)], [9 if i % 7 else 12 for i in range(700)], 1, 1,
+              128, 4, 32, BF16)
+    cache = c.filled()
+    c.check(cache.cross_attend(c.queries(), c.batch()))
+    assert cache.device_status() == 0
+
+
+@pytest.mark.parametrize("rows", (12, 30))
+@pytest.mark.parametrize("up", (True, False))
+def test_references_that_move(rows, up):
+    """Scores that grow (or fall) by hundreds along the sequence, in one row and not in
+    the others."""
+    c = Cross([1500], [rows], 1, 1, 128, 8, 64, F16, seed=3)
+    base = np.where(c.rng.random(128) < 0.5, -1, 1).astype(np.float32)
+    ramp = np.linspace(-1, 1, 1500).astype(np.float32) * (1 if up else -1)
+    c.K[0] = c._round(0.2 * c.rng.standard_normal((1500, 1, 128)).astype(np.float32)
+                      + ramp[:, None, None] * base)
+    c.q[:, 0] = c._round(0.3 * c.q[:, 0])
+    c.q[3, 0] = 30 * base
+    c.q[7, 0] = -30 * base
+    cache = c.filled()
+    out = cache.cross_attend(c.queries(), c.batch())
+    assert cache.device_status() == 0
+    c.check(out)
+
+
+def test_rows_that_are_not_numbers_stay_alone():
+    c = Cross([700, 40], [14, 10], 2, 1, 128, 4, 32, F16)
+    cache = c.filled()
+    q = c.queries()
+    want = cache.cross_attend(q, c.batch())
+    q[5, 1, 7] = float("nan")
+    q[15, 0, 100] = float("inf")
+    got = cache.cross_attend(q, c.batch())
+    keep = torch.ones(24, 2, dtype=torch.bool)
+    keep[5, 1] = keep[15, 0] = False
+    assert torch.equal(got[keep.cuda()], want[keep.cuda()])
+    assert got[5, 1].isnan().all() and got[15, 0].isnan().all()
+
+
+@pytest.mark.parametrize("rows", (10, 25))
+def test_beams_without_some_pages(rows):
+    c = Cross([300, 300, 64], [rows] * 3, 1, 1, 128, 4, 16, F16)
+    cache = c.filled()
+    c.table[1, 3] = -1
+    c.table[1, 18] = c.n_pages
+    out = cache.cross_attend(c.queries(), c.batch())
+    assert cache.device_status() == kvq.KVQ_EPAGE
+    lost = list(range(48, 64)) + list(range(288, 300))
+    check_rows(c.single_rows(), out, gone={rows + i: lost for i in range(rows)})
+    neg = cache.cross_attend(c.queries(), c.batch(kv=[-3, 0, -2 ** 31]))
+    assert (neg == 0).all() and cache.device_status() == 0
+
+
+def test_bad_rows_of_beams():
+    """Rows out of order and more rows than max_tokens says are reported."""
+    c = Cross([100, 100], [10, 10], 1, 1, 128, 4, 16, F16)
+    cache = c.filled()
+    batch = c.batch(max_tokens=12)
+    batch.cu_tokens.copy_(torch.tensor([0, 13, 20], dtype=torch.int32))
+    cache.cross_attend(c.queries(), batch)
+    assert cache.device_status() == kvq.KVQ_EINVAL
+    batch.cu_tokens.copy_(torch.tensor([0, 10, 20], dtype=torch.int32))
+    c.check(cache.cross_attend(c.queries(), batch))
+    assert cache.device_status() == 0
+
+
+def test_a_wait_that_runs_out_ends_the_call():
+    """Beams after the stall switch: the status says so, scratch is cleared, and the
+    next call is right."""
+    c = Cross([2000, 300], [12, 12], 2, 2, 128, 4, 32, F16)
+    cache = c.filled()
+    kvq.debug_stall_waits(2000)
+    try:
+        cache.cross_attend(c.queries(), c.batch())
+        assert cache.device_status() == kvq.KVQ_ETIMEOUT
+    finally:
+        kvq.debug_stall_waits(0)
+    c.check(cache.cross_attend(c.queries(), c.batch()))
+    assert cache.device_status() == 0
+
+
+def test_captured_beams_beside_the_causal_call():
+    """The same scratch serves cross and causal calls one after the other, captured."""
+    c = Cross([900, 64], [3, 3], 8, 2, 128, 4, 64, BF16)
+    cache = c.filled()
+    q, batch = c.queries(), c.batch()
+    want = cache.cross_attend(q, batch), cache.attend(q, batch)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cache.cross_attend(q, batch), cache.attend(q, batch)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [f(q, batch) for f in (cache.cross_attend, cache.attend) * 2]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want * 2):
+            assert torch.equal(x, y)
