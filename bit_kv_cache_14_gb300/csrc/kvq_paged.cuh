@@ -50,9 +50,6 @@ size_t paged_workspace_bytes();
 cudaError_t launch_paged_rows(const Paged &p, const void *q, int64_t qs, void *out, float scale,
                               int few, bool beside, void *ws, int num_sms, cudaStream_t st);
 size_t paged_rows_workspace();
-constexpr int kPagedCrossRows = 32;  // the most rows of kvq_paged_cross.cu
-cudaError_t launch_paged_cross(const Paged &p, const void *q, int64_t qs, void *out, float scale,
-                               int rows, void *ws, int num_sms, cudaStream_t st);
 cudaError_t launch_paged_chunk(const Paged &p, const void *q, int64_t qs, void *out, float scale,
                                int few, void *ws, int num_sms, cudaStream_t st);
 size_t paged_chunk_workspace();

@@ -20,11 +20,6 @@ cudaError_t launch_paged_attention(const Paged &p, const void *q, int64_t qs, vo
   const int sms = num_sms_cached();
   // (a call without rows, only padding, still looks whether that is so)
   const int64_t most = (int64_t)(p.max_tokens > 0 ? p.max_tokens : 1) * p.rg;
-  // cross attention of a few beams or samples: operands turned (kvq_paged_cross.cu)
-  if (p.cross && p.d == 128 && most > 8 && most <= kPagedCrossRows) {
-    *launches = 1;
-    return launch_paged_cross(p, q, qs, out, scale, (int)most, ws, sms, st);
-  }
   // a mixed call's small sequences are decode steps: the 8-row form of the
   // split kernel, where the heads of one token fit it (a chunk of 512 with 63
   // decodes of up to 8000 tokens: 190 us, 248 us with the 16-row form)

@@ -20,8 +20,9 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kReserveThreads = 1024;
 constexpr int kReserveWarps = kReserveThreads / 32;
 constexpr int kRowThreads = 256;             // kernels over the tables' rows: a warp a stretch
-constexpr int kStretch = 512;                // entries of a stretch
-constexpr int kMoveThreads = 256;            // compaction: a word of the map a thread
+constexpr int kStretch = 128;                // entries of a stretch
+constexpr int kMoveThreads = 256;
+constexpr int kMoveWords = 64;               // compaction: words of the map a block
 
 // The head of kvq_page_table.state.
 struct Head {
@@ -408,50 +409,52 @@ pages_map_kernel(const __grid_constant__ Table t) {
 __global__ void __launch_bounds__(kMoveThreads)
 pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copies) {
   __shared__ int64_t sums[kMoveThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ uint32_t word_bits[kMoveWords];
+  __shared__ int word_before[kMoveWords];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_trigger();
   grid_dep_wait();
   const int front = t.n_pages - t.head->free, front_word = front >> 5;
   const uint32_t front_bits = (1u << (front & 31)) - 1;  // of that word: before the front
-  const int w0 = blockIdx.x * kMoveThreads;
-  // free pages before the block's words, and before the front
+  const int w0 = blockIdx.x * kMoveWords;
+  // free pages before the block's words, and before the front, four words a load
+  const int ends = min(max(w0, front_word + 1), t.words);
   int64_t before = 0, holes = 0, total;
-  for (int w = tid; w < max(w0, min(front_word + 1, t.words)); w += kMoveThreads) {
-    const uint32_t bits = t.map[w];
+  auto count = [&](int w, uint32_t bits) {
     if (w < w0) before += __popc(bits);
     if (w < front_word) holes += __popc(bits);
     if (w == front_word) holes += __popc(bits & front_bits);
+  };
+#pragma unroll 4
+  for (int w = 4 * tid; w < ends; w += 4 * kMoveThreads) {
+    // (the map's room is a multiple of four words)
+    const uint4 v = *reinterpret_cast<const uint4 *>(t.map + w);
+    count(w, v.x);
+    count(w + 1, v.y);
+    count(w + 2, v.z);
+    count(w + 3, v.w);
   }
   block_scan<kMoveThreads / 32>(before, sums, total);
   before = total;
   block_scan<kMoveThreads / 32>(holes, sums, total);
   const int moves = (int)total;
   const int w = w0 + tid;
-  const uint32_t bits = w < t.words ? t.map[w] : 0u;
-  const int64_t count = __popc(bits);
-  const int here = (int)(before + block_scan<kMoveThreads / 32>(count, sums, total) - count);
-  if (w < t.words) reinterpret_cast<uint2 *>(t.rows)[w] = make_uint2(bits, (uint32_t)here);
+  const bool mine = tid < kMoveWords && w < t.words;
+  const uint32_t bits = mine ? t.map[w] : 0u;
+  const int64_t free = __popc(bits);
+  const int here = (int)(before + block_scan<kMoveThreads / 32>(free, sums, total) - free);
+  if (tid < kMoveWords) word_bits[tid] = bits, word_before[tid] = here;
+  if (mine) reinterpret_cast<uint2 *>(t.rows)[w] = make_uint2(bits, (uint32_t)here);
   if (blockIdx.x == 0 && tid == 0) t.head->moves = moves, t.head->front = front;
-  // a word at a time, a lane a page: a free one before the front, a live one behind
-  const int i0 = w * 32;
-  uint32_t ask = 0;
-  if (w < t.words) {
-    const uint32_t there = t.n_pages - i0 >= 32 ? kAll : (1u << (t.n_pages - i0)) - 1;
-    const uint32_t low = w < front_word ? kAll : w == front_word ? front_bits : 0u;
-    ask = (bits & low) | (~bits & ~low & there);
-  }
-  unsigned busy = __ballot_sync(kAll, ask != 0);
-  while (busy) {
-    const int l = __ffs(busy) - 1;
-    busy &= busy - 1;
-    const uint32_t which = __shfl_sync(kAll, ask, l), word = __shfl_sync(kAll, bits, l);
-    const int f = __shfl_sync(kAll, here, l) + __popc(word & ((1u << lane) - 1));
-    const int id = (w0 + (tid & ~31) + l) * 32 + lane;
-    if (!(which >> lane & 1)) continue;
-    if (id < front)
-      copies[f].y = id;
-    else
-      copies[(id - f) - (front - moves)].x = id;
+  __syncthreads();
+  // a warp a word, a lane a page: a free one before the front, a live one behind
+  for (int j = warp; j < kMoveWords && w0 + j < t.words; j += kMoveThreads / 32) {
+    const uint32_t word = word_bits[j];
+    const int f = word_before[j] + __popc(word & ((1u << lane) - 1));
+    const int id = (w0 + j) * 32 + lane;
+    const bool is_free = word >> lane & 1;
+    if (id < front && is_free) copies[f].y = id;
+    if (id >= front && id < t.n_pages && !is_free) copies[(id - f) - (front - moves)].x = id;
   }
   for (int64_t k = moves + (int64_t)blockIdx.x * kMoveThreads + tid; k < n_copies;
        k += (int64_t)gridDim.x * kMoveThreads)
@@ -646,7 +649,7 @@ int kvq_pages_compact(const kvq_page_table *table, int32_t *copies, int64_t n_co
   if (n_copies < t.n_pages / 2) return KVQ_ECAPACITY;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int2 *pairs = reinterpret_cast<int2 *>(copies);
-  cudaError_t e = launch_dependent(pages_moves_kernel, blocks_of(t.words, kMoveThreads),
+  cudaError_t e = launch_dependent(pages_moves_kernel, blocks_of(t.words, kMoveWords),
                                    kMoveThreads, 0, st, true, t, pairs, n_copies);
   const int rows = (int)row_blocks(t);
   if (e == cudaSuccess)
