@@ -241,14 +241,14 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
     for (int j = warp; j < kReserveThreads && map_before[j] < n; j += kReserveWarps) {
       const uint32_t word = map_bits[j];
       const int r = map_before[j] + __popc(word & ((1u << lane) - 1));
-      const bool take = (word >> lane & 1) && r < n;
+      const int page = (w0 + j) * 32 + lane;
+      const bool take = (word >> lane & 1) && r < n && page < t.n_pages;
       if (take) {
         int lo = 0, hi = t.B;  // the last b with first[b] <= r that needs a page
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (first[mid] <= r) lo = mid; else hi = mid;
         }
-        const int page = (w0 + j) * 32 + lane;
         t.table[lo * t.width + entry[lo] + (r - first[lo])] = page;
         t.refs[page] = 1;
         if (from[lo] >= 0 && r == first[lo]) copies[pair[lo]] = make_int2(from[lo], page);
@@ -453,8 +453,11 @@ pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copi
     const int f = word_before[j] + __popc(word & ((1u << lane) - 1));
     const int id = (w0 + j) * 32 + lane;
     const bool is_free = word >> lane & 1;
-    if (id < front && is_free) copies[f].y = id;
-    if (id >= front && id < t.n_pages && !is_free) copies[(id - f) - (front - moves)].x = id;
+    // (in range wherever the head's count is the map's)
+    const int64_t k = id < front ? f : (int64_t)id - f - (front - moves);
+    if (k < 0 || k >= n_copies || id >= t.n_pages) continue;
+    if (id < front && is_free) copies[k].y = id;
+    if (id >= front && !is_free) copies[k].x = id;
   }
   for (int64_t k = moves + (int64_t)blockIdx.x * kMoveThreads + tid; k < n_copies;
        k += (int64_t)gridDim.x * kMoveThreads)
@@ -462,7 +465,8 @@ pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copi
 }
 // Blocks [0, row_blocks): table entries; behind them: pages and the free map.
 __global__ void __launch_bounds__(kRowThreads)
-pages_rename_kernel(const __grid_constant__ Table t, const int2 *copies, int row_blocks) {
+pages_rename_kernel(const __grid_constant__ Table t, const int2 *copies, int64_t n_copies,
+                    int row_blocks) {
   const int lane = threadIdx.x & 31;
   grid_dep_trigger();
   grid_dep_wait();
@@ -471,7 +475,9 @@ pages_rename_kernel(const __grid_constant__ Table t, const int2 *copies, int row
   auto moved_to = [&](int id) {  // of a live page behind the front
     const uint2 s = snap[id >> 5];
     const int f = (int)s.y + __popc(s.x & ((1u << (id & 31)) - 1));
-    return copies[(id - f) - (front - moves)].y;
+    const int64_t k = (int64_t)id - f - (front - moves);
+    const int to = k >= 0 && k < n_copies ? copies[k].y : -1;
+    return to >= 0 && to < t.n_pages ? to : id;
   };
   if (blockIdx.x < row_blocks) {
     const Stretch p = row_of_warp(t);
@@ -489,8 +495,9 @@ pages_rename_kernel(const __grid_constant__ Table t, const int2 *copies, int row
   }
   const int64_t i = (int64_t)(blockIdx.x - row_blocks) * kRowThreads + threadIdx.x;
   if (i < t.n_pages && i >= front && !(snap[i >> 5].x >> (i & 31) & 1)) {
-    t.refs[moved_to((int)i)] = t.refs[i];
+    const int holders = t.refs[i];
     t.refs[i] = 0;
+    t.refs[moved_to((int)i)] = holders;
   }
   const unsigned bits = __ballot_sync(kAll, i < t.n_pages && i >= front);
   if (lane == 0 && i < (int64_t)t.words * 32) t.map[i >> 5] = bits;
@@ -655,7 +662,7 @@ int kvq_pages_compact(const kvq_page_table *table, int32_t *copies, int64_t n_co
   if (e == cudaSuccess)
     e = launch_dependent(pages_rename_kernel,
                          rows + blocks_of((int64_t)t.words * 32, kRowThreads), kRowThreads, 0, st,
-                         true, t, pairs, rows);
+                         true, t, pairs, n_copies, rows);
   return done(e, 2);
 }
 

@@ -675,6 +675,7 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
     if (!logits || !out_tokens || !logprobs || stride < V) return KVQ_EINVAL;
     if (draft_logits && draft_stride < V) return KVQ_EINVAL;
     if (temperature && (!uniform || !noise || noise_stride < V)) return KVQ_EINVAL;
+    if (out_tokens < batch->tokens + T && batch->tokens < out_tokens + T) return KVQ_EINVAL;
     if (((uintptr_t)logits & word) || ((uintptr_t)draft_logits & word)) return KVQ_EALIGN;
     for (const void *p : {(const void *)temperature, (const void *)uniform, (const void *)noise,
                           (const void *)out_tokens, (const void *)logprobs})

@@ -700,8 +700,8 @@ int kvq_verify_workspace_bytes(const kvq_draft_batch *batch, size_t *bytes);
  * of equal ones the lowest.  Its distribution is p's, whatever the drafts.  Greedy:
  * a draft stays while it is the lowest index of x's maximum, and that is the next
  * token.
- *   out_tokens [n_tokens]: for each sequence from its first row on, the drafts that
- *     stayed, then the next token, then -1.
+ *   out_tokens [n_tokens], apart from tokens: for each sequence from its first row on,
+ *     the drafts that stayed, then the next token, then -1.
  *   logprobs fp32 [n_tokens]: ln p of each of those tokens (greedy: at T = 1), 0
  *     for -1.
  *   accepted, dropped [n_seqs]: drafts that stayed, and the others: what

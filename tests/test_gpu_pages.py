@@ -138,6 +138,17 @@ def test_rows_longer_than_the_table():
     m.check(tab)
 
 
+@pytest.mark.parametrize("width", (20, 3000))
+def test_every_sequence_ends(width):
+    """The lengths themselves as what is taken back."""
+    m, tab = both(5000, 16, 5, width)
+    reserve(m, tab, [100, 0, 17, 1, 16 * min(width, 2000)])
+    m.drop(m.lens)
+    tab.drop(tab.seq_lens)
+    m.check(tab)
+    assert int(tab.free_pages) == 5000 and tab.device_status() == 0
+
+
 def test_long_rows_are_shared_by_warps():
     """Rows of 3000 entries (more than one stretch) forked, dropped and freed."""
     m, tab = both(9000, 16, 3, 3000)

@@ -149,6 +149,8 @@ def test_verify_refusals():
         assert _verify(_drafts(), **{name: VERIFY[name] + 2}) == E.KVQ_EALIGN, name
     for name in ("stride", "dstride", "nstride"):
         assert _verify(_drafts(), **{name: 99}) == E.KVQ_EINVAL, name
+    for at in (0x1000, 0x1000 + 36, 0x1000 - 36):    # outputs on the drafts
+        assert _verify(_drafts(), out=at) == E.KVQ_EINVAL
     assert _verify(_drafts(dtype=kvq.BF16), logits=0x2001) == E.KVQ_EALIGN
     n = ctypes.c_size_t()
     bytes_of = lambda d: kvq.lib().kvq_verify_workspace_bytes(ctypes.byref(d), ctypes.byref(n))  # noqa: E731
