@@ -510,21 +510,29 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
           out[k + 1] = exp2_approx(e.y);
         }
       };
-#pragma unroll 2
-      for (int i = v0 + tid * N; i < v1; i += kVerifyThreads * N) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(xr + (int64_t)i * L::kSize));
-        uint4 y = make_uint4(0, 0, 0, 0);
+      // (the next vectors are on their way while these are worked on)
+      uint4 x, y = make_uint4(0, 0, 0, 0);
+      float4 f[N / 4];
+      auto fetch = [&](int i) {
+        if (i >= v1) return;
+        x = __ldg(reinterpret_cast<const uint4 *>(xr + (int64_t)i * L::kSize));
         if (rest) y = __ldg(reinterpret_cast<const uint4 *>(yr + (int64_t)i * L::kSize));
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) f[k] = __ldg(reinterpret_cast<const float4 *>(er + i) + k);
+      };
+      fetch(v0 + tid * N);
+#pragma unroll 1
+      for (int i = v0 + tid * N; i < v1; i += kVerifyThreads * N) {
         float w[N], e[N];
 #pragma unroll
-        for (int k = 0; k < N; k += 4) {
-          const float4 f = __ldg(reinterpret_cast<const float4 *>(er + i + k));
-          e[k] = f.x, e[k + 1] = f.y, e[k + 2] = f.z, e[k + 3] = f.w;
-        }
-        pairs(x, np, w);
+        for (int k = 0; k < N; k += 4)
+          e[k] = f[k / 4].x, e[k + 1] = f[k / 4].y, e[k + 2] = f[k / 4].z, e[k + 3] = f[k / 4].w;
+        const uint4 cx = x, cy = y;
+        fetch(i + kVerifyThreads * N);
+        pairs(cx, np, w);
         if (rest) {
           float wy[N];
-          pairs(y, nq, wy);
+          pairs(cy, nq, wy);
 #pragma unroll
           for (int k = 0; k < N; ++k) w[k] = fmaf(-wy[k], ratio, w[k]);
         }
@@ -708,13 +716,11 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
   const bool even = ((uintptr_t)logits & 15) == 0 && stride * size % 16 == 0 &&
                     (!a.draft || (((uintptr_t)draft_logits & 15) == 0 && draft_stride * size % 16 == 0));
   a.row_pieces = even ? pieces_of(V, batch->dtype, 0) : most_pieces(V, batch->dtype);
-  // As many pieces a unit as leave one unit for each of the 32 warps an SM holds (a
-  // unit's start and end take as long as a piece, and a second round of few units as
-  // long as a whole one): 512 rows of 65 pieces in units of 6: 28 us, of 8: 26.
-  const int64_t rows = T + (a.draft ? std::max<int64_t>(T - a.B, 0) : 0);
-  const int64_t warps = (int64_t)num_sms_cached() * 32;
-  for (a.pieces = 1; a.pieces < 16; ++a.pieces)
-    if (rows * ((a.row_pieces + a.pieces - 1) / a.pieces) <= warps) break;
+  // Four pieces a unit, whose start and end take as long as one, or as few as give each
+  // of the 32 warps an SM holds a unit (64 x 5 rows of 131072 in units of 2, 4, 8: 45.1,
+  // 43.4, 43.3 us; 128 x 4 fp32 rows of 65537: 29.3, 26.6, 28.1).
+  const int64_t all = (a.draft ? 2 : 1) * T * a.row_pieces, warps = (int64_t)num_sms_cached() * 32;
+  a.pieces = (int)std::min<int64_t>(std::max<int64_t>(all / warps, 1), 4);
   a.n_parts = (a.row_pieces + a.pieces - 1) / a.pieces;
   uint8_t *w = static_cast<uint8_t *>(ws);
   a.keys = reinterpret_cast<unsigned long long *>(w);

@@ -76,7 +76,8 @@ def verify(logits, tokens, cu, draft, temperature, uniform, noise):
                         lq = np.log(q[c]) if draft is None or not have else have[1][c]
                         left = np.log(np.float64(uniform[r + i])) + lq
                     stay = bool(left < logp[c])
-                    close |= bool(abs(left - logp[c]) < MARGIN) and got is not None
+                    with np.errstate(invalid="ignore"):
+                        close |= bool(abs(left - logp[c]) < MARGIN) and got is not None
                 if stay:
                     t = c
                 else:
