@@ -344,7 +344,8 @@ paged_read_kernel(const __grid_constant__ Paged p, uint16_t *k, uint16_t *v) {
 }
 
 // A warp copies 4 KB of a page at a time, its lanes eight 16-byte vectors each, and
-// reads the next piece's page numbers meanwhile.
+// reads the next piece's page numbers meanwhile.  HBM bounds it: 3400 pages of 80 KB,
+// 557 MB in and out, 82 us = 6.8 TB/s, the copy rate.
 constexpr int kCopyVecs = 8, kCopyBytes = 32 * 16 * kCopyVecs;
 __global__ void __launch_bounds__(kIoThreads)
 paged_copy_kernel(const __grid_constant__ Paged p, const int2 *copies, int64_t n) {

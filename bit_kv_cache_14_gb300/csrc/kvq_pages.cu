@@ -7,6 +7,11 @@
 // numbers stay in use, and `hint` (no word before it has a free page) is where the
 // search begins.  Holder counts change by atomics, whose order does not matter: who
 // takes the last holder away sets the page's bit.
+//
+// Measured on a GB300 (graph replay): drop and reserve of 16 sequences 6.8 us, of 2048
+// over a pool of 431000 pages 10.3 (25 when one warp walked 32 neighbouring words of the
+// map); select, reserve and the copy of 60 forks' pages 14.3; recount, compact and the
+// copy of 278 MB in a pool of 14000 pages 100, 82 of them the copy.
 #include <algorithm>
 
 #include "kvq_paged.cuh"
