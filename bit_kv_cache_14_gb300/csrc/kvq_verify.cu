@@ -55,11 +55,9 @@ struct VerifyArgs {
 __device__ __forceinline__ void verify_error(const VerifyArgs &a, int code) {
   atomicCAS(a.status, 0, code);
 }
-__device__ __forceinline__ bool bad_range(const VerifyArgs &a, int r0, int r1) {
-  return r0 < 0 || r1 < r0 || r1 > a.T;
-}
 
-// The sequence of row t, found by the whole warp (32 candidates a round), or -1.
+// The sequence of row t, found by the whole warp (32 candidates a round), or -1: exact
+// where cu_tokens is in order, and nothing is made of it where it is not (the draw).
 __device__ __forceinline__ int sequence_of(const VerifyArgs &a, int64_t t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = a.B;  // the largest b with cu[b] <= t
@@ -70,8 +68,7 @@ __device__ __forceinline__ int sequence_of(const VerifyArgs &a, int64_t t) {
     lo += (31 - __clz(le)) * step;
     hi = min(lo + step, hi);
   }
-  const int r0 = a.cu[lo], r1 = a.cu[lo + 1];
-  return t >= r0 && t < r1 && !bad_range(a, r0, r1) ? lo : -1;
+  return t >= a.cu[lo] && t < a.cu[lo + 1] ? lo : -1;
 }
 
 // The temperature of sequence b; 0: greedy (also for NaN).
@@ -136,24 +133,6 @@ __device__ __forceinline__ float load_logit(const void *row, int64_t i) {
     x = TYPE == 1 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((uint16_t)h));
   }
   return tame<TYPE>(x);
-}
-// Elements of a 16-byte vector.
-template <int TYPE>
-__device__ __forceinline__ void unpack(uint4 v, float (&x)[Logit<TYPE>::kVec]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (TYPE == 2) {
-      x[i] = __uint_as_float(w[i]);
-    } else if constexpr (TYPE == 1) {
-      x[2 * i] = bf16_lo(w[i]);
-      x[2 * i + 1] = bf16_hi(w[i]);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
 }
 // How many elements before the row's first its first 16-byte vector begins.
 template <int TYPE>
@@ -404,7 +383,7 @@ __device__ __forceinline__ float rate(float e) {
 // Block (share, sequence).
 constexpr int kSaved = 64;  // rows whose joined parts a block keeps
 template <int TYPE>
-__global__ void __launch_bounds__(kVerifyThreads)
+__global__ void __launch_bounds__(kVerifyThreads, 4)
 verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   using L = Logit<TYPE>;
   constexpr int N = L::kVec;
@@ -414,15 +393,19 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y, share = blockIdx.x;
   if (tid == 0) stop = 0x7fffffff;
-  __syncthreads();
   grid_dep_trigger();
   // Until the wait only the call's inputs are looked at (the rows' kernel passes its
   // own wait before this one starts), and nothing is written.
   const int r0 = a.cu[b], r1 = a.cu[b + 1], n = r1 - r0;
-  if (bad_range(a, r0, r1) || n == 0) {
+  // rows out of order anywhere, or outside the packed arrays: which sums belong to which
+  // sequence is not known, and none is judged
+  bool bad = a.cu[0] < 0 || a.cu[a.B] > a.T;
+  for (int i = tid; i < a.B; i += kVerifyThreads) bad |= a.cu[i + 1] < a.cu[i];
+  bad = __syncthreads_or(bad);
+  if (bad || n == 0) {
     grid_dep_wait();
     if (share == 0 && tid == 0) {
-      if (n != 0 || bad_range(a, r0, r1)) verify_error(a, KVQ_EINVAL);
+      if (bad) verify_error(a, KVQ_EINVAL);
       a.accepted[b] = 0;
       a.dropped[b] = 0;
     }

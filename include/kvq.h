@@ -709,9 +709,10 @@ int kvq_verify_workspace_bytes(const kvq_draft_batch *batch, size_t *bytes);
  * Masked: a logit of -infinity or NaN has probability 0; +infinity counts as the
  * type's largest number.  A row of masked logits has no next token: -1.
  * e_i below 2^-126 counts as that, NaN takes i out.  T is held to 2^-100..2^100.
- * A draft outside [0, vocab) is refused and gives KVQ_EINVAL in the status word;
- * so do rows of a sequence out of order or behind n_tokens, whose outputs are left
- * alone but for 0 accepted, 0 dropped.  A sequence without rows gets those too.
+ * A draft outside [0, vocab) is refused and gives KVQ_EINVAL in the status word; so
+ * do cu_tokens that decrease, begin below 0 or end behind n_tokens: then no sequence is
+ * judged, and outputs are left alone but for 0 accepted, 0 dropped.  A sequence without
+ * rows gets those too.
  * Arithmetic: fp32, sums in fp32 in a fixed order; exponents of the drafts' tests
  * in 64 bits.  p and q are within 1e-6 (relative) of the exact ones, so numbers that
  * close to a border may fall on its other side.

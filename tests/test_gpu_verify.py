@@ -205,18 +205,24 @@ def test_drafts_that_are_no_tokens():
 
 
 def test_rows_out_of_order():
-    """Sequences whose rows are wrong are left alone, the others are not."""
-    for cu in ([0, 5, 3, 9], [0, -1, 4, 9], [0, 4, 9, 13], [3, 1, 4, 9]):
-        a = inputs([4, 4, 4], 70, F16, "model", seed=7)
-        a["cu"] = i32(cu)
-        v = kvq.DraftVerifier(3, 12, 70, F16)
-        got = call(v, **a)
-        assert v.device_status() == kvq.KVQ_EINVAL
-        for b in range(3):
-            r0, r1 = cu[b], cu[b + 1]
-            if r0 < 0 or r1 < r0 or r1 > 12:
-                assert got[1][b] == 0 and got[2][b] == 0
+    """Rows that overlap or lie outside are nobody's: no sequence is judged."""
+    for cu in ([0, 5, 3, 9], [0, -1, 4, 9], [0, 4, 9, 13], [3, 1, 4, 9], [-1, 4, 8, 12]):
+        for kind in ("model", "greedy"):
+            a = inputs([4, 4, 4], 70, F16, kind, seed=7)
+            a["cu"] = i32(cu)
+            v = kvq.DraftVerifier(3, 12, 70, F16)
+            got = call(v, **a)
+            assert v.device_status() == kvq.KVQ_EINVAL
+            assert not got[1].any() and not got[2].any()
+    # many sequences, one border out of order
+    n = [2] * 300
+    b = inputs(n, 40, BF16, "greedy", seed=1)
+    b["cu"][150] = 10
+    many = kvq.DraftVerifier(300, 600, 40, BF16)
+    got = call(many, **b)
+    assert many.device_status() == kvq.KVQ_EINVAL and not got[1].any()
     # what follows is not disturbed
+    a = inputs([4, 4, 4], 70, F16, "model", seed=7)
     a["cu"] = i32([0, 4, 8, 12])
     got = call(v, **a)
     check(got, expected(**a), [0, 4, 8, 12], a["tokens"].cpu().numpy(), allow_close=0.5)
