@@ -213,6 +213,23 @@ def test_beams_shared_by_blocks(bits, kv, rows):
         assert torch.equal(out, cache.cross_attend(q, c.batch()))
 
 
+@pytest.mark.parametrize("d,bits", [(128, 4), (64, 2), (128, 8), (64, 4)])
+@pytest.mark.parametrize("kv,new,rg", [([3000], [33], 1), ([9000, 100, 0, 1], [40, 128, 64, 20], 1),
+                                       ([700] * 60, [5, 30, 9] * 20, 4),
+                                       ([129, 128, 127, 2500] * 6, [17, 32, 100, 31] * 6, 4)])
+def test_tiles_of_a_few_dozen_rows(d, bits, kv, new, rg):
+    """17 to 128 rows per KV head: a tile over all blocks, tiles of one step, whole tiles
+    next to each other, tiles of more rows and of few among them."""
+    c = Cross(kv, new, rg * 2, 2, d, bits, 64, (F16, BF16)[bits == 4], seed=d)
+    cache = c.filled()
+    q = c.queries()
+    out = cache.cross_attend(q, c.batch())
+    assert cache.device_status() == 0
+    c.check(out)
+    for _ in range(2):
+        assert torch.equal(out, cache.cross_attend(q, c.batch()))
+
+
 def test_many_sequences_of_beams():
     c = Cross([(37 * i) % 300 for i in range(350)], [9 if i % 7 else 2 for i in range(350)], 1, 1,
               128, 4, 32, BF16)
