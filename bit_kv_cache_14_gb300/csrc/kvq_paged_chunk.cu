@@ -879,26 +879,41 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
     uint32_t sn = 0, step = 0;  // score tiles taken; steps of the block (for the bad-page bytes)
     uint32_t on = 0, gn = 0;    // tiles finished; meetings of the tile's threads
     bool ok = true;
-    // queries: LR lanes to a row, LR rows a lane (in two halves); scaled so that a row's largest
-    // is in [2^8, 2^9), which bf16 queries need to fit fp16
+    // queries: LR lanes to a row, LR rows a lane, copied to their places in the operand
+    // tile and scaled there so that a row's largest is in [2^8, 2^9), which bf16 queries
+    // need to fit fp16.  (In rolled loops: unrolled code that runs once an item spent 14 us
+    // on instructions that were in no cache, all of a small call's start.)
     constexpr int LR = D / 8;
     const int ql = lane % LR, qr = (warp & 3) * 32 + lane / LR;
-    auto load_queries = [&](const Item *it, int half, uint4 (&w)[LR / 2]) {
-#pragma unroll
-      for (int k = 0; k < LR / 2; ++k) {
-        const int row = it->row_first + i * 128 + qr + (k + half * (LR / 2)) * (32 / LR);
-        w[k] = make_uint4(0, 0, 0, 0);
-        if (row < it->rows)
-          w[k] = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(it->row0 + row / p.rg) * a.qs +
-                                                       (int64_t)(it->h * p.rg + row % p.rg) * D) +
-                       ql);
+    auto query_at = [&](int rr) {
+      return smem_s + C::off_q + i * C::kTile + (ql >> 3) * (kStep * 128) + rr * 128 +
+             (((ql & 7) ^ (rr & 7)) << 4);
+    };
+    const uint32_t rg_inv = (65535 + p.rg) / p.rg;  // n / rg = n * this >> 16 for n < 512
+    auto load_queries = [&](const Item *it) {
+      const int first = it->row_first + i * 128 + qr, t0 = first / p.rg, r0 = first - t0 * p.rg;
+#pragma unroll 1
+      for (int k = 0; k < LR; ++k) {
+        const int rr = qr + k * (32 / LR), n = r0 + k * (32 / LR);
+        const int dt = (int)(n * rg_inv >> 16);
+        const bool there = first + k * (32 / LR) < it->rows;
+        const uint16_t *src = a.q + (int64_t)(it->row0 + t0 + dt) * a.qs +
+                              (int64_t)(it->h * p.rg + n - dt * p.rg) * D + 8 * ql;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(query_at(rr)),
+                     "l"(there ? src : a.q), "r"(there ? 16 : 0)
+                     : "memory");
       }
     };
-    auto store_queries = [&](int half, const uint4 (&w)[LR / 2]) {
-#pragma unroll
-      for (int k = 0; k < LR / 2; ++k) {
-        const int rr = qr + (k + half * (LR / 2)) * (32 / LR);
-        const uint32_t ww[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    auto scale_queries = [&]() {  // (each lane what it copied itself)
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+      for (int k = 0; k < LR; ++k) {
+        const int rr = qr + k * (32 / LR);
+        uint32_t ww[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(ww[0]), "=r"(ww[1]), "=r"(ww[2]), "=r"(ww[3])
+                     : "r"(query_at(rr))
+                     : "memory");
         float f[8], big = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -921,10 +936,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           o4[c] = h2u(__floats2half2_rn(f[2 * c] * mul, f[2 * c + 1] * mul));
-        const uint32_t at = smem_s + C::off_q + i * C::kTile + (ql >> 3) * (kStep * 128) +
-                            rr * 128 + (((ql & 7) ^ (rr & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o4[0]), "r"(o4[1]),
-                     "r"(o4[2]), "r"(o4[3])
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(query_at(rr)), "r"(o4[0]),
+                     "r"(o4[1]), "r"(o4[2]), "r"(o4[3])
                      : "memory");
         // (never 0: a hidden column's -inf stays -inf)
         if (ql == 0)
@@ -950,11 +963,8 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
           bar_arrive_warp(bar_ie(item));
         }
         if (!it) break;
-        uint4 w0[LR / 2], w1[LR / 2];
-        load_queries(it, 0, w0);
-        load_queries(it, 1, w1);
-        store_queries(0, w0);
-        store_queries(1, w1);
+        load_queries(it);
+        scale_queries();
         queries_in();
       }
       const int row_first = it->row_first + i * 128, rows = it->rows;
@@ -1127,26 +1137,22 @@ paged_chunk_kernel(const __grid_constant__ ChunkArgs a) {
       }
       if (!ok) break;
 
-      // the next item's queries are on their way while the last sums are added,
-      // and its first scores are computed during this item's output.  Only the
-      // next item, though: this one still holds its entry of the ring, which the
-      // list refills once all have let go, so a tile that skipped on from here
-      // past items without rows for it could wait for itself.
+      // the next item's queries come in while the last sums are added (this item's scores
+      // are all there, so its own are not needed any more), and its first scores are
+      // computed during this item's output.  Only the next item, though: this one still
+      // holds its entry of the ring, which the list refills once all have let go, so a
+      // tile that skipped on from here past items without rows for it could wait for
+      // itself.
       const uint32_t this_item = item++;
       const Item *next = take_item(item);
       if (next && !has_rows(next)) next = nullptr;  // taken up after the release
-      {
-        uint4 w[LR / 2];
-        if (next) load_queries(next, 0, w);
-        if (!(ok = wait_warp(bar_o(i), on++ & 1))) break;
-        tc_fence_after();
-        if (next) {
-          store_queries(0, w);
-          load_queries(next, 1, w);
-          store_queries(1, w);
-          queries_in();
-        }
+      if (next) {
+        load_queries(next);
+        scale_queries();
+        queries_in();
       }
+      if (!(ok = wait_warp(bar_o(i), on++ & 1))) break;
+      tc_fence_after();
       // ---- output of the tile's steps [j0, j1)
       const bool whole = j0 == 0 && j1 == it->steps;
       const int64_t t = it->row0 + (in ? row / p.rg : 0);
