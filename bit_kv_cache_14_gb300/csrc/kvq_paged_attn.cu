@@ -4,17 +4,17 @@
 // Both forms run the same kernels: a row sees the tokens up to a position of its own,
 // and a cross row's is the last.  Cross attention on a GB300: 32 encoders of 1365 to
 // 4096 tokens, four beams of four heads each, 4 bits: 68 us (118 MB); 2 x 2048 rows
-// over 16384 tokens, 32 and 8 heads, 4 bits: 805 us = 1366 TFLOP/s, 73 % of the measured
+// over 16384 tokens, 32 and 8 heads, 4 bits: 762 us = 1443 TFLOP/s, 77 % of the measured
 // rate.  (For 9 to 32 rows a tcgen05 kernel with tokens and channels as the MMA rows was
 // built: 96 us for 16 rows where the split kernel takes 77, 130 to 138 for 20 to 32 where
-// the chunk kernel takes 153, 186 for 171 at 8 bits; not kept.)
+// the chunk kernel takes 120, 186 for 146 at 8 bits; not kept.)
 //
 // A sequence's rows are its new tokens times the query heads of one KV head.
 // Up to 16 rows the cache's bytes bound the time and the split kernel
 // (kvq_paged_rows.cu) reads them once, at 8 or 16 rows an MMA tile; from there
 // on the tcgen05 kernel (kvq_paged_chunk.cu) takes the sequence (32 sequences of
 // 8192 tokens, 4 new ones of 4 heads each, 4 bits: 128 us split, 223 us tcgen05;
-// 8 new ones: 226 us there).  Lengths are on the device, so a call whose
+// 8 new ones: 203 us there).  Lengths are on the device, so a call whose
 // max_tokens allows both launches both, and each kernel passes over the other's
 // sequences.
 #include "kvq_paged.cuh"

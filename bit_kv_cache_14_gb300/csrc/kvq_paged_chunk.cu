@@ -26,8 +26,9 @@
 // tiles, which both query tiles use.  Measured on a GB300, 32 query and 8 KV heads
 // of 128, 4 bits: 4096 tokens over 32768, 1424 us = 1448 TFLOP/s, 76 % of the
 // measured matrix rate (1510 us back to back for seconds, at a lower clock; 1583
-// at 2 bits, 1644 at 8, 1253 with heads of 64); four times 512 over 8192, 253 us =
-// 1050 TFLOP/s; 64 tokens alone, 22 us.
+// at 2 bits, 1644 at 8, 1253 with heads of 64); four times 512 over 8192, 224 us =
+// 1190 TFLOP/s; 64 tokens alone, 21 us.  Cross attention of 2 x 2048 rows over 16384
+// tokens: 762 us = 1443 TFLOP/s, 77 %.
 //
 // What made the difference: no role may spill (a spilled MMA thread needed 200
 // clocks an instruction instead of 64), role code has to be small or rolled (five

@@ -740,16 +740,6 @@ class PagedKVCache:
         """Causal attention of q [n_tokens][n_q_heads][head_dim], the rows of
         the batch's newest tokens, over everything their sequences hold (write
         those tokens first).  Returns [n_tokens][n_q_heads][head_dim]."""
-        return self._attention(self._attend, q, batch, out, scale, stream)
-
-    def cross_attend(self, q: torch.Tensor, batch: PagedBatch, out: torch.Tensor | None = None,
-                     scale: float | None = None, stream=None) -> torch.Tensor:
-        """Attention of q [n_tokens][n_q_heads][head_dim] where every row sees
-        all seq_lens tokens of its sequence (an encoder's states), however many
-        rows that has.  Returns [n_tokens][n_q_heads][head_dim]."""
-        return self._attention(self._cross, q, batch, out, scale, stream)
-
-    def _attention(self, fn, q, batch, out, scale, stream) -> torch.Tensor:
         qs = self._rows(q, batch, self.cfg.n_q_heads)
         if out is not None:
             self._rows(out, batch, self.cfg.n_q_heads)
@@ -759,7 +749,25 @@ class PagedKVCache:
                               device=self.device)
         else:
             out = self._output_on(stream, (batch.n_tokens,) + self._q_row)
-        self._call(fn, batch, stream, q.data_ptr(), qs, out.data_ptr(),
+        self._call(self._attend, batch, stream, q.data_ptr(), qs, out.data_ptr(),
+                   self._scale if scale is None else scale, self._ws_ptr, self.ws_bytes)
+        return out
+
+    def cross_attend(self, q: torch.Tensor, batch: PagedBatch, out: torch.Tensor | None = None,
+                     scale: float | None = None, stream=None) -> torch.Tensor:
+        """Attention of q [n_tokens][n_q_heads][head_dim] where every row sees
+        all seq_lens tokens of its sequence (an encoder's states), however many
+        rows that has.  Returns [n_tokens][n_q_heads][head_dim]."""
+        qs = self._rows(q, batch, self.cfg.n_q_heads)
+        if out is not None:
+            self._rows(out, batch, self.cfg.n_q_heads)
+            _ptr(out)
+        elif stream is None:
+            out = torch.empty((batch.n_tokens,) + self._q_row, dtype=self.dtype,
+                              device=self.device)
+        else:
+            out = self._output_on(stream, (batch.n_tokens,) + self._q_row)
+        self._call(self._cross, batch, stream, q.data_ptr(), qs, out.data_ptr(),
                    self._scale if scale is None else scale, self._ws_ptr, self.ws_bytes)
         return out
 
