@@ -345,38 +345,74 @@ paged_read_kernel(const __grid_constant__ Paged p, uint16_t *k, uint16_t *v) {
 
 // A warp copies 4 KB of a page at a time, its lanes eight 16-byte vectors each, and
 // reads the next piece's page numbers meanwhile.  HBM bounds it: 3400 pages of 80 KB,
-// 557 MB in and out, 82 us = 6.8 TB/s, the copy rate.
+// 557 MB in and out, 87.6 us = 6.4 TB/s, 94 % of the copy rate; 40000 pages 984 us = 6.7.
+//
+// The list ends at its first negative pair, which may stand anywhere and with any pairs
+// behind it, so each block looks at every pair up to those it is copying, 2048 a turn,
+// while its loads are on their way; what is stored is decided after that.  Blocks of 16
+// warps, so that few read the list (pages of 768 bytes, 200000 of them: 101 us, 125 with
+// 8 warps, 60 without a look); eight neighbouring pieces to a block, so that a short list
+// is on all SMs (60 pages 3.1 us, 2.9 without a look).
 constexpr int kCopyVecs = 8, kCopyBytes = 32 * 16 * kCopyVecs;
-__global__ void __launch_bounds__(kIoThreads)
-paged_copy_kernel(const __grid_constant__ Paged p, const int2 *copies, int64_t n) {
-  const int lane = threadIdx.x & 31;
-  const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
-  const int64_t step = (int64_t)gridDim.x * (kIoThreads / 32);
-  int64_t u = (int64_t)blockIdx.x * (kIoThreads / 32) + (threadIdx.x >> 5);
-  auto pair_of = [&](int64_t piece) {
-    const int64_t k = piece / pieces;
-    return k < n ? __ldg(copies + k) : make_int2(-1, -1);
+constexpr int kCopyThreads = 512, kCopyLook = 4, kCopyGroup = 8, kCopyGroups = 2;
+static_assert(kCopyGroup * kCopyGroups * 32 == kCopyThreads, "a warp a piece");
+__global__ void __launch_bounds__(kCopyThreads, 2)
+paged_copy_kernel(const __grid_constant__ Paged p, const int2 *copies, uint32_t n) {
+  __shared__ uint32_t found;  // the least negative pair's number
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t pieces = (uint32_t)((p.page_bytes + kCopyBytes - 1) / kCopyBytes);
+  // the warp's piece, as pair k and place `off` in its page, and the block's first one
+  const uint32_t first = blockIdx.x * kCopyGroup, row = gridDim.x * kCopyGroup;
+  const uint32_t u = first + warp / kCopyGroup * row + warp % kCopyGroup;
+  uint32_t k = u / pieces, off = u % pieces, k0 = first / pieces, off0 = first % pieces;
+  const uint32_t step = row * kCopyGroups, step_k = step / pieces, step_off = step % pieces;
+  auto advance = [&](uint32_t &kk, uint32_t &oo) {
+    kk += step_k;
+    oo += step_off;
+    if (oo >= pieces) oo -= pieces, ++kk;
   };
-  int2 c = pair_of(u);
-  while (c.x >= 0) {
-    const int64_t at = u % pieces * kCopyBytes + lane * 16;
-    u += step;
-    const int2 next = pair_of(u);
-    if (c.x >= p.n_pages || c.y < 0 || c.y >= p.n_pages) {
-      if (lane == 0) paged_error(p, KVQ_EPAGE);
-    } else if (c.x != c.y) {
-      const uint8_t *src = p.pages + c.x * p.page_bytes + at;
-      uint8_t *dst = p.pages + c.y * p.page_bytes + at;
-      uint4 v[kCopyVecs];
+  if (tid == 0) found = n;
+  auto pair_at = [&](uint32_t i) { return i < n ? __ldg(copies + i) : make_int2(-1, -1); };
+  uint32_t seen = 0, end = n;  // pairs looked at; where the list ends, as far as is known
+  int2 c = pair_at(k);
+  do {
+    const bool pages = c.x >= 0 && c.x < p.n_pages && c.y >= 0 && c.y < p.n_pages;
+    const int64_t at = (int64_t)off * kCopyBytes + lane * 16;
+    const uint8_t *src = p.pages + c.x * p.page_bytes + at;
+    uint8_t *dst = p.pages + c.y * p.page_bytes + at;
+    int left = pages && c.x != c.y ? (int)min(p.page_bytes - at, (int64_t)kCopyBytes) : 0;
+    uint4 v[kCopyVecs];
+#pragma unroll
+    for (int i = 0; i < kCopyVecs; ++i)
+      if (i * 512 < left) v[i] = *reinterpret_cast<const uint4 *>(src + i * 512);
+    const uint32_t mine = k;
+    advance(k, off);
+    const int2 next = pair_at(k);
+    // (the same for the whole block; no warp's pair is behind k0 + step_k + 1)
+    const uint32_t need = min(k0 + step_k + 2, n);
+    while (seen < need && end == n) {
+      uint32_t least = n;
+#pragma unroll
+      for (int i = kCopyLook - 1; i >= 0; --i) {
+        const uint32_t j = seen + i * kCopyThreads + tid;
+        if (j < n && __ldg(&copies[j].x) < 0) least = j;
+      }
+      if (__syncthreads_or(least < n)) {
+        if (least < n) atomicMin(&found, least);
+        __syncthreads();
+        end = found;
+      }
+      seen += kCopyLook * kCopyThreads;
+    }
+    if (mine < end) {
+      if (!pages && lane == 0) paged_error(p, KVQ_EPAGE);
 #pragma unroll
       for (int i = 0; i < kCopyVecs; ++i)
-        if (at + i * 512 < p.page_bytes) v[i] = *reinterpret_cast<const uint4 *>(src + i * 512);
-#pragma unroll
-      for (int i = 0; i < kCopyVecs; ++i)
-        if (at + i * 512 < p.page_bytes) *reinterpret_cast<uint4 *>(dst + i * 512) = v[i];
+        if (i * 512 < left) *reinterpret_cast<uint4 *>(dst + i * 512) = v[i];
     }
     c = next;
-  }
+    advance(k0, off0);
+  } while (k0 < end);
 }
 
 // Warps of a call: rows x groups of `per` heads.
@@ -432,10 +468,14 @@ cudaError_t launch_paged_read(const Paged &p, void *k, void *v, cudaStream_t st)
 
 cudaError_t launch_paged_copy(const Paged &p, const int32_t *copies, int64_t n, int num_sms,
                               cudaStream_t st) {
+  // Two blocks an SM at a time.  Twice as many are faster where a block copies long for
+  // each pair it looks at (3400 pages of 80 KB: 87.6 us, 91.5 with two), slower where it
+  // does not (100000 pages of 5 KB: 162 us with two, 221 with four).
   const int64_t pieces = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
-  const int64_t blocks = (n * pieces + kIoThreads / 32 - 1) / (kIoThreads / 32);
-  paged_copy_kernel<<<(unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8), kIoThreads, 0, st>>>(
-      p, reinterpret_cast<const int2 *>(copies), n);
+  const int64_t blocks = (n * pieces + kCopyGroup - 1) / kCopyGroup;
+  const int64_t most = (int64_t)num_sms * (pieces >= 8 ? 4 : 2);
+  paged_copy_kernel<<<(unsigned)(blocks < most ? blocks : most), kCopyThreads, 0, st>>>(
+      p, reinterpret_cast<const int2 *>(copies), (uint32_t)n);
   return cudaGetLastError();
 }
 

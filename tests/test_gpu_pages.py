@@ -300,6 +300,31 @@ def test_more_pairs_than_pages():
     assert torch.equal(cache.pages.view(2, -1)[0], cache.pages.view(2, -1)[1])
 
 
+@pytest.mark.parametrize("d,bits,page,hkv", [(64, 2, 16, 1), (128, 4, 64, 4)])
+@pytest.mark.parametrize("n,gap,behind", [(0, 1, 1), (1, 1, 1), (0, 3, 300), (7, 1, 60),
+                                          (300, 40, 1000), (4095, 1, 900), (4096, 1, 900),
+                                          (4000, 200, 4000)])
+def test_copies_end_at_the_first_negative_pair(d, bits, page, hkv, n, gap, behind):
+    """Pairs behind the list's end that would really copy: another list's, as in a
+    buffer used again.  All pages named behind it are left alone, wherever the end lies
+    and however the list is shared among warps."""
+    n_pages = n + behind + 9
+    cache = kvq.PagedKVCache(kvq.make_paged_config(hkv, hkv, d, bits, page, n_pages))
+    gen = torch.Generator("cuda").manual_seed(n)
+    cache.pages.random_(0, 256, generator=gen)
+    want = cache.pages.clone().view(n_pages, -1)
+    ids = torch.randperm(n_pages, generator=gen, device="cuda").to(torch.int32)
+    src = ids[torch.randint(0, 9, (n + behind,), generator=gen, device="cuda")]
+    pairs = torch.stack([src, ids[9:]], 1)
+    ends = torch.full((gap, 2), -1, dtype=torch.int32, device="cuda")
+    ends[:, 0] = torch.tensor([-1, -7, -2 ** 31] * gap, dtype=torch.int32)[:gap].cuda()
+    ends[:, 1] = ids[-gap:]     # (a negative pair names a page to copy to, too)
+    cache.copy_pages(torch.cat([pairs[:n], ends, pairs[n:]]))
+    want[pairs[:n, 1].long()] = want[pairs[:n, 0].long()]
+    assert torch.equal(cache.pages.view(n_pages, -1), want)
+    assert cache.device_status() == 0
+
+
 # ---- with the cache -------------------------------------------------------------
 
 def test_forks_write_apart_and_compaction_keeps_every_token():
