@@ -53,6 +53,13 @@ __device__ __forceinline__ void table_error(const Table &t, int code) {
 __device__ __forceinline__ int entries_of(const Table &t, int64_t n) {
   return n <= 0 ? 0 : (int)min((n + t.page - 1) >> t.page_log, t.width);
 }
+// What is wrong with a sequence of len tokens, recorded by `one` thread: nothing is made
+// of such a length, and its row stays as it is.
+__device__ __forceinline__ bool bad_length(const Table &t, int len, bool one) {
+  const bool bad = len < 0 || len > t.width * t.page;
+  if (bad && one) table_error(t, len < 0 ? KVQ_EINVAL : KVQ_EPAGE);
+  return bad;
+}
 
 // Takes a holder off page id; the last one frees it.  Called by whole warps, with
 // `on` the lanes that do.
@@ -284,7 +291,7 @@ pages_drop_kernel(const __grid_constant__ Table t, const int32_t *tokens) {
   const Stretch p = row_of_warp(t);
   if (p.b >= t.B) return;
   const int drop = tokens[p.b], len = t.lens[p.b];
-  if (drop <= 0 || len <= 0) return;
+  if (bad_length(t, len, p.s == 0 && lane == 0) || drop <= 0 || len == 0) return;
   const int left = max(len - drop, 0);
   const int e0 = entries_of(t, left), e1 = entries_of(t, len);
   int32_t *row = t.table + p.b * t.width;
@@ -314,16 +321,15 @@ pages_gather_kernel(const __grid_constant__ Table t, const int32_t *parents) {
   grid_dep_wait();
   const Stretch p = row_of_warp(t);
   if (p.b >= t.B) return;
-  const int parent = parents[p.b];
-  if (parent == p.b || parent >= t.B || parent < -1) {
-    if (p.s == 0 && lane == 0) {
-      if (parent != p.b) table_error(t, KVQ_EINVAL);
-      t.held[p.b] = -1;  // stays as it is
-    }
+  const int parent = parents[p.b], len = t.lens[p.b];
+  const bool one = p.s == 0 && lane == 0, known = parent >= -1 && parent < t.B;
+  if (!known && one) table_error(t, KVQ_EINVAL);
+  const int to = known && parent >= 0 ? t.lens[parent] : 0;
+  if (bad_length(t, len, one) || !known || parent == p.b || bad_length(t, to, one)) {
+    if (one) t.held[p.b] = -1;  // stays as it is
     return;
   }
-  const int to = parent < 0 ? 0 : t.lens[parent];
-  const int old = entries_of(t, t.lens[p.b]), now = entries_of(t, to);
+  const int old = entries_of(t, len), now = entries_of(t, to);
   const int32_t *src = t.table + max(parent, 0) * t.width, *row = t.table + p.b * t.width;
   for (int e = p.s * 32 + lane; e < now; e += t.stretches * 32) {
     const int id = src[e];
@@ -334,8 +340,7 @@ pages_gather_kernel(const __grid_constant__ Table t, const int32_t *parents) {
     else
       table_error(t, KVQ_EPAGE);
   }
-  if (p.s == 0 && lane == 0)
-    t.held[p.b] = old, t.held[t.B + p.b] = now, t.held[2 * t.B + p.b] = to;
+  if (one) t.held[p.b] = old, t.held[t.B + p.b] = now, t.held[2 * t.B + p.b] = to;
 }
 __global__ void __launch_bounds__(kRowThreads)
 pages_replace_kernel(const __grid_constant__ Table t) {
@@ -375,9 +380,8 @@ pages_count_kernel(const __grid_constant__ Table t) {
   grid_dep_wait();
   const Stretch p = row_of_warp(t);
   if (p.b >= t.B) return;
-  const int64_t len = t.lens[p.b];
-  if (p.s == 0 && lane == 0 && (len < 0 || len > t.width * t.page))
-    table_error(t, len < 0 ? KVQ_EINVAL : KVQ_EPAGE);
+  const int len = t.lens[p.b];
+  bad_length(t, len, p.s == 0 && lane == 0);
   const int held = entries_of(t, len);
   int32_t *row = t.table + p.b * t.width;
   for (int64_t e = p.s * 32 + lane; e < t.width; e += t.stretches * 32) {
@@ -487,14 +491,18 @@ pages_rename_kernel(const __grid_constant__ Table t, const int2 *copies, int64_t
   if (blockIdx.x < row_blocks) {
     const Stretch p = row_of_warp(t);
     if (p.b >= t.B) return;
-    const int held = entries_of(t, t.lens[p.b]);
+    // (of a length that is none, what entries are pages follow them all the same)
+    const int len = t.lens[p.b];
+    const bool bad = bad_length(t, len, p.s == 0 && lane == 0);
+    const int held = bad ? (int)t.width : entries_of(t, len);
     int32_t *row = t.table + p.b * t.width;
     for (int e = p.s * 32 + lane; e < held; e += t.stretches * 32) {
       const int id = row[e];
-      if (id < 0 || id >= t.n_pages || (snap[id >> 5].x >> (id & 31) & 1))
-        table_error(t, id < 0 || id >= t.n_pages ? KVQ_EPAGE : KVQ_EINVAL);
-      else if (id >= front)
+      if (id < 0 || id >= t.n_pages || (snap[id >> 5].x >> (id & 31) & 1)) {
+        if (!bad) table_error(t, id < 0 || id >= t.n_pages ? KVQ_EPAGE : KVQ_EINVAL);
+      } else if (id >= front) {
         row[e] = moved_to(id);
+      }
     }
     return;
   }

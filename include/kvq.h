@@ -598,8 +598,9 @@ int kvq_read_status(int32_t *dev_status, void *stream);
  * on one table never run at the same time.
  *
  * What the device arrays say is checked there, and goes to the status word: an
- * entry that is no page (KVQ_EPAGE, skipped), a negative length or holder counts
- * that do not agree with the tables (KVQ_EINVAL).
+ * entry that is no page (KVQ_EPAGE, skipped), a negative length (KVQ_EINVAL) or one
+ * beyond the table (KVQ_EPAGE; such a sequence stays as it is, and none becomes it),
+ * holder counts that do not agree with the tables (KVQ_EINVAL).
  * Every call returns KVQ_OK, KVQ_EINVAL (null, sizes), KVQ_EUNSUPPORTED, KVQ_EALIGN
  * or KVQ_ECUDA, and what is said there.
  */

@@ -220,6 +220,43 @@ def test_entries_that_are_no_pages():
     assert tab.device_status() == kvq.KVQ_EINVAL
 
 
+@pytest.mark.parametrize("bad", (-1, -4, -2 ** 31, 8 * 16 + 1, 2 ** 31 - 1))
+def test_lengths_that_are_none(bad):
+    """A negative length, or one beyond the table: every call that meets it says so and
+    leaves that sequence as it is; the others get what they were to."""
+    code = kvq.KVQ_EINVAL if bad < 0 else kvq.KVQ_EPAGE
+    m, tab = both(50, 16, 4, 8)
+    reserve(m, tab, [20, 35, 40, 0])
+    tab.seq_lens[1] = bad
+
+    def check(status):
+        assert tab.device_status() == status
+        true, m.lens[1] = m.lens[1], bad
+        m.check(tab)
+        m.lens[1] = true
+
+    for tokens in ([1, 5, 17, 0], [0, 0, 0, 0], [0, 2 ** 31 - 1, 3, 9]):
+        tab.drop(i32(tokens))
+        m.drop([0 if b == 1 else n for b, n in enumerate(tokens)])
+        check(code)
+    for parents, want in (([0, 1, 1, 0], [0, 1, 2, 0]),   # a parent without a length
+                          ([0, 0, 2, -1], [0, 1, 2, -1]),  # itself without one
+                          ([2, -1, 0, 0], [2, 1, 0, 0])):
+        tab.select(i32(parents))
+        m.select(want)
+        check(code)
+    m.drop([99, 0, 99, 99])
+    tab.drop(i32([99, 0, 99, 99]))
+    check(code)
+    moves = m.compact()                      # pages of all rows move, also that one's
+    assert moves and any(to in m.rows[1] for _, to in moves)
+    got = tab.compact()
+    assert np.array_equal(got.cpu().numpy(), pairs_of(moves, 25))
+    check(code)
+    tab.seq_lens[1] = m.lens[1]              # put right, the tables agree again
+    reserve(m, tab, [1, 1, 1, 1])
+
+
 def test_tables_taken_over():
     """Given tables with garbage behind each sequence's last entry."""
     m, _ = both(60, 32, 4, 6)
