@@ -204,9 +204,8 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
     const int64_t pairs = (int64_t)c0 + c1;
     place = (int)(block_scan<kReserveWarps>(pairs, sums, n_copies) - pairs);
   }
-  if (!fail && total > free) {
-    // not enough: the holds go back
-    if (tid == 0) table_error(t, KVQ_ECAPACITY);
+  // the holds go back, and the call hands out nothing
+  auto give_back = [&]() {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -215,11 +214,18 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (claim[i]) atomicAdd(&t.refs[id[i]], 1);
+  };
+  auto outputs = [&]() {
+    for (int i = tid; i <= t.B; i += kReserveThreads) cu_call[i] = fail ? 0 : cu[i];
+    for (int i = tid; i < t.B; i += kReserveThreads)
+      if (fail || i >= n_copies) copies[i] = make_int2(-1, -1);
+  };
+  if (!fail && total > free) {  // not enough
+    if (tid == 0) table_error(t, KVQ_ECAPACITY);
+    give_back();
     fail = true;
   }
-  for (int i = tid; i <= t.B; i += kReserveThreads) cu_call[i] = fail ? 0 : cu[i];
-  for (int i = tid; i < t.B; i += kReserveThreads)
-    if (fail || i >= n_copies) copies[i] = make_int2(-1, -1);
+  outputs();
   if (fail) return;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -271,7 +277,31 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
     done += found;
     hint = w0;
   }
-  if (tid == 0) t.head->hint = hint;
+  if (done >= n) {
+    if (tid == 0) t.head->hint = hint;
+    return;
+  }
+  // the map holds fewer free pages than the head says: those handed out go back
+  if (tid == 0) table_error(t, KVQ_EINVAL), t.head->free = free;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = b0 + i;
+    if (i >= per || b >= t.B) break;
+    int32_t *row = t.table + b * t.width + entry[b];
+    const int64_t got = min(need[i], done - first[b]);
+    for (int64_t k = 0; k < got; ++k) {
+      const int page = row[k];
+      row[k] = k == 0 ? from[b] : -1;
+      if (page < 0 || page >= t.n_pages) continue;  // (a bit behind the last page's)
+      t.refs[page] = 0;
+      atomicOr(&t.map[page >> 5], 1u << (page & 31));
+    }
+    if (rows[i] > 0) t.lens[b] = (int)len[i];
+  }
+  give_back();
+  fail = true;
+  outputs();
 }
 
 // ---- kernels over the rows: a warp takes every `stretches`-th stretch of a row ----

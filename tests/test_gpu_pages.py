@@ -257,6 +257,31 @@ def test_lengths_that_are_none(bad):
     reserve(m, tab, [1, 1, 1, 1])
 
 
+@pytest.mark.parametrize("B", (6, 1500))
+@pytest.mark.parametrize("forks", (False, True))
+def test_a_free_count_beyond_the_map(B, forks):
+    """The head of the state says that more pages are free than the map holds (it was
+    written to from outside): reported, and as with too few pages nothing changes."""
+    n_pages = B + 40
+    m, tab = both(n_pages, 16, B, 60)
+    reserve(m, tab, [20, 0, 0] + [16] * (B - 3))
+    if forks:
+        p = [0, 0, 0] + list(range(3, B))
+        m.select(p)
+        tab.select(i32(p))
+    free = int(tab.free_pages)
+    n = [1 if forks else 0, 2 if forks else 0, 16 * free, 16] + [0] * (B - 4)
+    out = torch.full((B, 2), 7, dtype=torch.int32, device="cuda"), i32([9] * (B + 1))
+    tab.free_pages.fill_(2 * n_pages)
+    tab.reserve(i32(cu_of(n)), out=out)
+    assert tab.device_status() == kvq.KVQ_EINVAL
+    assert (out[0] == -1).all() and (out[1] == 0).all()
+    assert int(tab.free_pages) == 2 * n_pages
+    tab.free_pages.fill_(free)
+    m.check(tab)
+    reserve(m, tab, [1] * 4 + [0] * (B - 4))
+
+
 def test_tables_taken_over():
     """Given tables with garbage behind each sequence's last entry."""
     m, _ = both(60, 32, 4, 6)
