@@ -50,6 +50,7 @@ struct VerifyArgs {
   int64_t T;
   int B, V, splits;
   int row_pieces, pieces, n_parts;  // pieces of a row, of a part; parts of a row
+  int padded;  // rows that no sequence owns are written, too
 };
 
 __device__ __forceinline__ void verify_error(const VerifyArgs &a, int code) {
@@ -402,8 +403,16 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
   bool bad = a.cu[0] < 0 || a.cu[a.B] > a.T;
   for (int i = tid; i < a.B; i += kVerifyThreads) bad |= a.cu[i + 1] < a.cu[i];
   bad = __syncthreads_or(bad);
+  // after the wait: rows that no sequence owns (where bad, all of them)
+  auto unowned = [&]() {
+    if (!a.padded || share != 0) return;
+    const int64_t from = bad ? a.T : a.cu[0], to = bad ? 0 : a.cu[a.B];
+    for (int64_t t = b * kVerifyThreads + tid; t < a.T; t += a.B * kVerifyThreads)
+      if (t < from || t >= to) a.out[t] = -1, a.logprobs[t] = 0.0f;
+  };
   if (bad || n == 0) {
     grid_dep_wait();
+    unowned();
     if (share == 0 && tid == 0) {
       if (bad) verify_error(a, KVQ_EINVAL);
       a.accepted[b] = 0;
@@ -449,6 +458,7 @@ verify_draw_kernel(const __grid_constant__ VerifyArgs a) {
     }
   }
   if (!waited) grid_dep_wait();
+  unowned();
   __syncthreads();
   const int kept = stop;
   const int64_t t = r0 + kept;
@@ -643,29 +653,11 @@ int check_drafts(const kvq_draft_batch *d) {
   return KVQ_OK;
 }
 
-}  // namespace
-}  // namespace kvq
-
-using namespace kvq;
-
-extern "C" {
-
-int kvq_verify_workspace_bytes(const kvq_draft_batch *batch, size_t *bytes) {
-  if (!bytes || !batch) return KVQ_EINVAL;
-  if (batch->n_seqs < 1 || batch->vocab < 1 || batch->n_tokens < 0) return KVQ_EINVAL;
-  if (batch->dtype != KVQ_F16 && batch->dtype != KVQ_BF16 && batch->dtype != KVQ_F32)
-    return KVQ_EINVAL;
-  if (batch->n_seqs > kMaxSeqs || batch->n_tokens > kMaxRows || batch->vocab > kMaxVocab)
-    return KVQ_EUNSUPPORTED;
-  *bytes = verify_bytes(batch->n_tokens, batch->vocab, batch->dtype);
-  return KVQ_OK;
-}
-
-int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t stride,
-                      const void *draft_logits, int64_t draft_stride, const float *temperature,
-                      const float *uniform, const float *noise, int64_t noise_stride,
-                      int32_t *out_tokens, int32_t *accepted, int32_t *dropped, float *logprobs,
-                      void *ws, size_t ws_bytes, void *stream) {
+int verify_drafts(bool padded, const kvq_draft_batch *batch, const void *logits, int64_t stride,
+                  const void *draft_logits, int64_t draft_stride, const float *temperature,
+                  const float *uniform, const float *noise, int64_t noise_stride,
+                  int32_t *out_tokens, int32_t *accepted, int32_t *dropped, float *logprobs,
+                  void *ws, size_t ws_bytes, void *stream) {
   const int r = check_drafts(batch);
   if (r != KVQ_OK) return r;
   if (!accepted || !dropped || !ws) return KVQ_EINVAL;
@@ -701,6 +693,7 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
   a.logprobs = logprobs;
   a.status = batch->dev_status;
   a.T = T;
+  a.padded = padded;
   a.B = batch->n_seqs;
   a.V = (int)V;
   // rows that all begin on a 16-byte vector have no lead
@@ -731,6 +724,45 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
   if (e != cudaSuccess) return KVQ_ECUDA;
   note_launch(n);
   return KVQ_OK;
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" {
+
+int kvq_verify_workspace_bytes(const kvq_draft_batch *batch, size_t *bytes) {
+  if (!bytes || !batch) return KVQ_EINVAL;
+  if (batch->n_seqs < 1 || batch->vocab < 1 || batch->n_tokens < 0) return KVQ_EINVAL;
+  if (batch->dtype != KVQ_F16 && batch->dtype != KVQ_BF16 && batch->dtype != KVQ_F32)
+    return KVQ_EINVAL;
+  if (batch->n_seqs > kMaxSeqs || batch->n_tokens > kMaxRows || batch->vocab > kMaxVocab)
+    return KVQ_EUNSUPPORTED;
+  *bytes = verify_bytes(batch->n_tokens, batch->vocab, batch->dtype);
+  return KVQ_OK;
+}
+
+int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t stride,
+                      const void *draft_logits, int64_t draft_stride, const float *temperature,
+                      const float *uniform, const float *noise, int64_t noise_stride,
+                      int32_t *out_tokens, int32_t *accepted, int32_t *dropped, float *logprobs,
+                      void *ws, size_t ws_bytes, void *stream) {
+  return verify_drafts(false, batch, logits, stride, draft_logits, draft_stride, temperature,
+                       uniform, noise, noise_stride, out_tokens, accepted, dropped, logprobs, ws, ws_bytes,
+                       stream);
+}
+
+int kvq_verify_drafts_padded(const kvq_draft_batch *batch, const void *logits, int64_t stride,
+                             const void *draft_logits, int64_t draft_stride,
+                             const float *temperature, const float *uniform, const float *noise,
+                             int64_t noise_stride, int32_t *out_tokens, int32_t *accepted,
+                             int32_t *dropped, float *logprobs, void *ws, size_t ws_bytes,
+                             void *stream) {
+  return verify_drafts(true, batch, logits, stride, draft_logits, draft_stride, temperature,
+                       uniform, noise, noise_stride, out_tokens, accepted, dropped, logprobs, ws, ws_bytes,
+                       stream);
 }
 
 }  // extern "C"

@@ -44,7 +44,7 @@ EXPORTS = (
     "kvq_paged_attention", "kvq_paged_status", "kvq_paged_cross_attention", "kvq_paged_copy",
     "kvq_read_status", "kvq_pages_state_bytes", "kvq_pages_recount", "kvq_pages_reserve",
     "kvq_pages_drop", "kvq_pages_select", "kvq_pages_compact", "kvq_verify_workspace_bytes",
-    "kvq_verify_drafts",
+    "kvq_verify_drafts", "kvq_verify_drafts_padded",
 )
 
 
@@ -158,6 +158,7 @@ def lib():
             L.kvq_verify_workspace_bytes.argtypes = [PD, PS]
             L.kvq_verify_drafts.argtypes = [PD, P, I64, P, I64, P, P, P, I64, P, P, P, P, P,
                                             ctypes.c_size_t, P]
+            L.kvq_verify_drafts_padded.argtypes = L.kvq_verify_drafts.argtypes
             L.kvq_last_launch_count.argtypes = []
             L.kvq_debug_stall_waits.argtypes = [ctypes.c_int64]
             L.kvq_debug_stall_waits.restype = None
@@ -870,7 +871,8 @@ class PageTable:
         """Pages for cu_tokens' new tokens; seq_lens grows by them.  Returns
         (copies, cu): int32 [n_seqs][2] for PagedKVCache.copy_pages, to run before
         the tokens are written, and int32 [n_seqs + 1] for the batch of the calls
-        that follow (cu_tokens, or zeros where pages did not suffice).  ``out``:
+        that follow, DraftVerifier.verify too (cu_tokens, or zeros where pages did not
+        suffice).  ``out``:
         the two tensors to fill."""
         cu = self._of_seqs(cu_tokens, self.n_seqs + 1)
         if out is None:
@@ -934,7 +936,7 @@ class DraftVerifier:
         self.ws_bytes = n.value
         self.ws = torch.zeros(n.value, dtype=torch.uint8, device=self.device)
         self.status = _zeroed(1, torch.int32, self.device)
-        self._verify, self._ws_ptr = lib().kvq_verify_drafts, self.ws.data_ptr()
+        self._verify, self._ws_ptr = lib().kvq_verify_drafts_padded, self.ws.data_ptr()
         self._status_ptr, self._code = self.status.data_ptr(), _LOGIT_DTYPES[dtype]
 
     def _rows(self, t: torch.Tensor, rows: int, dtype) -> int:
@@ -958,7 +960,9 @@ class DraftVerifier:
         exponential distribution.  Returns (tokens, accepted, dropped, logprobs):
         per row the drafts that stay, then the next token, then -1; per sequence the
         drafts that stay and those that do not (PageTable.drop); per row the
-        token's log probability."""
+        token's log probability.  Rows that no sequence has get -1 and 0.  cu_tokens
+        is the cu that PageTable.reserve returned: after a failed reservation nothing
+        is judged, and nothing is dropped."""
         device, index, i32, f32 = self.device, self._index, torch.int32, torch.float32
         T, B = tokens.numel(), cu_tokens.numel() - 1
         if B < 1 or B > self.n_seqs or T > self.n_tokens:

@@ -631,8 +631,10 @@ int kvq_pages_recount(const kvq_page_table *table, void *stream);
  *   copies int32 [n_seqs][2], 8-byte aligned: the copies to make before the tokens
  *     are written, for kvq_paged_copy; (-1, -1) behind the last.
  *   cu_call int32 [n_seqs+1], apart from cu_tokens: cu_tokens again, or zeros where
- *     the call failed; given to kvq_paged_write and kvq_paged_attention as
- *     cu_tokens, it makes a failed step write and attend to nothing.
+ *     the call failed; given as cu_tokens to every call of the step that follows
+ *     (kvq_paged_write, kvq_paged_attention, kvq_paged_cross_attention,
+ *     kvq_verify_drafts), it makes a failed step write, attend to and judge nothing,
+ *     so that no token is dropped that was not reserved.
  * All or nothing: where pages (KVQ_ECAPACITY) or table entries (KVQ_ECAPACITY) do
  * not suffice or the arrays are wrong (KVQ_EINVAL, KVQ_EPAGE), the status word says
  * so, nothing changes and there are no copies.
@@ -725,6 +727,16 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
                       const float *uniform, const float *noise, int64_t noise_stride,
                       int32_t *out_tokens, int32_t *accepted, int32_t *dropped, float *logprobs,
                       void *ws, size_t ws_bytes, void *stream);
+
+/* The same, and every row of out_tokens and logprobs is written: rows that no
+ * sequence owns (padding; all of them where no sequence is judged, or after a failed
+ * kvq_pages_reserve) get -1 and 0. */
+int kvq_verify_drafts_padded(const kvq_draft_batch *batch, const void *logits, int64_t stride,
+                             const void *draft_logits, int64_t draft_stride,
+                             const float *temperature, const float *uniform, const float *noise,
+                             int64_t noise_stride, int32_t *out_tokens, int32_t *accepted,
+                             int32_t *dropped, float *logprobs, void *ws, size_t ws_bytes,
+                             void *stream);
 
 /* Number of kernel launches the last successful call of this thread enqueued. */
 int kvq_last_launch_count(void);

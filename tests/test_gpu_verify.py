@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from bit_kv_cache_14_gb300 import build_lib, kvq
-from pages_util import cu_of, i32
+from pages_util import both, cu_of, i32
 from verify_util import call, check, expected
 
 pytestmark = pytest.mark.gpu
@@ -244,6 +244,96 @@ def test_padding_rows_are_left_alone():
     assert code == 0 and (out[5:] == 77).all() and (lp[5:] == 5).all()
     check((out, acc, drop, lp), expected(**a), [0, 3, 5], a["tokens"].cpu().numpy(),
           allow_close=0.5)
+
+
+def used_memory(T):
+    """Memory that the next outputs are likely to get, as a step before left it."""
+    held = [torch.full((T,), 7, dtype=torch.int32, device="cuda") for _ in range(12)]
+    del held
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,pad", [([3, 2], 4), ([1, 0, 4], 3000), ([0, 0], 9)])
+def test_rows_that_nobody_has(kind, n, pad):
+    """Padding, rows before the first sequence's, all rows where no pages were reserved
+    or cu_tokens is out of order: -1 and 0 from the binding."""
+    a = inputs(n, 90, BF16, kind, seed=2, pad=pad)
+    T, real = sum(n) + pad, cu_of(n)
+    v = kvq.DraftVerifier(len(n), T, 90, BF16)
+    used_memory(T)
+    got = call(v, **a)
+    assert v.device_status() == 0
+    check(got, expected(**a), real.tolist(), a["tokens"].cpu().numpy(), allow_close=0.5)
+    assert (got[0][sum(n):] == -1).all() and (got[3][sum(n):] == 0).all()
+    late = dict(a, cu=i32(real + 2))
+    used_memory(T)
+    got = call(v, **late)
+    assert v.device_status() == 0
+    assert (got[0][:2] == -1).all() and (got[3][:2] == 0).all()
+    assert (got[0][sum(n) + 2:] == -1).all() and (got[3][sum(n) + 2:] == 0).all()
+    for cu, status in ((0 * real, 0), (real[::-1].copy(), kvq.KVQ_EINVAL if sum(n) else 0),
+                       (real - 1, kvq.KVQ_EINVAL), (real + pad + 1, kvq.KVQ_EINVAL)):
+        used_memory(T)
+        got = call(v, **dict(a, cu=i32(cu)))
+        assert v.device_status() == status
+        assert (got[0] == -1).all() and not got[3].any() and not got[1].any() and not got[2].any()
+
+
+def test_a_captured_step_without_pages():
+    """A captured speculative step, replayed until the pool is used up and on: a step
+    that gets no pages gives no tokens and takes none back, and once a sequence has
+    ended the steps go on."""
+    page, H, d, B, V, n = 16, 1, 64, 3, 200, [4, 4, 4]
+    T = sum(n)
+    g = torch.Generator("cuda").manual_seed(0)
+    m, tab = both(7, page, B, 8)
+    cache = kvq.PagedKVCache(kvq.make_paged_config(H, H, d, 8, page, 7))
+    cache.pages.zero_()
+    a = inputs(n, V, F16, "model", seed=3)
+    ver = kvq.DraftVerifier(B, T, V, F16)
+    k = torch.randn(T, H, d, generator=g, device="cuda").half()
+    bufs = torch.empty(B, 2, dtype=torch.int32, device="cuda"), i32([0] * (B + 1))
+
+    def step():
+        copies, cu = tab.reserve(a["cu"], out=bufs)
+        cache.copy_pages(copies)
+        batch = tab.batch(cu, T, 4)
+        cache.write(k, k, batch)
+        x = cache.attend(k, batch)
+        res = ver.verify(a["logits"], a["tokens"], cu, a["draft"], a["temperature"],
+                         a["uniform"], a["noise"])
+        tab.drop(res[2])
+        return (x,) + res
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        tab.drop(i32([99] * B))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, tokens, kept, dropped, logs = step()
+    want = expected(**a)
+    failed = 0
+    for i in range(40):
+        graph.replay()
+        if m.reserve(n) is None:
+            failed += 1
+            assert tab.device_status() == kvq.KVQ_ECAPACITY
+            assert (tokens == -1).all() and not logs.any()
+            assert not kept.any() and not dropped.any()
+            m.check(tab)
+            if failed % 3 == 0:
+                m.drop([0, 99, 0])
+                tab.drop(i32([0, 99, 0]))
+        else:
+            assert tab.device_status() == 0
+            check((tokens, kept, dropped, logs), want, cu_of(n).tolist(),
+                  a["tokens"].cpu().numpy(), allow_close=0.5)
+            m.drop(dropped.tolist())
+        m.check(tab)
+    assert failed >= 3 and cache.device_status() == ver.device_status() == 0
 
 
 def test_no_rows_at_all():

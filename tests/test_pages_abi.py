@@ -161,6 +161,15 @@ def test_verify_refusals():
         assert bytes_of(_drafts(**kw)) == code
 
 
+def test_padded_verify_refuses_what_verify_refuses():
+    fn = kvq.lib().kvq_verify_drafts_padded
+    for kw in (dict(logits=None), dict(out=0x1000), dict(accepted=None), dict(stride=99),
+               dict(noise=0x2002), dict(ws=0x4008), dict(ws_bytes=8), dict(uniform=None)):
+        code = fn(ctypes.byref(_drafts()), *{**VERIFY, **kw}.values(), None)
+        assert code != E.KVQ_OK and code == _verify(_drafts(), **kw), kw
+    assert fn(None, *VERIFY.values(), None) == E.KVQ_EINVAL
+
+
 def test_workspace_grows_with_each_size():
     """A verifier made for the largest sizes has room for every smaller call."""
     n = ctypes.c_size_t()
