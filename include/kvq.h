@@ -716,9 +716,12 @@ int kvq_verify_workspace_bytes(const kvq_draft_batch *batch, size_t *bytes);
  * do cu_tokens that decrease, begin below 0 or end behind n_tokens: then no sequence is
  * judged, and outputs are left alone but for 0 accepted, 0 dropped.  A sequence without
  * rows gets those too.
- * Arithmetic: fp32, sums in fp32 in a fixed order; exponents of the drafts' tests
- * in 64 bits.  p and q are within 1e-6 (relative) of the exact ones, so numbers that
- * close to a border may fall on its other side.
+ * Arithmetic: fp32, sums in fp32 in a fixed order, exponents in two parts of fp32.
+ * A token t_i = (max x - x_i) / (T ln 2) powers of two below its row's likeliest has
+ * its probability within (t_i + 64 + vocab / 2^13) 2^-23 of the exact one (relative),
+ * in p and in q, so numbers that close to a border may fall on its other side.  In the
+ * sums and in the race a token with t_i beyond 126 counts as 0; as a draft it is
+ * judged like any other.
  * Errors: KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EALIGN, KVQ_ECAPACITY (ws too small),
  *   KVQ_ECUDA.
  */

@@ -246,6 +246,59 @@ def test_padding_rows_are_left_alone():
           allow_close=0.5)
 
 
+@pytest.mark.parametrize("kind", ("model", "lookup"))
+@pytest.mark.parametrize("V,most", [(50, 60), (5000, 60), (70001, 60), (700, 170)])
+def test_stated_arithmetic(kind, V, most):
+    """Drafts far below their rows' likeliest tokens, fp32: a number off p / q by the
+    stated bounds of p and of q (and its own rounding) is decided as the exact one.
+
+    A weight 2^-t: x - max and the product with log2(e) / T are rounded once each, so
+    its exponent is off by t 2^-23, itself by 0.7 of that, and the exponential by 2^-22
+    (2 units of 2^-23).  The sum's terms have those errors, 0.7 times their mean t, which
+    is below log2 V, and 2; a lane adds 4 * 32 pairs to a running sum whose reference
+    moves at most 4 times (16 + 10 units at most: roundings of half a unit, moves of 2 and
+    a half), five steps join the lanes (5), and a lane joins 1 / 32 of the at most
+    V / 1024 parts (2.5 units each: V / 2^13): 64 units cover the constants."""
+    B = 256
+    rng = np.random.default_rng(V)
+    x, y = (2.0 * rng.standard_normal((B, V)) for _ in range(2))
+    T = (0.5 + rng.random(B)).astype(np.float32)
+    c = rng.integers(0, V, B)
+    rows = np.arange(B)
+    x[rows, c] = y[rows, c] = -1e4
+    tp = rng.uniform(20, most, B)
+    tq = rng.uniform(0, tp - 18)
+    unit = T.astype(np.float64) * np.log(2)
+    x[rows, c] = x.max(1) - tp * unit
+    y[rows, c] = y.max(1) - tq * unit
+    x, y = x.astype(np.float32), y.astype(np.float32)
+
+    def exact(z):
+        t = (z.astype(np.float64) - z.max(1, keepdims=True)) / T[:, None].astype(np.float64)
+        e = np.exp(t)
+        return t[rows, c] - np.log(e.sum(1)), -t[rows, c] / np.log(2)
+
+    lp, ep = exact(x)
+    lq, eq = exact(y) if kind == "model" else (0.0, -64 - V / 2 ** 13)
+    bound = (ep + eq + 2 * (64 + V / 2 ** 13)) * 2.0 ** -23 + 2.0 ** -24
+    odds = np.exp(lp - lq)
+    # (a number below 2^-126 has fewer bits)
+    ok = (odds < 0.9) & (odds > 2.0 ** -120)
+    assert ok.sum() > B // 3
+    up = lambda a: np.repeat(a, 2, 0)  # noqa: E731
+    v = kvq.DraftVerifier(B, 2 * B, V, F32)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    noise = torch.ones(1, V, device="cuda").expand(B, V).contiguous()
+    for side, stays in ((1 - bound, 1), (1 + bound, 0)):
+        u = up((odds * side).astype(np.float32))
+        tokens = np.stack([0 * c, c], 1).reshape(-1).astype(np.int32)
+        _, accepted, _, _ = v.verify(
+            dev(up(x)), dev(tokens), i32(2 * np.arange(B + 1)),
+            dev(up(y)) if kind == "model" else None, dev(T), dev(u), noise)
+        assert (accepted.cpu().numpy()[ok] == stays).all()
+    assert v.device_status() == 0
+
+
 def used_memory(T):
     """Memory that the next outputs are likely to get, as a step before left it."""
     held = [torch.full((T,), 7, dtype=torch.int32, device="cuda") for _ in range(12)]
