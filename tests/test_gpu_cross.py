@@ -141,6 +141,20 @@ def test_missing_pages_and_lengths(rows):
     assert (neg == 0).all() and cache.device_status() == 0
 
 
+@pytest.mark.parametrize("rows", (1, 3, 12, 30, 70))
+@pytest.mark.parametrize("length", (65, 10 ** 6, 2 ** 31 - 1))
+def test_a_length_beyond_the_table_ends_with_it(rows, length):
+    """What is attended to is what the table holds: its 64 tokens, and the other
+    sequence's as ever."""
+    c = Cross([64, 50], [rows] * 2, 4, 1, 64, 4, 16, F16)
+    cache = c.filled()
+    out = cache.cross_attend(c.queries(), c.batch(kv=[length, 50]))
+    assert cache.device_status() == kvq.KVQ_EPAGE
+    c.check(out)
+    assert torch.equal(out, cache.cross_attend(c.queries(), c.batch()))
+    assert cache.device_status() == 0
+
+
 def test_queries_of_a_wider_tensor_and_any_scale():
     c = Cross([130, 260], [2, 50], 4, 2, 128, 8, 64, BF16)
     cache = c.filled()

@@ -86,6 +86,38 @@ def test_most_drafts_stay_or_none(kind):
     run_and_check(a, allow_close=0.5)
 
 
+def run_and_check_all(a):
+    """No sequence of the case has a decision that is too near to call (the 64-bit form
+    says so, for these seeds), so all of the call's outputs are compared."""
+    assert not any(close for _, _, close in expected(**a))
+    run_and_check(a, allow_close=0)
+
+
+@pytest.mark.parametrize("dtype", (F16, BF16, F32))
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V", (1, 2, 7, 100, 2047, 2049, 8191, 8193, 33333))
+def test_every_decision_against_64_bits(dtype, kind, V):
+    run_and_check_all(inputs([5, 1, 0, 9, 2, 3], V, dtype, kind, seed=V))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,V", [([1], 50), ([3] * 300, 200), ([40, 1], 1000), ([2] * 2048, 20),
+                                 ([0] * 9 + [4], 77), ([300], 64)])
+def test_every_decision_of_many_sequences(kind, n, V):
+    run_and_check_all(inputs(n, V, BF16, kind, seed=len(n)))
+
+
+@pytest.mark.parametrize("kind", ("model", "lookup"))
+def test_every_decision_where_drafts_stay_or_go(kind):
+    a = inputs([6] * 40, 500, F32, kind, seed=1, noise=0.02)
+    a["uniform"] *= 0.01
+    run_and_check_all(a)
+    a["uniform"] = 1.0 - 2.0 ** -24 - 0.0 * a["uniform"]
+    if kind == "model":
+        a["draft"] = torch.roll(a["logits"], 7, 1).contiguous()
+    run_and_check_all(a)
+
+
 def test_the_same_model_twice_keeps_everything():
     """q = p: every draft stays for any u < 1 (both sides are the same sums)."""
     a = inputs([9] * 30, 4097, BF16, "model", seed=2)
