@@ -135,7 +135,7 @@ pages_reserve_kernel(const __grid_constant__ Table t, const int32_t *cu, int2 *c
   const int b0 = tid * per;
   const int64_t cap = t.width * t.page;
   const int free = t.head->free;
-  int hint = t.head->hint;
+  int hint = max(t.head->hint, 0);
 
   // ---- what each sequence needs
   int rows[kPer], held[kPer], id[kPer];
@@ -453,7 +453,9 @@ pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copi
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_trigger();
   grid_dep_wait();
-  const int front = t.n_pages - t.head->free, front_word = front >> 5;
+  // (a count that is none leaves a front in range; the last block finds it out)
+  const int64_t live = (int64_t)t.n_pages - t.head->free;
+  const int front = (int)min(max(live, (int64_t)0), (int64_t)t.n_pages), front_word = front >> 5;
   const uint32_t front_bits = (1u << (front & 31)) - 1;  // of that word: before the front
   const int w0 = blockIdx.x * kMoveWords;
   // free pages before the block's words, and before the front, four words a load
@@ -484,7 +486,11 @@ pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copi
   const int here = (int)(before + block_scan<kMoveThreads / 32>(free, sums, total) - free);
   if (tid < kMoveWords) word_bits[tid] = bits, word_before[tid] = here;
   if (mine) reinterpret_cast<uint2 *>(t.rows)[w] = make_uint2(bits, (uint32_t)here);
-  if (blockIdx.x == 0 && tid == 0) t.head->moves = moves, t.head->front = front;
+  if (blockIdx.x == gridDim.x - 1 && tid == 0) {
+    const bool agree = before + total == t.head->free;
+    t.head->moves = moves, t.head->front = agree ? front : -1;
+    if (!agree) table_error(t, KVQ_EINVAL);
+  }
   __syncthreads();
   // a warp a word, a lane a page: a free one before the front, a live one behind
   for (int j = warp; j < kMoveWords && w0 + j < t.words; j += kMoveThreads / 32) {
@@ -492,8 +498,8 @@ pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copi
     const int f = word_before[j] + __popc(word & ((1u << lane) - 1));
     const int id = (w0 + j) * 32 + lane;
     const bool is_free = word >> lane & 1;
-    // (in range wherever the head's count is the map's)
     const int64_t k = id < front ? f : (int64_t)id - f - (front - moves);
+    // (in range wherever the head's count is the map's)
     if (k < 0 || k >= n_copies || id >= t.n_pages) continue;
     if (id < front && is_free) copies[k].y = id;
     if (id >= front && !is_free) copies[k].x = id;
@@ -504,12 +510,18 @@ pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copi
 }
 // Blocks [0, row_blocks): table entries; behind them: pages and the free map.
 __global__ void __launch_bounds__(kRowThreads)
-pages_rename_kernel(const __grid_constant__ Table t, const int2 *copies, int64_t n_copies,
+pages_rename_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copies,
                     int row_blocks) {
   const int lane = threadIdx.x & 31;
   grid_dep_trigger();
   grid_dep_wait();
   const int front = t.head->front, moves = t.head->moves;
+  if (front < 0) {  // the count and the map do not agree: nothing moves
+    for (int64_t k = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; k < n_copies;
+         k += (int64_t)gridDim.x * kRowThreads)
+      copies[k] = make_int2(-1, -1);
+    return;
+  }
   const uint2 *snap = reinterpret_cast<const uint2 *>(t.rows);
   auto moved_to = [&](int id) {  // of a live page behind the front
     const uint2 s = snap[id >> 5];

@@ -849,7 +849,7 @@ class PageTable:
 
     @property
     def free_pages(self) -> torch.Tensor:
-        """Number of free pages: int32 [1], on the device."""
+        """Number of free pages: int32 [1], on the device (to be read only)."""
         return self.state[:4].view(torch.int32)
 
     def batch(self, cu_tokens, n_tokens: int, max_tokens: int | None = None) -> PagedBatch:

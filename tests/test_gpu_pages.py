@@ -282,6 +282,29 @@ def test_a_free_count_beyond_the_map(B, forks):
     reserve(m, tab, [1] * 4 + [0] * (B - 4))
 
 
+@pytest.mark.parametrize("count", (0, 21, 25, 10 ** 6, -1, -2 ** 31, 2 ** 31 - 1))
+def test_compacting_with_a_free_count_that_is_none(count):
+    """Reported, and nothing moves; a reservation after it stays inside the pool."""
+    m, tab = both(60, 16, 3, 8)
+    reserve(m, tab, [100, 37, 90])
+    m.drop([99, 0, 0])
+    tab.drop(i32([99, 0, 0]))
+    free = int(tab.free_pages)
+    assert free not in (0, 21, 25)
+    tab.free_pages.fill_(count)
+    got = tab.compact()
+    assert tab.device_status() == kvq.KVQ_EINVAL
+    assert (got == -1).all()
+    tab.free_pages.fill_(free)
+    m.check(tab)
+    tab.free_pages.fill_(count)
+    tab.reserve(i32([0, 800, 1600, 2400]))       # more than there is, by any count
+    assert tab.device_status() != 0
+    tab.free_pages.fill_(free)
+    m.check(tab)
+    reserve(m, tab, [5, 5, 5])
+
+
 def test_tables_taken_over():
     """Given tables with garbage behind each sequence's last entry."""
     m, _ = both(60, 32, 4, 6)
