@@ -2,18 +2,27 @@
 // all of a sequence -- which kernel takes which sequence.
 //
 // Both forms run the same kernels: a row sees the tokens up to a position of its own,
-// and a cross row's is the last.  Cross attention on a GB300: 32 encoders of 1365 to
-// 4096 tokens, four beams of four heads each, 4 bits: 68 us (118 MB); 2 x 2048 rows
+// and a cross row's is the last.  Cross attention on a GB300: 32 encoders of 1515 to
+// 4096 tokens, four beams of four heads each, 4 bits: 68 us (118 MB); one row of four
+// heads each over 64 of 8192 tokens, 4 bits: 155 us = 64 % of the copy rate; 2 x 2048 rows
 // over 16384 tokens, 32 and 8 heads, 4 bits: 762 us = 1443 TFLOP/s, 77 % of the measured
-// rate.  (For 9 to 32 rows a tcgen05 kernel with tokens and channels as the MMA rows was
+// rate (809 us back to back for seconds, at a lower clock: 80 % of the sustained rate).
+//
+// Its errors are the causal call's, from operands rounded to fp16: against 64 bits, as a
+// share of the output's norm, fp16 with 122 to 219 rows at 2 bits 7.1e-4, of which 6.2e-4
+// are the keys' rounding and 2.1e-4 the output's; few rows 2.3e-4; bf16 1.7e-3, the
+// output's rounding.  Keys in two parts would take that away, for half as many matrix
+// operations again and 64 KB of shared memory that the operand tiles do not leave.
+//
+// (For 9 to 32 rows a tcgen05 kernel with tokens and channels as the MMA rows was
 // built: 96 us for 16 rows where the split kernel takes 77, 130 to 138 for 20 to 32 where
-// the chunk kernel takes 120, 186 for 146 at 8 bits; not kept.)
+// the chunk kernel took 120, 186 for 146 at 8 bits; not kept.)
 //
 // A sequence's rows are its new tokens times the query heads of one KV head.
 // Up to 16 rows the cache's bytes bound the time and the split kernel
 // (kvq_paged_rows.cu) reads them once, at 8 or 16 rows an MMA tile; from there
 // on the tcgen05 kernel (kvq_paged_chunk.cu) takes the sequence (32 sequences of
-// 8192 tokens, 4 new ones of 4 heads each, 4 bits: 128 us split, 223 us tcgen05;
+// 8192 tokens, 4 new ones of 4 heads each, 4 bits: 129 us split, 223 us tcgen05;
 // 8 new ones: 203 us there).  Lengths are on the device, so a call whose
 // max_tokens allows both launches both, and each kernel passes over the other's
 // sequences.

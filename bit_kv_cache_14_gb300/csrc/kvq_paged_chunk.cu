@@ -15,8 +15,9 @@
 // at 2^4 or more, so weights down to 2^-18 of it are normal fp16 numbers and
 // smaller ones keep an absolute 2^-29 of it (held at 1, weights of 2^-26.5 went to
 // zero, and with them the output of rows that thousands of those make up).  More
-// room costs moves: 4096 tokens over 32768 at 2 bits in 1502, 1549, 1585 and 1611
-// us at 0, 3, 4 and 5; at 4 bits 1410, 1419, 1425 and 1437.
+// room costs moves: 4096 tokens of 32768 at 2 bits in 1502, 1549, 1585 and 1611
+// us at 0, 3, 4 and 5; at 4 bits 1410, 1419, 1425 and 1437 (before the queries came
+// asynchronously, which took 60 us off either).
 //
 // Bound: 4*128*256*d operations per step on the tensor core against 128*256
 // exponentials and the dequantization of 128 keys and values: eight producer
@@ -24,11 +25,11 @@
 // into fp16 (1024 + code by one LOP3, the code by one HFMA2, code * scale +
 // zero by a second: exact but for one rounding) and store the swizzled operand
 // tiles, which both query tiles use.  Measured on a GB300, 32 query and 8 KV heads
-// of 128, 4 bits: 4096 tokens over 32768, 1424 us = 1448 TFLOP/s, 76 % of the
-// measured matrix rate (1510 us back to back for seconds, at a lower clock; 1583
-// at 2 bits, 1644 at 8, 1253 with heads of 64); four times 512 over 8192, 224 us =
-// 1190 TFLOP/s; 64 tokens alone, 21 us.  Cross attention of 2 x 2048 rows over 16384
-// tokens: 762 us = 1443 TFLOP/s, 77 %.
+// of 128, 4 bits: the last 4096 tokens of 32768, 1357 us = 1520 TFLOP/s, 81 % of the
+// measured matrix rate (1471 us back to back for seconds, at a lower clock: 82 % of the
+// sustained rate; 1524 at 2 bits, 1665 at 8, 1239 with heads of 64); the last 512 of 8192
+// four times, 226 us = 1180 TFLOP/s; 64 tokens alone, 20 us.  Cross attention of 2 x 2048
+// rows over 16384 tokens: 762 us = 1443 TFLOP/s, 77 %.
 //
 // What made the difference: no role may spill (a spilled MMA thread needed 200
 // clocks an instruction instead of 64), role code has to be small or rolled (five

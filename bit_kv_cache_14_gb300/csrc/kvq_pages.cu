@@ -11,7 +11,7 @@
 // Measured on a GB300 (graph replay): drop and reserve of 16 sequences 6.8 us, of 2048
 // over a pool of 431000 pages 10.3 (25 when one warp walked 32 neighbouring words of the
 // map); select, reserve and the copy of 60 forks' pages 14.3; recount, compact and the
-// copy of 278 MB in a pool of 14000 pages 100, 82 of them the copy.
+// copy of 278 MB in a pool of 14000 pages 101, 83 of them the copy.
 #include <algorithm>
 
 #include "kvq_paged.cuh"
@@ -444,7 +444,9 @@ pages_map_kernel(const __grid_constant__ Table t) {
 // ---- compact ---------------------------------------------------------------------
 // n live pages go to [0, n): the k-th live page from n on moves to the k-th free page
 // before n.  Each block counts the free pages before its words by itself (the map is
-// a bit a page), so blocks wait for nothing.
+// a bit a page), so blocks wait for nothing.  That is work with the square of the pool:
+// both launches take 20 us for 2^20 pages, 107 for 2^22, 1190 for 2^24 and by that some
+// 20 ms for the 2^26 that a table may have.
 __global__ void __launch_bounds__(kMoveThreads)
 pages_moves_kernel(const __grid_constant__ Table t, int2 *copies, int64_t n_copies) {
   __shared__ int64_t sums[kMoveThreads / 32];

@@ -7,21 +7,23 @@
 // largest p_i / e_i, with the caller's exponential e (the smallest of exponentials
 // of rates p_i is at i with probability p_i).
 //
-// Two launches.  Rows: a warp reads 4 KB of a row and leaves its maximum m and s = sum
-// 2^((x - m) c), c = log2(e) / T, so each logit is read once; all rows are taken, since
-// which draft is the first refused is known only afterwards.  Draw: the blocks of a
-// sequence each join its rows' parts (a KB a row), decide, and race their share of the
-// one row that is drawn from; shares are joined by a maximum over (score, lowest
-// index), which has no order.  The draw's blocks come in as the rows' leave, look up
-// their drafts' logits and call their noise into L2 before they wait for the parts.
+// Two launches.  Rows: a warp reads up to four pieces of 4 KB of a row (one where there
+// are few) and leaves their maximum m and s = sum 2^((x - m) c), c = log2(e) / T, so each
+// logit is read once; all rows are taken, since which draft is the first refused is known
+// only afterwards.  Draw: the blocks of a sequence each join its rows' parts (16 bytes
+// each: 256 bytes of a bf16 row of 131072 in parts of four pieces), decide, and race their
+// share of the one row that is drawn from; shares are joined by a maximum over (score,
+// lowest index), which has no order.  The draw's blocks come in as the rows' leave, look
+// up their drafts' logits and call their noise into L2 before they wait for the parts.
 //
-// What bounds them is HBM, 4.4 to 5.2 TB/s of it.  Measured on a GB300 (graph replay):
-// 64 sequences of 4 drafts, bf16 logits of 131072 tokens and a draft model's, 185 MB:
-// 43.2 us = 4.3 TB/s, 63 % of the copy rate (rows 5.1 TB/s; the draw reads 61 MB in 15 us,
-// 6 to 11 of them the race, the rest its chain of loads and the join); 128 x 3 greedy,
-// fp32, 65537 tokens: 26.9 us = 5.0 TB/s, 73 %; 24 sequences, 50001 tokens, no draft model:
-// 12.9 us; one sequence, 32000 tokens: 8.5 us, latency.  With one block a part, factors
-// in 64 bits (which this GPU divides slowly) and single loads the first took 173 us.
+// Large calls are bound by HBM, the draw also by its chain of loads.  Measured on a GB300
+// (graph replay): 64 sequences of 4 drafts, bf16 logits of 131072 tokens and a draft
+// model's, 185 MB: 43.7 us = 4.2 TB/s, 62 % of the copy rate (the draw reads 61 MB in 15
+// us, 6 to 11 of them the race, the rest its chain and the join); 128 x 3 greedy, fp32,
+// 65537 tokens: 26.9 us = 5.0 TB/s, 73 %.  Small ones by latency: 24 sequences, 50001
+// tokens, no draft model: 13.2 us; one sequence, 32000 tokens: 8.6.  With one block a
+// part, factors in 64 bits (which this GPU divides slowly) and single loads the first
+// took 173 us.
 #include <algorithm>
 
 #include "kvq_paged.cuh"

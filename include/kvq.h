@@ -547,8 +547,9 @@ int kvq_paged_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cach
  * all seq_lens[b] tokens (an encoder's states, written once), whatever the number
  * of its rows, which may be larger: the rows are no tokens of the sequence.  Rows
  * that read the same states (beams, samples) go in as rows of one sequence and
- * share its reads.  Arguments, arithmetic, results and errors are otherwise those
- * of kvq_paged_attention; a sequence without tokens gives its rows zeros.
+ * share its reads.  Arguments, arithmetic (fp16 operands, with their errors), results
+ * and errors are otherwise those of kvq_paged_attention; a sequence without tokens
+ * gives its rows zeros, one longer than its table ends with that (KVQ_EPAGE).
  */
 int kvq_paged_cross_attention(const kvq_paged_config *cfg, const kvq_paged_cache *cache,
                               const kvq_paged_batch *batch, const void *q, int64_t q_stride,
