@@ -725,8 +725,8 @@ int kvq_verify_drafts(const kvq_draft_batch *batch, const void *logits, int64_t 
                       int32_t *out_tokens, int32_t *accepted, int32_t *dropped, float *logprobs,
                       void *ws, size_t ws_bytes, void *stream) {
   return verify_drafts(false, batch, logits, stride, draft_logits, draft_stride, temperature,
-                       uniform, noise, noise_stride, out_tokens, accepted, dropped, logprobs, ws, ws_bytes,
-                       stream);
+                       uniform, noise, noise_stride, out_tokens, accepted, dropped, logprobs, ws,
+                       ws_bytes, stream);
 }
 
 int kvq_verify_drafts_padded(const kvq_draft_batch *batch, const void *logits, int64_t stride,
@@ -736,8 +736,8 @@ int kvq_verify_drafts_padded(const kvq_draft_batch *batch, const void *logits, i
                              int32_t *dropped, float *logprobs, void *ws, size_t ws_bytes,
                              void *stream) {
   return verify_drafts(true, batch, logits, stride, draft_logits, draft_stride, temperature,
-                       uniform, noise, noise_stride, out_tokens, accepted, dropped, logprobs, ws, ws_bytes,
-                       stream);
+                       uniform, noise, noise_stride, out_tokens, accepted, dropped, logprobs, ws,
+                       ws_bytes, stream);
 }
 
 }  // extern "C"

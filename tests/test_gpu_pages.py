@@ -305,6 +305,29 @@ def test_compacting_with_a_free_count_that_is_none(count):
     reserve(m, tab, [5, 5, 5])
 
 
+@pytest.mark.parametrize("bad", (-1, 16 * 3000 + 1))
+def test_long_rows_without_a_length(bad):
+    """The same where several warps share a row: all of them leave it alone, and what
+    they count among themselves stays at zero for the next call."""
+    m, tab = both(9000, 16, 3, 3000)
+    reserve(m, tab, [47990, 20000, 33333])
+    tab.seq_lens[1] = bad
+    for _ in range(2):
+        tab.drop(i32([20001, 20001, 17]))
+        m.drop([20001, 0, 17])
+        tab.select(i32([2, 0, 1]))
+        m.select([2, 1, 2])
+        assert tab.device_status() == (kvq.KVQ_EINVAL if bad < 0 else kvq.KVQ_EPAGE)
+        true, m.lens[1] = m.lens[1], bad
+        m.check(tab)
+        m.lens[1] = true
+    tab.seq_lens[1] = m.lens[1]
+    m.drop([5, 19000, 33333])
+    tab.drop(i32([5, 19000, 33333]))
+    m.check(tab)
+    assert tab.device_status() == 0
+
+
 def test_tables_taken_over():
     """Given tables with garbage behind each sequence's last entry."""
     m, _ = both(60, 32, 4, 6)
@@ -364,6 +387,31 @@ def test_copied_pages(d, bits, page, hkv, n):
     want[to.long()] = before[src.long()]
     assert torch.equal(cache.pages.view(n_pages, -1), want)
     assert cache.device_status() == 0
+
+
+def test_lists_that_begin_anywhere_in_a_buffer():
+    """A list is 8-byte aligned: parts of a longer one, copied on two streams."""
+    n = 700
+    pools = [kvq.PagedKVCache(kvq.make_paged_config(2, 2, 64, 4, 16, 2 * n)) for _ in range(2)]
+    buf = torch.empty(2 * n + 9, 2, dtype=torch.int32, device="cuda")
+    want = []
+    for i, pool in enumerate(pools):
+        gen = torch.Generator("cuda").manual_seed(i)
+        pool.pages.random_(0, 256, generator=gen)
+        ids = torch.randperm(2 * n, generator=gen, device="cuda").to(torch.int32)
+        part = buf[1 + i * (n + 4):][:n]
+        part[:, 0], part[:, 1] = ids[:n], ids[n:]
+        part[n - 50 - i] = -1
+        w = pool.pages.clone().view(2 * n, -1)
+        w[ids[n:2 * n - 50 - i].long()] = w[ids[:n - 50 - i].long()]
+        want.append(w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in pools]
+    for i, pool in enumerate(pools):
+        pool.copy_pages(buf[1 + i * (n + 4):][:n], stream=streams[i])
+    torch.cuda.synchronize()
+    for pool, w in zip(pools, want):
+        assert torch.equal(pool.pages.view(2 * n, -1), w) and pool.device_status() == 0
 
 
 def test_copies_of_pages_that_are_not_there():
